@@ -348,7 +348,8 @@ CONVROT_API convrot_status convrot_linear_noalloc(const void* X, int64_t M, int6
 /*
  * convrot_read_device_status -- copy the status word of a workspace used by
  * convrot_linear / convrot_gemm_* back to the host and return it
- * (CONVROT_OK, or CONVROT_ERR_DEVICE_TIMEOUT if a bounded wait ran out).
+ * (CONVROT_OK, or CONVROT_ERR_DEVICE_TIMEOUT if a bounded wait ran out; for
+ * convrot_cache_attention also CONVROT_ERR_INVALID_ARG, see there).
  * SYNCHRONISES `stream`. The word is reset at the start of every call that
  * uses the workspace (except a call with M = 0, which enqueues nothing).
  */
@@ -380,6 +381,131 @@ CONVROT_API size_t convrot_attention_workspace_bytes(int64_t BH, int64_t Sq, int
 CONVROT_API convrot_status convrot_attention_int8(const void* Q, const void* K, const void* V, int64_t BH,
                                                   int64_t Sq, int64_t Skv, int64_t D, float softmax_scale,
                                                   void* O, void* ws, size_t ws_bytes, convrot_stream_t stream);
+
+/*
+ * Rotary positions with several axes (time, height, width, ...): from the rows
+ * of a fused projection to the head vectors the attention reads. Pair i of the
+ * R/2 pairs of a head vector turns by angle = positions[axis[i]] * freq[i]:
+ *   (y1, y2) = (x1 cos - x2 sin, x2 cos + x1 sin)
+ * with channels (i, i + R/2) as the pair, or (2i, 2i + 1) with `interleaved`;
+ * channels R .. D-1 are copied. `inverse` turns by -angle: the inverse and the
+ * transpose of the rotation, hence also its gradient (X then holds dL/dY and Y
+ * receives dL/dX). The pages describe no positions; the models they measure
+ * turn Q and K this way before their attention.
+ *   X, Y      in `dtype`; element (b, s, h, d) at b*x_batch + s*x_token +
+ *             h*x_head + d (strides in elements, any sign). Y may be X itself
+ *             (same pointer and strides); otherwise they must not overlap, and
+ *             no two elements of Y may share an address.
+ *   B, S, H   B and S may be 0 (nothing is launched); B * S < 2^31, H <= 65535.
+ *   D, R      1 <= D <= 512; 0 <= R <= D, R even. D and R multiples of 16, strides
+ *             multiples of 8 and 16-byte aligned pointers take 16-byte accesses;
+ *             anything else a slower kernel.
+ *   positions [axes, B, S] int32 or float32 (pos_dtype) with strides pos_axis,
+ *             pos_batch (0: shared by the batch) and pos_token in elements.
+ *   freq      [R/2] double, device: radians per unit of position. The angle is
+ *             formed and reduced in double.
+ *   axis      [R/2] int32, device: the axis of each pair; a pair whose axis is
+ *             outside [0, axes) is not turned.
+ * One kernel launch.
+ */
+typedef enum { CONVROT_POS_I32 = 0, CONVROT_POS_F32 = 1 } convrot_pos_dtype;
+CONVROT_API convrot_status convrot_rope(const void* X, int dtype, int64_t B, int64_t S, int64_t H, int64_t D,
+                                        int64_t R, int64_t x_batch, int64_t x_token, int64_t x_head,
+                                        const void* positions, int pos_dtype, int64_t axes, int64_t pos_axis,
+                                        int64_t pos_batch, int64_t pos_token, const double* freq,
+                                        const int32_t* axis, int interleaved, int inverse, void* Y,
+                                        int64_t y_batch, int64_t y_token, int64_t y_head, convrot_stream_t stream);
+
+/*
+ * The rotated int8 key/value cache. A cell holds one token of one key/value
+ * head: 128 int8 codes and one float32 scale for the key, and the same for the
+ * value, each by the layer's per-token rule over the head vector (rotated by
+ * H_128/sqrt(128), s = absmax/127, codes rne(x R / s); the bits of
+ * convrot_quant_act with g = 128). Cells lie in pages of page_size tokens:
+ *   k_codes, v_codes [num_pages, H, page_size, 128] int8, 16-byte aligned;
+ *   k_scale, v_scale [num_pages, H, page_size] float, 16-byte aligned.
+ * page_size is a power of two in [CONVROT_MIN_PAGE, CONVROT_MAX_PAGE],
+ * H <= CONVROT_MAX_CACHE_HEADS, num_pages * page_size < 2^31. The cache needs
+ * no initialisation: a cell that was never written is never used unless a
+ * length or a slot names it.
+ *
+ * convrot_cache_append writes the T tokens of K and V to the cells of their
+ * slots, slot = page * page_size + place in the page. The slots of one call
+ * must differ, except that any number may be negative: those tokens are skipped.
+ *   K, V      [T, H, 128] in `dtype`, 16-byte aligned; element (t, h, d) at
+ *             t*k_token + h*k_head + d (v_token, v_head), strides multiples of 8.
+ *   slots     [T] int32, device.
+ *   status    one int, device, or NULL: a slot at or past num_pages * page_size
+ *             skips its token and ORs CONVROT_ERR_INVALID_ARG in. Never cleared.
+ * convrot_cache_read is the way back, K = (codes * scale) R, rounded once to
+ * `dtype`; a token whose slot is negative (or past the end, with the status
+ * as above) reads as zeros. Here slots may repeat.
+ * D must be 128 (else CONVROT_ERR_UNSUPPORTED). T = 0 launches nothing, else one
+ * kernel. A read or an attention on another stream must be ordered after the
+ * append by the caller.
+ */
+#define CONVROT_MIN_PAGE 16
+#define CONVROT_MAX_PAGE 1024
+#define CONVROT_MAX_CACHE_HEADS 1024
+CONVROT_API convrot_status convrot_cache_append(const void* K, const void* V, int dtype, int64_t T, int64_t H,
+                                                int64_t D, int64_t k_token, int64_t k_head, int64_t v_token,
+                                                int64_t v_head, const int32_t* slots, int8_t* k_codes,
+                                                int8_t* v_codes, float* k_scale, float* v_scale, int64_t num_pages,
+                                                int64_t page_size, int* status, convrot_stream_t stream);
+CONVROT_API convrot_status convrot_cache_read(const int32_t* slots, int64_t T, int64_t H, int64_t D,
+                                              const int8_t* k_codes, const int8_t* v_codes, const float* k_scale,
+                                              const float* v_scale, int64_t num_pages, int64_t page_size, void* K,
+                                              void* V, int dtype, int64_t k_token, int64_t k_head, int64_t v_token,
+                                              int64_t v_head, int* status, convrot_stream_t stream);
+
+/*
+ * convrot_cache_attention -- attention of the newest tokens of B sequences over
+ * the cache, their own keys and values included (append them first):
+ *   O = (softmax(S) V) R with S, V from the cells as convrot_attention_int8 takes
+ *   them from dense heads: the query head vector rotated and quantised to int8
+ *   per head, exact integer products, float32 softmax; the weights p s_v are
+ *   rounded to fp16 and P V accumulates in float32.
+ * Sequence b has lengths[b] keys in the cells that row b of the page table
+ * names (key j in page pages[b, j / page_size], place j % page_size), and the
+ * query tokens starts[b] .. starts[b+1]-1 of Q, n of them, which are its last n
+ * keys. Query token i sees every key before those n, and of the n
+ *   - without `tree`: keys 0 .. i (causal);
+ *   - with `tree`: key m where bit m of tree[starts[b] + i] is set: a tree of
+ *     drafted tokens, each token's mask holding itself and its ancestors.
+ *     At most 64 tokens per sequence: later keys of the n are not seen, and the
+ *     status word becomes CONVROT_ERR_INVALID_ARG.
+ * A query that sees no key (an idle place with length 0, an empty mask) gives
+ * zeros. Rows of O outside every [starts[b], starts[b+1]) are left as they were.
+ *   Q, O      [T, Hq, 128] in `dtype`, 16-byte aligned; element (t, h, d) at
+ *             t*q_token + h*q_head + d (o_token, o_head), strides multiples of 8.
+ *             O must not overlap Q. Query head h reads key head h / (Hq / H).
+ *             T <= 2^20.
+ *   cache     as above, with Hkv heads; num_pages * page_size * Hkv < 2^31.
+ *   pages     [B, table_pages] int32, device, rows table_stride >= 0 elements
+ *             apart; entries past a sequence's last page are never read. B <= 2^24.
+ *   lengths   [B] int32, device.
+ *   starts    [B+1] int32, device, rising from >= 0 to <= T; or NULL with T = B:
+ *             one token per sequence.
+ *   tree      [T] 64-bit masks, device, or NULL.
+ *   ws        >= convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes,
+ *             256-byte aligned, no initialisation; its first word is the status
+ *             word (convrot_read_device_status), written by every call with T > 0:
+ *             CONVROT_ERR_INVALID_ARG if a length was outside [0, table_pages *
+ *             page_size] (the nearest bound is used), a page outside
+ *             [0, num_pages) (its keys are not seen), or the starts did not rise
+ *             within [0, T] (they are clamped).
+ * Keys are read once per 16, 32 or 64 query rows (n * Hq / Hkv rows per key
+ * head), so this is the form for single tokens, drafts and short chunks; long
+ * prompts belong to convrot_attention_int8. Two kernels; how the work is cut
+ * follows from the lengths, and the result does not depend on timing.
+ */
+CONVROT_API size_t convrot_cache_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+CONVROT_API convrot_status convrot_cache_attention(
+    const void* Q, int dtype, int64_t T, int64_t Hq, int64_t D, int64_t q_token, int64_t q_head,
+    const int8_t* k_codes, const int8_t* v_codes, const float* k_scale, const float* v_scale, int64_t num_pages,
+    int64_t page_size, int64_t Hkv, const int32_t* pages, int64_t B, int64_t table_pages, int64_t table_stride,
+    const int32_t* lengths, const int32_t* starts, const int64_t* tree, float softmax_scale, void* O,
+    int64_t o_token, int64_t o_head, void* ws, size_t ws_bytes, convrot_stream_t stream);
 
 /*
  * convrot_probe_i8_peak -- measurement aid for the GEMM's roofline (not part

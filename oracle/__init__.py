@@ -11,6 +11,13 @@ from .attention_oracle import (  # noqa: F401
     quantize_heads,
     softmax,
 )
+from .cache_oracle import (  # noqa: F401
+    cache_attention,
+    cache_value,
+    cache_write,
+    rope,
+    seen,
+)
 from .convrot_oracle import (  # noqa: F401
     QMAX,
     bf16_to_f64,

@@ -1,0 +1,142 @@
+"""What the rope and cache entry points refuse, on the host (no GPU: nothing is launched)."""
+
+from __future__ import annotations
+
+import pytest
+
+FAKE = 0x10000  # aligned and never dereferenced: every call fails validation or has nothing to do
+
+
+@pytest.fixture(scope="module")
+def L():
+    from w8a8_rotated_int8_token_b200 import _lib, build
+
+    build.build()
+    return _lib.load()
+
+
+def _caller(fn, names, values):
+    names = names.split()
+    assert len(names) == len(values) == len(fn.argtypes)
+
+    def call(**over):
+        assert set(over) <= set(names)
+        return fn(*[over.get(n, v) for n, v in zip(names, values)])
+
+    return call
+
+
+def test_rope(L):
+    call = _caller(L.convrot_rope, "X dtype B S H D R xb xs xh pos pos_dtype axes pa pb ps freq axis inter inverse Y yb ys "
+                   "yh stream",
+                   [FAKE, 0, 1, 4, 2, 128, 128, 0, 256, 128, FAKE, 0, 3, 4, 0, 1, FAKE, FAKE, 0, 0, FAKE, 0, 256, 128,
+                    None])
+    assert call(dtype=2) == 2 and call(pos_dtype=2) == 2
+    assert call(R=127) == 1 and call(R=130) == 1 and call(R=-2) == 1
+    assert call(H=0) == 1 and call(D=0, R=0) == 1 and call(B=-1) == 1 and call(S=-1) == 1 and call(axes=0) == 1
+    assert call(D=514) == 2 and call(H=65536) == 2 and call(B=1 << 20, S=1 << 12) == 2
+    for name in ("X", "Y", "pos", "freq", "axis"):
+        assert call(**{name: None}) == 1, name
+    assert call(X=FAKE + 1) == 1 and call(pos=FAKE + 2) == 1 and call(freq=FAKE + 4) == 1 and call(axis=FAKE + 2) == 1
+    assert call(S=0, X=None, Y=None, pos=None) == 0 and call(B=0) == 0
+    assert call(S=0, R=127) == 1
+
+
+CELLS = [FAKE, FAKE, FAKE, FAKE]
+
+
+def test_append_and_read(L):
+    append = _caller(L.convrot_cache_append, "K V dtype T H D kt kh vt vh slots kc vc ks vs pages page status stream",
+                     [FAKE, FAKE, 0, 4, 2, 128, 256, 128, 256, 128, FAKE, *CELLS, 8, 64, None, None])
+    read = _caller(L.convrot_cache_read, "slots T H D kc vc ks vs pages page K V dtype kt kh vt vh status stream",
+                   [FAKE, 4, 2, 128, *CELLS, 8, 64, FAKE, FAKE, 0, 256, 128, 256, 128, None, None])
+    for call in (append, read):
+        assert call(dtype=3) == 2 and call(D=64) == 2
+        assert call(page=8) == 2 and call(page=48) == 2 and call(page=2048) == 2 and call(page=0) == 1
+        assert call(pages=0) == 1 and call(H=0) == 1 and call(T=-1) == 1
+        assert call(H=1025) == 2 and call(pages=1 << 25) == 2 and call(T=1 << 30) == 2
+        assert call(kt=4) == 1 and call(vh=12) == 1
+        for name in ("K", "V", "slots", "kc", "vc", "ks", "vs"):
+            assert call(**{name: None}) == 1, name
+        assert call(K=FAKE + 8) == 1 and call(slots=FAKE + 2) == 1 and call(kc=FAKE + 8) == 1 and call(vs=FAKE + 8) == 1
+        assert call(status=FAKE + 2) == 1
+        assert call(T=0, K=None, V=None, slots=None) == 0 and call(T=0, D=64) == 2
+
+
+def test_attention(L):
+    call = _caller(L.convrot_cache_attention,
+                   "Q dtype T Hq D qt qh kc vc ks vs pages page Hkv table B cols stride lengths starts tree scale O ot oh "
+                   "ws ws_bytes stream",
+                   [FAKE, 0, 4, 8, 128, 1024, 128, *CELLS, 8, 64, 2, FAKE, 4, 3, 3, FAKE, None, None, 0.1, FAKE, 1024,
+                    128, FAKE, 1 << 30, None])
+    assert call(dtype=2) == 2 and call(D=64) == 2
+    assert call(Hq=7) == 1 and call(Hkv=0) == 1 and call(Hq=0) == 1 and call(pages=0) == 1 and call(cols=-1) == 1
+    assert call(stride=-1) == 1 and call(page=24) == 2 and call(page=4096) == 2 and call(page=0) == 1
+    assert call(T=5) == 1  # one token per sequence without starts
+    assert call(T=5, starts=FAKE, B=(1 << 24) + 1) == 2 and call(T=(1 << 20) + 1, starts=FAKE) == 2
+    assert call(pages=1 << 24) == 2 and call(cols=1 << 28) == 2 and call(Hq=2 * 1025) == 2
+    assert call(scale=0.0) == 1 and call(scale=-1.0) == 1 and call(scale=float("inf")) == 1
+    assert call(scale=float("nan")) == 1
+    assert call(qt=1020) == 1 and call(oh=4) == 1
+    for name in ("Q", "O", "kc", "vc", "ks", "vs", "lengths", "table"):
+        assert call(**{name: None}) == 1, name
+    assert call(Q=FAKE + 8) == 1 and call(lengths=FAKE + 2) == 1 and call(starts=FAKE + 1) == 1
+    assert call(tree=FAKE + 4) == 1
+    assert call(ws=None) == 3 and call(ws=FAKE + 16) == 3 and call(ws_bytes=4096) == 3
+    assert call(T=0, B=0, Q=None, O=None, ws=None) == 0 and call(T=0, starts=FAKE, Q=None, O=None, ws=None) == 0
+    assert call(T=0, B=0, Hq=7) == 1
+
+
+def test_attention_workspace(L):
+    size = L.convrot_cache_attention_workspace_bytes
+    assert size(0, 0, 8, 2, 128) == 256
+    assert size(4, 4, 8, 2, 64) == 0 and size(4, 4, 7, 2, 128) == 0 and size(-1, 4, 8, 2, 128) == 0
+    # a row of sums per piece's two ends: 480 pieces, tiles of 16 or 32 rows
+    assert size(4, 4, 8, 2, 128) >= 2 * 480 * 16 * 128 * 4
+    assert size(64, 4, 8, 2, 128) >= 2 * 480 * 32 * 128 * 4
+
+
+def test_binding_refuses_before_the_library():
+    import torch
+
+    import w8a8_rotated_int8_token_b200 as cr
+
+    x = torch.zeros(4, 2, 128, dtype=torch.bfloat16)
+    i = torch.zeros(4, dtype=torch.int32)
+    cells = (torch.zeros(2, 2, 16, 128, dtype=torch.int8),) * 2 + (torch.zeros(2, 2, 16),) * 2
+    for call in (lambda: cr.convrot_rope(x, i[None], *cr.convrot_rope_tables([64], device="cpu")),
+                 lambda: cr.convrot_cache_append(x, x, i, *cells),
+                 lambda: cr.convrot_cache_read(i, *cells),
+                 lambda: cr.convrot_cache_attention(x, *cells, i[:, None], i)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(TypeError):
+        cr.convrot_rope(x.float(), i[None], None, None)
+    with pytest.raises(ValueError):
+        cr.convrot_rope_tables([4, -1], device="cpu")
+
+
+def test_rope_tables():
+    import numpy as np
+    import torch
+
+    import w8a8_rotated_int8_token_b200 as cr
+
+    freq, axis = cr.convrot_rope_tables([1, 2, 0, 1], theta=100.0, device="cpu")
+    assert axis.dtype == torch.int32 and axis.tolist() == [0, 1, 1, 3]
+    np.testing.assert_allclose(freq.numpy(), [1.0, 1.0, 0.1, 1.0], rtol=1e-15)
+    freq, _ = cr.convrot_rope_tables([1, 2, 0, 1], theta=16.0, shared=True, device="cpu")
+    np.testing.assert_allclose(freq.numpy(), [1.0, 0.5, 0.25, 0.125], rtol=1e-15)
+
+
+def test_cache_slots():
+    import torch
+
+    import w8a8_rotated_int8_token_b200 as cr
+
+    cache = cr.ConvRotCache(4, 1, 16, device="cpu")
+    pages = torch.tensor([[3, 1], [2, -1]], dtype=torch.int32)
+    seq = torch.tensor([0, 0, 1, 1, 0, 2, -1, 0])
+    pos = torch.tensor([0, 17, 15, 16, 32, 0, 0, -1])
+    assert cache.slots(pages, seq, pos).tolist() == [48, 17, 47, -1, -1, -1, -1, -1]
+    assert cache.slots(pages[:, :0], seq, pos).tolist() == [-1] * 8

@@ -1,0 +1,484 @@
+"""convrot_cache_attention against the oracle on the same cells, on a B200.
+
+Tolerance of an output row, in the 2-norm, which the final rotation keeps. Before
+the rotation a channel is sum_k w_k s_k c_k with weights w of the softmax. Its
+error is at most
+    A eps + 2^-24 max_k(w_k s_k) sum_k |c_k|,   A = sum_k w_k s_k |c_k|,
+    eps = 2^-11 (weight to fp16) + 2 e (exponent, above and below the line)
+          + (L/16 + 64) 2^-22 (float32 sums: a term per 16 keys in the matrix
+          instruction, the joins),
+    e = ln 2 * 6 * 2^-24 max|t| (logits in base 2, six roundings) + 2^-22 (exp2) + f,
+the second term for weights below fp16's normal range (2^-25 of the largest, the
+largest kept above 1). f covers query codes that round the other way: where the
+oracle's quotient lies within 1e-3 of a tie, a step of that code moves logit k by
+s_q s_k |c_k| softmax_scale. The output's half step comes on top, and 8 float32
+roundings of the rotation.
+"""
+
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+from parity import OUT_ABS, OUT_REL
+
+pytestmark = pytest.mark.gpu
+
+SCALE = 1.0 / math.sqrt(128)
+
+
+@pytest.fixture(scope="module")
+def cr():
+    import torch
+
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import w8a8_rotated_int8_token_b200 as cr
+
+    cr.lib()
+    return cr
+
+
+class Setup:
+    """Sequences with (keys, new tokens) each over a cache whose unused cells hold NaN scales and any codes."""
+
+    def __init__(self, cr, seqs, hq, hkv, page, kind="bf16", seed=0, tree=None, spare=3):
+        import torch
+
+        self.cr, self.seqs, self.hq, self.hkv, self.page, self.kind = cr, seqs, hq, hkv, page, kind
+        rng = np.random.default_rng(seed)
+        need = [-(-k // page) for k, _ in seqs]
+        order = rng.permutation(sum(need) + spare)
+        self.pages = np.full((len(seqs), max(need + [0]) + 1), -7, np.int32)
+        at = 0
+        for b, n in enumerate(need):
+            self.pages[b, :n] = order[at:at + n]
+            at += n
+        shape = (len(order), hkv, page)
+        self.codes = [rng.integers(-127, 128, (*shape, 128)).astype(np.int8) for _ in range(2)]
+        self.scales = [np.full(shape, np.nan, np.float32) for _ in range(2)]
+        for b, (keys, _) in enumerate(seqs):
+            for s in self.scales:
+                for j in range(0, keys, page):
+                    n = min(page, keys - j)
+                    s[self.pages[b, j // page], :, :n] = rng.uniform(0.005, 0.03, (hkv, n))
+        self.starts = np.concatenate([[0], np.cumsum([n for _, n in seqs])]).astype(np.int32)
+        self.tree = tree
+        self.T = int(self.starts[-1])
+        self.dtype = torch.bfloat16 if kind == "bf16" else torch.float16
+        q = torch.from_numpy(rng.standard_normal((self.T, hq, 128)) * 3.0).to(self.dtype)
+        self.q = q.double().numpy()
+        self.Q = q.cuda()
+
+    def cells(self):
+        import torch
+
+        return [torch.from_numpy(x).cuda() for x in (*self.codes, *self.scales)]
+
+    def args(self, starts=True):
+        import torch
+
+        a = [torch.from_numpy(self.pages).cuda(),
+             torch.tensor([k for k, _ in self.seqs], dtype=torch.int32, device="cuda"),
+             torch.from_numpy(self.starts).cuda() if starts else None]
+        if self.tree is not None:
+            a.append(torch.from_numpy(np.asarray(self.tree, np.uint64).view(np.int64)).cuda())
+        return a
+
+    def run(self, starts=True, status=0, **more):
+        import torch
+
+        need = self.cr.convrot_cache_attention_workspace_bytes(self.T, len(self.seqs), self.hq, self.hkv)
+        ws = torch.full((max(need, 256),), 255, dtype=torch.uint8, device="cuda")
+        O = self.cr.convrot_cache_attention(self.Q, *self.cells(), *self.args(starts), ws=ws, **more)
+        assert self.cr.convrot_read_device_status(ws) == status
+        return O
+
+    def dense(self, b, which, keep=None):
+        """(codes [Hkv, keys, 128], scales [Hkv, keys]) of sequence b."""
+        keys = self.seqs[b][0]
+        at = self.pages[b, np.arange(keys) // self.page]
+        off = np.arange(keys) % self.page
+        return self.codes[which][at, :, off].transpose(1, 0, 2), self.scales[which][at, :, off].T
+
+    def check(self, O, scale=SCALE, see=None, sequences=None):
+        """Every row of O against the oracle; `see` replaces the visibility of sequences."""
+        o = O.double().cpu().numpy()
+        assert np.all(np.isfinite(o))
+        group = self.hq // self.hkv
+        for b in range(len(self.seqs)) if sequences is None else sequences:
+            keys, news = self.seqs[b]
+            rows = slice(self.starts[b], self.starts[b + 1])
+            tree = None if self.tree is None else self.tree[rows]
+            on = oracle.seen(keys, news, tree) if see is None else see[b]
+            (kc, ks), (vc, vs) = self.dense(b, 0), self.dense(b, 1)
+            some = on.any(0)  # cells nothing sees may hold anything
+            ks, vs = np.where(some, ks, 1.0), np.where(some, vs, 0.0)
+            ref, w, qc, sq = oracle.cache_attention(self.q[rows], kc, ks, vc, vs, on, scale)
+            turned = oracle.rotate(self.q[rows], 128)
+            quot = turned / np.where(sq > 0, sq, 1.0)[..., None].astype(np.float64)
+            tie = np.abs(np.abs(quot - np.floor(quot)) - 0.5) < 1e-3
+            for h in range(self.hq):
+                c, s = np.abs(vc[h // group].astype(np.float64)), vs[h // group].astype(np.float64)
+                kk = np.abs(kc[h // group].astype(np.float64)) * ks[h // group].astype(np.float64)[:, None]
+                logits = np.abs(qc[:, h].astype(np.float64) @ (kc[h // group] * ks[h // group][:, None]).T) \
+                    * sq[:, h, None] * scale if keys else np.zeros((news, 0))
+                for i in range(news):
+                    got, want = o[self.starts[b] + i, h], ref[i, h]
+                    if not on[i].any():
+                        assert not got.any()
+                        continue
+                    ws = w[i, h] * s
+                    e = math.log(2) * 6 * 2.0**-24 * (logits[i].max() * math.log2(math.e)) + 2.0**-22
+                    if tie[i, h].any():
+                        f = float((kk[on[i]] * tie[i, h]).sum(1).max()) * float(sq[i, h]) * scale
+                        e += f * math.exp(f)
+                    eps = 2.0**-11 + 2 * e + (keys / 16 + 64) * 2.0**-22
+                    off = eps * (ws @ c) + 2.0**-24 * ws.max() * c[on[i]].sum(0)
+                    u = OUT_REL[self.kind]
+                    slack = np.linalg.norm(off) * (1 + u) + 8 * 2.0**-24 * np.linalg.norm(ws @ c)
+                    bound = u * np.linalg.norm(want) + slack + OUT_ABS[self.kind] * math.sqrt(128)
+                    assert np.linalg.norm(got - want) <= bound, (b, i, h, np.linalg.norm(got - want) / bound)
+                    assert np.all(np.abs(got - want) <= u * np.abs(want) + slack + OUT_ABS[self.kind]), (b, i, h)
+        return o
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("lengths,hq,hkv,page", [
+    ([1], 1, 1, 16), ([16], 4, 1, 16), ([17], 8, 2, 16), ([64], 5, 5, 32), ([65], 3, 1, 32), ([1000], 8, 2, 64),
+    ([5, 0, 130, 63], 6, 2, 16), ([300, 1, 64, 200, 128], 16, 1, 128), ([90, 257], 20, 1, 256), ([700], 64, 2, 1024),
+    ([0, 0], 4, 4, 16), ([31] * 9, 2, 2, 16)])
+def test_single_tokens(cr, kind, lengths, hq, hkv, page):
+    s = Setup(cr, [(n, 1) for n in lengths], hq, hkv, page, kind, seed=sum(lengths) + hq)
+    O = s.run(starts=False)
+    s.check(O)
+    import torch
+
+    assert torch.equal(s.run(), O)  # with starts, bit by bit the same
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("seqs,hq,hkv,page", [
+    ([(70, 70), (200, 3), (5, 5), (40, 0), (0, 0), (33, 1)], 4, 2, 32), ([(129, 17)], 7, 1, 16), ([(64, 64)], 1, 1, 64),
+    ([(3, 7), (0, 2), (500, 2)], 2, 1, 16), ([(400, 100)], 8, 8, 16), ([(1, 1), (66, 2)], 32, 2, 128)])
+def test_causal_chunks(cr, kind, seqs, hq, hkv, page):
+    s = Setup(cr, seqs, hq, hkv, page, kind, seed=len(seqs) + hq)
+    s.check(s.run())
+
+
+def _tree(rng, news):
+    """Masks of random trees; now and then a token that sees nothing of the draft, not even itself."""
+    out = []
+    for n in news:
+        masks = []
+        for i in range(n):
+            parent = int(rng.integers(-1, i)) if i else -1
+            masks.append((masks[parent] if parent >= 0 else 0) | 1 << i)
+        if n > 3:
+            masks[2] = 0
+        out += masks
+    return np.array(out, np.uint64)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("seqs,hq,hkv,page", [([(64, 64)], 4, 1, 16), ([(300, 12), (1, 1), (77, 33), (9, 9)], 8, 2, 32),
+                                              ([(2000, 64)], 2, 2, 64), ([(5, 9), (0, 4)], 3, 1, 16),
+                                              ([(90, 2), (40, 5), (130, 3)], 2, 1, 128)])
+def test_trees(cr, kind, seqs, hq, hkv, page):
+    rng = np.random.default_rng(hq)
+    s = Setup(cr, seqs, hq, hkv, page, kind, seed=hq, tree=_tree(rng, [n for _, n in seqs]))
+    s.check(s.run())
+
+
+def test_causal_equals_a_line_of_drafts(cr):
+    import torch
+
+    seqs = [(100, 20), (64, 64), (3, 3)]
+    line = np.array([(1 << (i + 1)) - 1 for _, n in seqs for i in range(n)], np.uint64)
+    a, b = Setup(cr, seqs, 4, 2, 16), Setup(cr, seqs, 4, 2, 16, tree=line)
+    assert torch.equal(a.run(), b.run())
+
+
+def test_drafts_past_the_64th_are_not_seen(cr):
+    full = np.full(70, 2**64 - 1, np.uint64)
+    s = Setup(cr, [(100, 70)], 2, 1, 16, tree=full)
+    see = np.ones((70, 100), bool)
+    see[:, 94:] = False  # 30 keys of context, then 64 drafts
+    s.check(s.run(status=1), see=[see])
+
+
+@pytest.mark.parametrize("hq,hkv,keys", [(4, 1, 20000), (40, 1, 9000), (16, 8, 6001)])
+def test_one_long_sequence_is_cut_among_all_ctas(cr, hq, hkv, keys):
+    s = Setup(cr, [(keys, 1)], hq, hkv, 64, "f16", seed=keys)
+    s.check(s.run(starts=False))
+
+
+def test_many_sequences(cr):
+    rng = np.random.default_rng(5)
+    seqs = [(int(n), 1) for n in rng.integers(0, 200, 400)]
+    s = Setup(cr, seqs, 4, 2, 16, seed=5)
+    O = s.run(starts=False)
+    s.check(O, sequences=range(0, 400, 7))
+
+
+def test_maximum_that_keeps_rising(cr):
+    s = Setup(cr, [(900, 2)], 4, 1, 64, "f16", seed=6)
+    for b, j in [(0, j) for j in range(900)]:
+        s.scales[0][s.pages[b, j // 64], :, j % 64] = 0.001 * 1.01 ** j
+    s.check(s.run())
+
+
+def test_value_scales_of_any_range(cr):
+    """Value scales over 24 powers of ten, in either order along the keys, and values that are all zero."""
+    for order in (1, -1):
+        s = Setup(cr, [(600, 1), (50, 1)], 4, 2, 16, "bf16", seed=7)
+        for j in range(600):
+            s.scales[1][s.pages[0, j // 16], :, j % 16] = 10.0 ** (order * (j - 300) / 25.0)
+        for j in range(50):
+            s.scales[1][s.pages[1, j // 16], :, j % 16] = 0.0
+        o = s.check(s.run(starts=False))
+        assert not o[1].any()
+
+
+def test_unseen_cells_may_hold_anything(cr):
+    """Infinities and NaN in drafted cells that no mask names, and in those behind the last key."""
+    seqs = [(40, 6)]
+    tree = np.array([1, 3, 1, 9, 17, 33], np.uint64)  # nothing sees draft 2
+    s = Setup(cr, seqs, 4, 2, 16, seed=8, tree=tree)
+    j = 40 - 6 + 2
+    s.scales[0][s.pages[0, j // 16], :, j % 16] = np.inf
+    s.scales[1][s.pages[0, j // 16], :, j % 16] = np.nan
+    s.check(s.run())
+
+
+def test_zero_keys_and_queries(cr):
+    s = Setup(cr, [(100, 1)], 2, 1, 16, seed=9)
+    s.Q.zero_()
+    s.q[:] = 0.0
+    s.check(s.run())  # equal weights
+    s = Setup(cr, [(100, 1)], 2, 1, 16, seed=9)
+    s.scales[0][np.isfinite(s.scales[0])] = 0.0
+    s.check(s.run())
+
+
+def test_softmax_scale(cr):
+    s = Setup(cr, [(200, 3)], 4, 2, 32, seed=10)
+    s.check(s.run(softmax_scale=0.5), scale=0.5)
+    s.check(s.run(softmax_scale=1e-6), scale=1e-6)
+
+
+def test_strided_queries_and_outputs_and_rows_left_alone(cr):
+    import torch
+
+    s = Setup(cr, [(100, 2), (30, 1)], 6, 2, 16, seed=11)
+    want = s.run()
+    rows = torch.full((5, 10, 128), 9.0, dtype=s.dtype, device="cuda")
+    rows[:3, :6] = s.Q
+    out = torch.full((7, 5, 128), 3.0, dtype=s.dtype, device="cuda")  # head-major, two tokens behind the last
+    cr.convrot_cache_attention(rows[:, :6], *s.cells(), *s.args(), O=out[:6].transpose(0, 1))
+    assert torch.equal(out[:6, :3].transpose(0, 1), want)
+    assert bool((out[:6, 3:] == 3.0).all()) and bool((out[6] == 3.0).all())
+
+
+def test_shared_table_row_and_wide_table(cr):
+    import torch
+
+    s = Setup(cr, [(50, 1)], 4, 2, 16, seed=12)
+    pages, lengths, _ = s.args()
+    two = torch.cat([s.Q, s.Q])
+    O = cr.convrot_cache_attention(two, *s.cells(), pages.expand(2, -1), lengths.repeat(2))
+    assert torch.equal(O[0], O[1]) and torch.equal(O[:1], s.run())
+
+
+def test_bad_pages_hide_their_keys(cr):
+    for page in (16, 64):
+        s = Setup(cr, [(200, 1), (40, 1)], 4, 2, page, seed=13)
+        see = [np.ones((1, 200), bool), np.ones((1, 40), bool)]
+        good = s.pages.copy()
+        for column, bad in ((0, -1), (2, len(s.codes[0]))):
+            s.pages[0, column] = bad
+            see[0][0, column * page:(column + 1) * page] = False
+        O = s.run(starts=False, status=1)
+        s.pages = good
+        s.check(O, see=see)
+
+
+def test_bad_lengths_and_starts_are_bounded(cr):
+    import torch
+
+    s = Setup(cr, [(32, 1), (20, 1), (16, 1)], 2, 1, 16, seed=14)
+    pages, lengths, starts = s.args()
+    pages[:, 2:] = 0  # a table of valid pages
+    ws = torch.empty(cr.convrot_cache_attention_workspace_bytes(3, 3, 2, 1), dtype=torch.uint8, device="cuda")
+    cells = [c.nan_to_num(0.5) if c.is_floating_point() else c for c in s.cells()]
+    want = cr.convrot_cache_attention(s.Q, *cells, pages, lengths, starts, ws=ws)
+    wrong = lengths.clone()
+    wrong[0] = -5
+    O = cr.convrot_cache_attention(s.Q, *cells, pages, wrong, starts, ws=ws)
+    assert cr.convrot_read_device_status(ws) == 1
+    assert not bool(O[0].any()) and torch.equal(O[1:], want[1:])
+    wrong[0] = 2**31 - 1
+    full = lengths.clone()
+    full[0] = pages.shape[1] * 16
+    O = cr.convrot_cache_attention(s.Q, *cells, pages, wrong, starts, ws=ws)
+    assert cr.convrot_read_device_status(ws) == 1
+    assert torch.equal(O, cr.convrot_cache_attention(s.Q, *cells, pages, full, starts, ws=ws))
+    assert cr.convrot_read_device_status(ws) == 0
+    for bad in ([0, 1, 2, 2**31 - 1], [-9, 1, 2, 3], [0, 5, 2, 3], [3, 2, 1, 0]):
+        cr.convrot_cache_attention(s.Q, *cells, pages, lengths, torch.tensor(bad, dtype=torch.int32, device="cuda"), ws=ws)
+        assert cr.convrot_read_device_status(ws) == 1
+    assert torch.equal(cr.convrot_cache_attention(s.Q, *cells, pages, lengths, starts, ws=ws), want)
+
+
+def test_no_table(cr):
+    import torch
+
+    s = Setup(cr, [(0, 1), (0, 1)], 2, 1, 16, seed=15)
+    _, lengths, _ = s.args()
+    O = cr.convrot_cache_attention(s.Q, *s.cells(), torch.empty(2, 0, dtype=torch.int32, device="cuda"), lengths)
+    assert not bool(O.any())
+
+
+def test_refusals(cr):
+    import torch
+
+    s = Setup(cr, [(40, 1), (20, 1)], 4, 2, 16, seed=16)
+    pages, lengths, starts = s.args()
+    cells = s.cells()
+
+    def call(Q=s.Q, pages=pages, lengths=lengths, **more):
+        return cr.convrot_cache_attention(Q, *cells, pages, lengths, **more)
+
+    for bad in (dict(Q=s.Q[:1]), dict(Q=s.Q[:, :3]), dict(Q=s.Q.float()), dict(pages=pages.long()),
+                dict(pages=pages[:1]), dict(pages=pages.cpu()), dict(lengths=lengths.long()), dict(lengths=lengths[:1]),
+                dict(starts=starts[:2]), dict(starts=starts.long()), dict(tree=torch.zeros(2, device="cuda")),
+                dict(tree=torch.zeros(3, dtype=torch.int64, device="cuda")), dict(O=s.Q[:, :1].expand(2, 4, 128)),
+                dict(O=s.Q.float()), dict(pages=pages.t().contiguous().t())):
+        with pytest.raises((ValueError, TypeError)):
+            call(**bad)
+    for bad, status in ((dict(softmax_scale=0.0), 1), (dict(ws=torch.empty(256, dtype=torch.uint8, device="cuda")), 3)):
+        with pytest.raises(cr.ConvRotError) as e:
+            call(**bad)
+        assert e.value.status == status
+
+
+def test_the_same_every_time_and_on_another_stream(cr):
+    import torch
+
+    s = Setup(cr, [(5000, 2), (300, 1), (64, 5)], 8, 2, 64, seed=17)
+    cells, args = s.cells(), s.args()
+    want = cr.convrot_cache_attention(s.Q, *cells, *args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [cr.convrot_cache_attention(s.Q, *cells, *args, stream=st) for _ in range(5) for st in (None, side)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_two_graphs_share_a_workspace_and_follow_the_lengths(cr):
+    import torch
+
+    s = Setup(cr, [(900, 1), (700, 1)], 4, 2, 16, seed=18)
+    pages, lengths, _ = s.args()
+    cells = s.cells()
+    ws = torch.empty(cr.convrot_cache_attention_workspace_bytes(2, 2, 4, 2), dtype=torch.uint8, device="cuda")
+    outs, graphs = [torch.empty_like(s.Q) for _ in range(2)], []
+    other = s.Q.flip(0).contiguous()
+    for q, o in ((s.Q, outs[0]), (other, outs[1])):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            cr.convrot_cache_attention(q, *cells, pages, lengths, O=o, ws=ws)
+        graphs.append(graph)
+    for now in ((900, 700), (1, 650), (0, 64), (513, 700)):
+        lengths.copy_(torch.tensor(now, dtype=torch.int32))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], cr.convrot_cache_attention(s.Q, *cells, pages, lengths))
+        assert torch.equal(outs[1], cr.convrot_cache_attention(other, *cells, pages, lengths))
+    s.seqs = [(513, 1), (700, 1)]
+    s.check(outs[0])
+    graphs.clear()
+
+
+def test_a_decoder_step_by_step(cr):
+    """Projection, positions, cache and attention as a decoder runs them: a prompt, single tokens, then a tree of
+    drafts, against the oracle on the cells the cache ends up with, and the cells against the tokens' own keys."""
+    import torch
+
+    torch.manual_seed(0)
+    hq, hkv, width, page, B = 4, 2, 256, 16, 2
+    layer = cr.ConvRotLinear(torch.randn((hq + 2 * hkv) * 128, width, device="cuda").mul_(0.1).bfloat16())
+    freq, axis = cr.convrot_rope_tables([16, 24, 24], shared=True)
+    cache = cr.ConvRotCache(12, hkv, page)
+    pages = torch.randperm(12, device="cuda").view(B, 6).to(torch.int32)
+    length = [0, 0]
+
+    def step(news, tree=None):
+        T = sum(news)
+        seq = torch.tensor([b for b in range(B) for _ in range(news[b])], device="cuda")
+        at = torch.tensor([length[b] + i for b in range(B) for i in range(news[b])], device="cuda")
+        rows = layer(torch.randn(T, width, device="cuda").bfloat16()).view(T, hq + 2 * hkv, 128)
+        pos = torch.stack([at, at // 3, at % 3]).to(torch.int32)
+        heads = cr.convrot_rope(rows[:, :hq + hkv], pos, freq, axis)
+        slots = cache.slots(pages, seq, at)
+        cache.append(heads[:, hq:], rows[:, hq + hkv:], slots)
+        for b in range(B):
+            length[b] += news[b]
+        lengths = torch.tensor(length, dtype=torch.int32, device="cuda")
+        starts = torch.tensor([0, news[0], T], dtype=torch.int32, device="cuda")
+        O = cache.attention(heads[:, :hq], pages, lengths, starts, tree)
+        # the cells hold this step's keys and values
+        kc, vc, ks, vs = [t[slots.long() // page, :, slots.long() % page].cpu().numpy() for t in cache.cells]
+        for X, c, f in ((heads[:, hq:], kc, ks), (rows[:, hq + hkv:], vc, vs)):
+            ref_c, ref_f = oracle.cache_write(X.double().cpu().numpy())
+            assert np.abs(c.astype(int) - ref_c).max() <= 1 and np.allclose(f, ref_f, rtol=1e-6)
+        s = Setup.__new__(Setup)
+        s.hq, s.hkv, s.page, s.kind = hq, hkv, page, "bf16"
+        s.seqs, s.pages = list(zip(length, news)), pages.cpu().numpy()
+        s.codes = [t.cpu().numpy() for t in (cache.k_codes, cache.v_codes)]
+        s.scales = [t.cpu().numpy() for t in (cache.k_scale, cache.v_scale)]
+        s.starts, s.tree = starts.cpu().numpy(), None if tree is None else tree.cpu().numpy().view(np.uint64)
+        s.q = heads[:, :hq].double().cpu().numpy()
+        s.check(O)
+
+    step([37, 5])
+    for _ in range(3):
+        step([1, 1])
+    step([4, 2], torch.tensor([1, 3, 5, 13, 1, 2], dtype=torch.int64, device="cuda"))
+    cache.check()
+
+
+def test_a_prompt_through_the_dense_attention(cr):
+    """Positions written head by head feed the dense INT8 attention, and keys read back from the cache stand for
+    the same cells: the attention over the cache agrees with the dense one on the values read back."""
+    import torch
+
+    torch.manual_seed(1)
+    S, heads = 200, 3
+    x = torch.randn(3, S, heads, 128, device="cuda").bfloat16()
+    freq, axis = cr.convrot_rope_tables([16, 24, 24])
+    pos = torch.stack([torch.zeros(S), torch.arange(S) // 20, torch.arange(S) % 20]).to(torch.int32).cuda()
+    q, k = (torch.empty(heads, S, 128, dtype=x.dtype, device="cuda") for _ in range(2))
+    cr.convrot_rope(x[0], pos, freq, axis, True, Y=q.transpose(0, 1))
+    cr.convrot_rope(x[1], pos, freq, axis, True, Y=k.transpose(0, 1))
+    cache = cr.ConvRotCache(13, heads, 16)
+    slots = torch.randperm(13 * 16, device="cuda")[:S].to(torch.int32)
+    cache.append(k.transpose(0, 1), x[2], slots)
+    kb, vb = (torch.empty(heads, S, 128, dtype=x.dtype, device="cuda") for _ in range(2))
+    cache.read(slots, K=kb.transpose(0, 1), V=vb.transpose(0, 1))
+    ref = oracle.attention_int8(*(t.double().cpu().numpy() for t in (q, k, vb)))
+    # the last token over the cache, its keys gathered through one page per token place
+    dense = cr.convrot_attention_int8(q, k, vb).double().cpu().numpy()
+    assert np.linalg.norm(dense - ref) <= 3e-3 * np.linalg.norm(ref)
+    # the order of keys does not matter to a token that sees them all
+    flat = torch.full((1, 13), -1, dtype=torch.int32, device="cuda")
+    tight = cr.ConvRotCache(13, heads, 16)
+    tight.append(k.transpose(0, 1), x[2], torch.arange(S, dtype=torch.int32, device="cuda"))
+    flat[0] = torch.arange(13)
+    O = tight.attention(q[:, -1:].transpose(0, 1).contiguous(), flat, torch.tensor([S], dtype=torch.int32, device="cuda"))
+    last = O[0].double().cpu().numpy()
+    assert np.linalg.norm(last - ref[:, -1]) <= 1e-2 * np.linalg.norm(ref[:, -1])

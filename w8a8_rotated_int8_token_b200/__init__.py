@@ -40,14 +40,22 @@ __all__ = [
     "convrot_probe_i8_peak",
     "convrot_attention_workspace_bytes",
     "convrot_attention_int8",
+    "convrot_rope_tables",
+    "convrot_rope",
+    "convrot_cache_append",
+    "convrot_cache_read",
+    "convrot_cache_attention_workspace_bytes",
+    "convrot_cache_attention",
+    "ConvRotCache",
     "ConvRotLinear",
     "lib",
 ]
 
-# convrot_dtype, convrot_wscale_mode, convrot_activation (include/convrot.h)
+# convrot_dtype, convrot_wscale_mode, convrot_activation, convrot_pos_dtype (include/convrot.h)
 DTYPE_BF16, DTYPE_F16 = 0, 1
 WSCALE_TENSOR, WSCALE_CHANNEL = 0, 1
 ACT_NONE, ACT_GELU_ERF = 0, 1
+POS_I32, POS_F32 = 0, 1
 
 STATUS_NAMES = {0: "CONVROT_OK", 1: "CONVROT_ERR_INVALID_ARG", 2: "CONVROT_ERR_UNSUPPORTED",
                 3: "CONVROT_ERR_WORKSPACE", 4: "CONVROT_ERR_CUDA", 5: "CONVROT_ERR_DEVICE_TIMEOUT"}
@@ -398,6 +406,320 @@ def convrot_attention_int8(Q, K, V, softmax_scale=None, O=None, ws=None, stream=
     _check(lib().convrot_attention_int8(_ptr(Q), _ptr(K), _ptr(V), BH, Sq, Skv, D, float(softmax_scale), _ptr(O),
                                         _ptr(ws), ws.numel(), _stream_ptr(stream)), "convrot_attention_int8")
     return O
+
+
+def _elsewhere(t, stream):
+    """None if a call on `t` runs where torch is: t's device current, its current stream.
+    Otherwise a context that makes it so, within which buffers are allocated for the
+    stream that uses them."""
+    import torch
+
+    index = t.get_device()
+    if stream is None:
+        return None if index == torch.cuda.current_device() else torch.cuda.device(index)
+    ptr = _stream_ptr(stream)
+    if index == torch.cuda.current_device() and ptr == _stream_ptr(None):
+        return None
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(ptr, device=index) if ptr else torch.cuda.default_stream(index)
+    elif stream.device_index != index:
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)
+
+
+def _beside(t, name, like, dtype, shape):
+    """A contiguous tensor argument of the given type and shape on the device of `like`."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be on the device of the other tensors")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _heads_view(t, name, dims):
+    """The type code of bf16 or fp16 head vectors [..., heads, D] whose channels are contiguous."""
+    code = _dtype_code(t, name)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dim() not in dims:
+        raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dims)} dimensions, got {t.dim()}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    return code
+
+
+def _strides(t):
+    """Strides in elements, 0 for a dimension of one element (there torch may hold any number)."""
+    return [st if n > 1 else 0 for n, st in zip(t.shape, t.stride())]
+
+
+def _writable(t, name):
+    """Refuses an output whose elements share addresses (an expanded dimension)."""
+    for n, st in zip(t.shape, t.stride()):
+        if n > 1 and st == 0:
+            raise ValueError(f"{name} must not be an expanded tensor")
+
+
+def convrot_rope_tables(sections, theta: float = 10000.0, shared: bool = False, device="cuda"):
+    """The tables of convrot_rope for axes with sections[a] pairs of channels each, in order:
+    (freq float64, axis int32), both [sum(sections)]. Each axis has its own ladder
+    theta^(-i / sections[a]), or, `shared`, pair i of all n takes theta^(-i / n)."""
+    import torch
+
+    sections = [int(n) for n in sections]
+    if not sections or min(sections) < 0 or not theta > 0:
+        raise ValueError("sections must be non-negative counts of pairs, theta positive")
+    n = sum(sections)
+    power = [i / n for i in range(n)] if shared else [i / m for m in sections for i in range(m)]
+    axis = [a for a, m in enumerate(sections) for _ in range(m)]
+    freq = torch.tensor([float(theta) ** -p for p in power], dtype=torch.float64, device=device)
+    return freq, torch.tensor(axis, dtype=torch.int32, device=device)
+
+
+def convrot_rope(X, positions, freq, axis, interleaved: bool = False, inverse: bool = False, Y=None, stream=None):
+    """Rotary positions with several axes: X [B, S, H, D] or [S, H, D] (bf16 or fp16, any
+    strides, channels contiguous) with the pairs of its first 2 * len(freq) channels turned by
+    positions[axis[i]] * freq[i]. positions [axes, S] or [axes, B, S], int32 or float32;
+    freq float64 (radians), axis int32. `inverse` turns back, which is also the gradient.
+    Y: an output of X's shape and any strides (X itself works in place); with
+    Y = buf.transpose(-3, -2) the heads come out as convrot_attention_int8 takes them."""
+    import torch
+
+    code = _heads_view(X, "X", (3, 4))
+    where = _elsewhere(X, stream)
+    if where is not None:
+        with where:
+            return convrot_rope(X, positions, freq, axis, interleaved, inverse, Y)
+    S, H, D = X.shape[-3:]
+    B = X.shape[0] if X.dim() == 4 else 1
+    pairs = freq.shape[0] if freq.dim() == 1 else -1
+    if pairs < 0 or 2 * pairs > D:
+        raise ValueError("freq must be [pairs] with at most D / 2 pairs")
+    _beside(freq, "freq", X, torch.float64, (pairs,))
+    _beside(axis, "axis", X, torch.int32, (pairs,))
+    if positions.dtype == torch.int32:
+        pos_code = POS_I32
+    elif positions.dtype == torch.float32:
+        pos_code = POS_F32
+    else:
+        raise TypeError(f"positions: expected int32 or float32, got {positions.dtype}")
+    if positions.get_device() != X.get_device():
+        raise ValueError("positions must be on the device of the other tensors")
+    if positions.dim() not in (2, 3) or positions.shape[0] < 1 or positions.shape[-1] != S or \
+            (positions.dim() == 3 and positions.shape[1] != B):
+        raise ValueError(f"positions: expected [axes, {S}] or [axes, {B}, {S}], got {tuple(positions.shape)}")
+    if Y is None:
+        Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    else:
+        if _heads_view(Y, "Y", (X.dim(),)) != code or Y.shape != X.shape or Y.get_device() != X.get_device():
+            raise ValueError("Y must have the shape, dtype and device of X")
+        _writable(Y, "Y")
+    xs, ys, ps = _strides(X), _strides(Y), _strides(positions)
+    batched = X.dim() == 4
+    _check(lib().convrot_rope(_ptr(X), code, B, S, H, D, 2 * pairs, xs[0] if batched else 0, xs[-3], xs[-2],
+                              _ptr(positions), pos_code, positions.shape[0], ps[0], ps[1] if len(ps) == 3 else 0,
+                              ps[-1], _ptr(freq), _ptr(axis), int(interleaved), int(inverse), _ptr(Y),
+                              ys[0] if batched else 0, ys[-3], ys[-2], _stream_ptr(None)), "convrot_rope")
+    return Y
+
+
+def _cells(like, k_codes, v_codes, k_scale, v_scale):
+    """(pages, heads, page size) of the four cache tensors, on the device of `like`."""
+    import torch
+
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes must be [pages, heads, page size, 128]")
+    shape = k_codes.shape
+    _beside(k_codes, "k_codes", like, torch.int8, shape)
+    _beside(v_codes, "v_codes", like, torch.int8, shape)
+    _beside(k_scale, "k_scale", like, torch.float32, shape[:3])
+    _beside(v_scale, "v_scale", like, torch.float32, shape[:3])
+    if shape[3] != 128:
+        raise ValueError("the cache holds head vectors of 128 channels")
+    return shape[0], shape[1], shape[2]
+
+
+def convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status=None, stream=None):
+    """Write keys and values K, V [T, H, 128] (bf16 or fp16, strided tokens and heads) into the
+    rotated int8 cache: token t to slot slots[t] (int32; page * page size + place; negative: skipped;
+    the others must differ). Cache: codes int8 [pages, H, page size, 128], scales float32 [pages, H,
+    page size]. status: an int32 [1] tensor that a slot past the cache sets to 1, or None."""
+    import torch
+
+    code = _heads_view(K, "K", (3,))
+    where = _elsewhere(K, stream)
+    if where is not None:
+        with where:
+            return convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status)
+    if _heads_view(V, "V", (3,)) != code or V.shape != K.shape or V.get_device() != K.get_device():
+        raise ValueError("V must have the shape, dtype and device of K")
+    T, H, D = K.shape
+    pages, heads, page = _cells(K, k_codes, v_codes, k_scale, v_scale)
+    if heads != H:
+        raise ValueError(f"K has {H} heads, the cache {heads}")
+    _beside(slots, "slots", K, torch.int32, (T,))
+    if status is not None:
+        _beside(status, "status", K, torch.int32, (1,))
+    kt, kh, _ = _strides(K)
+    vt, vh, _ = _strides(V)
+    _check(lib().convrot_cache_append(_ptr(K), _ptr(V), code, T, H, D, kt, kh, vt, vh, _ptr(slots), _ptr(k_codes),
+                                      _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), pages, page, _ptr(status),
+                                      _stream_ptr(None)), "convrot_cache_append")
+
+
+def convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype=None, K=None, V=None, status=None,
+                       stream=None):
+    """Read the keys and values of slots [T] back: (K, V) [T, H, 128] in `dtype` (bf16 by default, or
+    fp16); a negative slot reads as zeros. K, V: outputs with strided tokens and heads, or None."""
+    import torch
+
+    if not slots.is_cuda:
+        raise ValueError("slots must be on a CUDA device")
+    where = _elsewhere(slots, stream)
+    if where is not None:
+        with where:
+            return convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype, K, V, status)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [T]")
+    T = slots.shape[0]
+    _beside(slots, "slots", slots, torch.int32, (T,))
+    pages, H, page = _cells(slots, k_codes, v_codes, k_scale, v_scale)
+    if dtype is None:
+        dtype = K.dtype if K is not None else V.dtype if V is not None else torch.bfloat16
+    if K is None:
+        K = torch.empty((T, H, 128), dtype=dtype, device=slots.device)
+    if V is None:
+        V = torch.empty((T, H, 128), dtype=dtype, device=slots.device)
+    for t, name in ((K, "K"), (V, "V")):
+        code = _heads_view(t, name, (3,))
+        if t.dtype != dtype or t.shape != (T, H, 128) or t.get_device() != slots.get_device():
+            raise ValueError(f"{name} must be [{T}, {H}, 128] {dtype} on the device of the other tensors")
+        _writable(t, name)
+    if status is not None:
+        _beside(status, "status", slots, torch.int32, (1,))
+    kt, kh, _ = _strides(K)
+    vt, vh, _ = _strides(V)
+    _check(lib().convrot_cache_read(_ptr(slots), T, H, 128, _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
+                                    _ptr(v_scale), pages, page, _ptr(K), _ptr(V), code, kt, kh, vt, vh, _ptr(status),
+                                    _stream_ptr(None)), "convrot_cache_read")
+    return K, V
+
+
+def convrot_cache_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int = 128) -> int:
+    return int(lib().convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D))
+
+
+def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts=None, tree=None,
+                            softmax_scale=None, O=None, ws=None, stream=None):
+    """Attention of the newest tokens over the rotated int8 cache: Q [T, Hq, 128] (bf16 or fp16,
+    strided tokens and heads) -> O [T, Hq, 128]. pages [B, n] int32: the cache pages of each sequence;
+    lengths [B] int32: its keys, the new tokens' included; starts [B + 1] int32: its tokens in Q
+    (None: token b belongs to sequence b). Among its new tokens a query sees the earlier ones and
+    itself, or, with tree [T] int64, those whose bit is set in its mask (at most 64 a sequence).
+    See include/convrot.h."""
+    import torch
+
+    code = _heads_view(Q, "Q", (3,))
+    where = _elsewhere(Q, stream)
+    if where is not None:
+        with where:
+            return convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree,
+                                           softmax_scale, O, ws)
+    T, Hq, D = Q.shape
+    num_pages, Hkv, page = _cells(Q, k_codes, v_codes, k_scale, v_scale)
+    if Hq % Hkv != 0 or Hq == 0:
+        raise ValueError(f"{Hq} query heads do not divide among {Hkv} key heads")
+    if lengths.dim() != 1:
+        raise ValueError("lengths must be [B]")
+    B = lengths.shape[0]
+    _beside(lengths, "lengths", Q, torch.int32, (B,))
+    if pages.dtype != torch.int32:
+        raise TypeError(f"pages: expected torch.int32, got {pages.dtype}")
+    if pages.dim() != 2 or pages.shape[0] != B or (pages.stride(1) != 1 and pages.shape[1] > 1) or \
+            pages.get_device() != Q.get_device():
+        raise ValueError(f"pages must be [{B}, n] with contiguous rows on the device of the other tensors")
+    if starts is not None:
+        _beside(starts, "starts", Q, torch.int32, (B + 1,))
+    elif T != B:
+        raise ValueError("without starts Q must hold one token per sequence")
+    if tree is not None:
+        _beside(tree, "tree", Q, torch.int64, (T,))
+    if softmax_scale is None:
+        softmax_scale = 0.08838834764831845  # 1 / sqrt(128)
+    if O is None:
+        O = torch.empty((T, Hq, D), dtype=Q.dtype, device=Q.device)
+    else:
+        if _heads_view(O, "O", (3,)) != code or O.shape != Q.shape or O.get_device() != Q.get_device():
+            raise ValueError("O must have the shape, dtype and device of Q")
+        _writable(O, "O")
+    if ws is None:
+        need = convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D)
+        ws = torch.empty((max(need, 256),), dtype=torch.uint8, device=Q.device)
+    elif ws.get_device() != Q.get_device() or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous on the device of the other tensors")
+    qt, qh, _ = _strides(Q)
+    ot, oh, _ = _strides(O)
+    _check(lib().convrot_cache_attention(_ptr(Q), code, T, Hq, D, qt, qh, _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
+                                         _ptr(v_scale), num_pages, page, Hkv, _ptr(pages), B, pages.shape[1],
+                                         _strides(pages)[0], _ptr(lengths), _ptr(starts), _ptr(tree),
+                                         float(softmax_scale), _ptr(O), ot, oh, _ptr(ws),
+                                         ws.numel() * ws.element_size(), _stream_ptr(None)),
+           "convrot_cache_attention")
+    return O
+
+
+class ConvRotCache:
+    """A paged cache of rotated int8 keys and values for `heads` key/value heads of 128 channels.
+
+    ``cache.append(K, V, slots)``, ``cache.read(slots)`` and ``cache.attention(Q, pages, lengths)`` are
+    the entry points of the same names on its tensors; ``cache.slots(pages, sequence, position)`` finds
+    the slots of tokens. ``check()`` synchronises and raises if a slot was past the cache.
+    """
+
+    def __init__(self, num_pages: int, heads: int, page_size: int = 64, device="cuda"):
+        import torch
+
+        shape = (num_pages, heads, page_size)
+        self.page_size = page_size
+        self.k_codes = torch.zeros((*shape, 128), dtype=torch.int8, device=device)
+        self.v_codes = torch.zeros((*shape, 128), dtype=torch.int8, device=device)
+        self.k_scale = torch.zeros(shape, dtype=torch.float32, device=device)
+        self.v_scale = torch.zeros(shape, dtype=torch.float32, device=device)
+        self.status = torch.zeros((1,), dtype=torch.int32, device=device)
+
+    @property
+    def cells(self):
+        return self.k_codes, self.v_codes, self.k_scale, self.v_scale
+
+    def slots(self, pages, sequence, position):
+        """Slots (int32) of the tokens at `position` of the sequences whose rows of `pages` are
+        `sequence`; -1 where `pages` has no such place or no page for it."""
+        import torch
+
+        sequence, position = sequence.long(), position.long()
+        if pages.numel() == 0:
+            return torch.full(position.shape, -1, dtype=torch.int32, device=position.device)
+        column = position // self.page_size
+        page = pages[sequence.clamp(0, pages.shape[0] - 1), column.clamp(0, pages.shape[1] - 1)]
+        there = ((sequence >= 0) & (sequence < pages.shape[0]) & (position >= 0) & (column < pages.shape[1])
+                 & (page >= 0))
+        return torch.where(there, page * self.page_size + position % self.page_size, -1).to(torch.int32)
+
+    def append(self, K, V, slots, stream=None):
+        convrot_cache_append(K, V, slots, *self.cells, status=self.status, stream=stream)
+
+    def read(self, slots, dtype=None, K=None, V=None, stream=None):
+        return convrot_cache_read(slots, *self.cells, dtype=dtype, K=K, V=V, status=self.status, stream=stream)
+
+    def attention(self, Q, pages, lengths, starts=None, tree=None, softmax_scale=None, O=None, ws=None, stream=None):
+        return convrot_cache_attention(Q, *self.cells, pages, lengths, starts, tree, softmax_scale, O, ws, stream)
+
+    def check(self):
+        if int(self.status.item()) != 0:
+            raise ConvRotError(int(self.status.item()), "ConvRotCache")
 
 
 class ConvRotLinear:

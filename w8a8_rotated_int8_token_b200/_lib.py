@@ -50,6 +50,18 @@ SIGNATURES = {
     "convrot_attention_workspace_bytes": (_size, [_i64, _i64, _i64, _i64]),
     "convrot_attention_int8": (_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _i64, ctypes.c_float,
                                       _c_void_p, _c_void_p, _size, _c_void_p]),
+    "convrot_rope": (_int, [_c_void_p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _c_void_p, _int, _i64,
+                            _i64, _i64, _i64, _c_void_p, _c_void_p, _int, _int, _c_void_p, _i64, _i64, _i64,
+                            _c_void_p]),
+    "convrot_cache_append": (_int, [_c_void_p, _c_void_p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _c_void_p,
+                                    _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p]),
+    "convrot_cache_read": (_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64,
+                                  _c_void_p, _c_void_p, _int, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p]),
+    "convrot_cache_attention_workspace_bytes": (_size, [_i64, _i64, _i64, _i64, _i64]),
+    "convrot_cache_attention": (_int, [_c_void_p, _int, _i64, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
+                                       _c_void_p, _i64, _i64, _i64, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p,
+                                       _c_void_p, ctypes.c_float, _c_void_p, _i64, _i64, _c_void_p, _size,
+                                       _c_void_p]),
     "convrot_probe_i8_peak_ctas": (_int, []),
     "convrot_probe_ex2_peak": (_int, [_i64, _c_void_p, _size, _c_void_p]),
     "convrot_probe_ex2_per_iter": (_i64, []),

@@ -1,0 +1,904 @@
+// Attention of a few new tokens per sequence over the rotated int8 key/value
+// cache: single tokens, causal chunks and trees of drafted tokens.
+//
+//   S[r, j] = (cq[r] . ck[j]) s_q[r] s_k[j] softmax_scale,  O = (softmax(S) (cv s_v)) R,
+//
+// with cq, s_q the int8 codes of the rotated query (the rule of the INT8
+// attention), the integer products exact, softmax in float32 in one pass over
+// the keys with a running maximum and sum, and one rotation of the output row
+// (R = H_128 / sqrt(128) is its own inverse and linear, so it commutes with the
+// sum over keys).
+//
+// Bound by memory: every key costs 264 bytes and is read once per tile of
+// query rows. The rows of a tile are the query heads that share a key head
+// times the sequence's new tokens. The work (sequence, row tile, key head,
+// tiles of 64 keys) is one long line cut into equal pieces, one per CTA, so that
+// ragged lengths and small batches fill the GPU alike; a CTA finds its piece
+// from the lengths on the device. Where an item is cut, each CTA leaves its
+// unnormalised sum, maximum and row sum in the workspace, and a second kernel
+// joins them in a fixed order, so the result does not depend on timing.
+//
+// One CTA is four warps; warp w takes keys 16 w .. 16 w + 15 of every 64-key tile
+// for all 16 MT rows. Each warp feeds itself: one lane streams its keys' codes by
+// TMA (boxes of 16 keys, 128-byte swizzle, so that a box never crosses a page)
+// and their scales by bulk copies into the warp's own ring of stages, so no warp
+// waits for another before the end of a run. A warp that issued no copies of
+// others' keys needs no producer warp beside it: with a fifth warp a quarter of
+// an SM would hold three of them at two CTAs and leave 168 registers a thread.
+//   S     int8 mma m16n8k32 on fragments read from shared memory, with the
+//         channels permuted alike on both sides so that a thread reads 32
+//         consecutive bytes of a key;
+//   P V   fp16 mma m16n8k16, the codes widened exactly to fp16 in registers. The
+//         weights p s_v are brought to fp16's range by a factor per row, kept so
+//         that the largest weight so far lies between 1 and 2^12: rounding one to
+//         fp16 costs at most 2^-11 of it or 2^-25 of the largest, whatever the
+//         range of the value scales.
+// The running maximum and that factor move only when a key passes them by 2^8
+// and 2^12; a vote of the warp is all it costs otherwise.
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <cstdint>
+
+#include "convrot.h"
+#include "fwht128.cuh"
+#include "fwht_dev.cuh"
+#include "ptx_sm100.cuh"
+
+namespace convrot {
+
+namespace {
+
+constexpr int CA_D = 128;
+constexpr int CA_WARPS = 4;
+constexpr int CA_THREADS = 32 * CA_WARPS;
+constexpr int CA_SUB = 16;                 // keys of a warp's stage
+constexpr int CA_KT = CA_SUB * CA_WARPS;   // keys of a tile
+constexpr int CA_CODES = CA_SUB * CA_D;    // key (or value) codes of a stage
+constexpr int CA_STAGE = 2 * CA_CODES;
+constexpr int CA_QPITCH = CA_D + 16;       // bytes between query rows in shared memory
+constexpr uint64_t CA_TIMEOUT_NS = 2000000000ull;
+constexpr int CA_BAD = CONVROT_ERR_INVALID_ARG;
+constexpr int CA_TIMEOUT = CONVROT_ERR_DEVICE_TIMEOUT;
+constexpr int CA_MAX_WORKERS = 480;        // pieces the workspace has room for
+
+// A shape of CTA: 16 MT rows, stages of a warp's ring, CTAs per SM.
+template <int MT, int ST, int OCC>
+struct CaShape {
+  static constexpr int kMt = MT, kStages = ST, kOcc = OCC;
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kOffScale = CA_WARPS * ST * CA_STAGE;  // per stage: 16 key, 16 value scales
+  static constexpr int kOffQ = kOffScale + CA_WARPS * ST * 2 * CA_SUB * 4;
+  static constexpr int kOffRow = kOffQ + kRows * CA_QPITCH;   // per row: tree bits, factor, first key not seen
+  static constexpr int kOffScan = kOffRow + kRows * 16;
+  static constexpr int kOffBar = kOffScan + 64;
+  static constexpr int kBytes = kOffBar + CA_WARPS * ST * 8;
+  static constexpr int kAlloc = kBytes + 1024;                // slack to align the base to 1024 bytes
+  // the end of a run exchanges sums through the (then idle) ring: per warp 8 KB and statistics per 16 rows
+  static constexpr int kJoinWarp = MT * 16 * 32 * 16 + MT * 32 * 16;
+  static_assert(2 * kJoinWarp <= kOffScale, "exchange fits the ring");
+};
+
+using Shape16 = CaShape<1, 4, 3>;
+using Shape32 = CaShape<2, 6, 2>;
+
+// What a piece leaves for the join: its last item, if that goes on in the next pieces.
+struct CaCut {
+  int pieces;       // pieces that hold a part of the item (0: nothing to join)
+  int rows;         // rows of the tile
+  int row0;         // first row of the tile in the sequence's rows
+  int head;         // key head
+  int token0;       // first query token of the sequence
+  int pad[3];
+};
+
+struct CaParams {
+  const uint16_t* q;
+  uint16_t* o;
+  int64_t qt, qh, ot, oh;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* pages;
+  const int32_t* lengths;
+  const int32_t* starts;      // null: token b belongs to sequence b
+  const unsigned long long* tree;  // null: causal
+  int64_t table_stride;
+  int T, B, Hkv, G, table_pages, num_pages, page_shift;
+  float c_scale;              // softmax_scale log2(e)
+  int* piece_status;          // [workers]
+  CaCut* cuts;                // [workers]
+  float* part;                // [2 workers][rows][128]
+  float2* part_ml;            // [2 workers][rows] maximum, sum
+  int* status;                // the call's status word, written by the join
+  int workers;
+};
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// float(acc) for |acc| < 2^22 (128 products of codes up to 127) without a conversion instruction
+__device__ __forceinline__ float code_sum_to_float(int acc) {
+  return __uint_as_float(static_cast<uint32_t>(acc) + 0x4B400000u) - 12582912.0f;
+}
+
+// A sequence: its keys, its query tokens, and its share of the line of work.
+struct CaSeq {
+  int keys, first, news;
+  int tiles;        // key tiles of an item (at least one, which writes a row without keys)
+  int64_t count;    // tiles of all its items
+};
+
+template <int ROWS>
+__device__ __forceinline__ CaSeq ca_seq(const CaParams& p, int b, int& bad) {
+  CaSeq s;
+  const int64_t room = static_cast<int64_t>(p.table_pages) << p.page_shift;
+  int keys = __ldg(p.lengths + b), lo = b, hi = b + 1;
+  if (p.starts != nullptr) lo = __ldg(p.starts + b), hi = __ldg(p.starts + b + 1);
+  if (keys < 0 || keys > room || lo < 0 || hi < lo || hi > p.T) bad |= CA_BAD;
+  keys = keys < 0 ? 0 : keys > room ? static_cast<int>(room) : keys;
+  lo = lo < 0 ? 0 : lo > p.T ? p.T : lo;
+  hi = hi < lo ? lo : hi > p.T ? p.T : hi;
+  s.keys = keys;
+  s.first = lo;
+  s.news = hi - lo;
+  const int64_t rows = static_cast<int64_t>(s.news) * p.G;
+  s.tiles = keys > CA_KT ? static_cast<int>((static_cast<int64_t>(keys) + CA_KT - 1) / CA_KT) : 1;
+  s.count = (rows + ROWS - 1) / ROWS * p.Hkv * s.tiles;
+  return s;
+}
+
+// A run of one item's tiles within a piece.
+struct CaRun {
+  int head, row0, rows, t0, t1;
+};
+
+// Walks a piece: the runs from `pos` to `end`, the same for every warp.
+template <int ROWS>
+struct CaWalk {
+  int64_t pos, end, base;
+  int b;
+  CaSeq s;
+  __device__ __forceinline__ bool next(const CaParams& p, CaRun* r, int& bad) {
+    if (pos >= end) return false;
+    while (pos >= base + s.count) {
+      base += s.count;
+      ++b;
+      s = ca_seq<ROWS>(p, b, bad);  // pos < total, so a sequence with work follows
+    }
+    const int64_t rel = pos - base, item = rel / s.tiles;
+    r->t0 = static_cast<int>(rel - item * s.tiles);
+    const int64_t left = end - pos, most = s.tiles - r->t0;
+    r->t1 = r->t0 + static_cast<int>(left < most ? left : most);
+    r->head = static_cast<int>(item % p.Hkv);
+    const int64_t row0 = item / p.Hkv * ROWS;
+    r->row0 = static_cast<int>(row0);
+    const int64_t rows = static_cast<int64_t>(s.news) * p.G - row0;
+    r->rows = rows < ROWS ? static_cast<int>(rows) : ROWS;
+    pos += r->t1 - r->t0;
+    return true;
+  }
+};
+
+template <class Shape, bool F16>
+__global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
+    cache_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                           const CaParams p) {
+  constexpr int MT = Shape::kMt, ST = Shape::kStages, ROWS = Shape::kRows;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  int64_t* scan = reinterpret_cast<int64_t*>(smem + Shape::kOffScan);  // a sum per warp; then found
+  uint8_t* qs = smem + Shape::kOffQ;
+  unsigned long long* row_bits = reinterpret_cast<unsigned long long*>(smem + Shape::kOffRow);
+  float* row_c = reinterpret_cast<float*>(row_bits + ROWS);
+  int* row_lim = reinterpret_cast<int*>(row_c + ROWS);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t4 = lane & 3;
+  uint8_t* ring = smem + warp * ST * CA_STAGE;
+  float* ring_scale = reinterpret_cast<float*>(smem + Shape::kOffScale) + warp * ST * 2 * CA_SUB;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Shape::kOffBar) + warp * ST;
+
+  griddep_launch_dependents();  // the join's CTAs may take their places; they wait for this grid
+  if (lane == 0) {
+    for (int i = 0; i < ST; ++i) mbar_init(full + i, 1);
+    fence_mbar_init();
+  }
+  if (tid == 0) {
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+
+  // The piece: all tiles summed over the sequences, then the sequence it starts in.
+  int bad = 0;
+  CaWalk<ROWS> walk{};
+  int64_t per = 0;
+  {
+    int64_t mine = 0, sum = 0;
+    for (int b = tid; b < p.B; b += CA_THREADS) {
+      const int64_t count = ca_seq<ROWS>(p, b, bad).count;
+      if (b == tid) mine = count;
+      sum += count;
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+    if (lane == 0) scan[warp] = sum;
+    __syncthreads();
+    const int64_t total = (scan[0] + scan[1]) + (scan[2] + scan[3]);
+    per = (total + gridDim.x - 1) / gridDim.x;
+    walk.pos = blockIdx.x * per;
+    walk.end = walk.pos + per < total ? walk.pos + per : total;
+    if (walk.pos < total) {
+      int64_t before = 0;
+      for (int b0 = 0; b0 < p.B; b0 += CA_THREADS) {
+        const int b = b0 + tid;
+        int64_t count = mine;
+        if (b0 > 0) count = b < p.B ? ca_seq<ROWS>(p, b, bad).count : 0;
+        int64_t incl = count;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+          const int64_t other = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+          if (lane >= m) incl += other;
+        }
+        __syncthreads();  // the sums before have been read
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        int64_t lo = before + incl - count;
+#pragma unroll
+        for (int w = 0; w < CA_WARPS; ++w) {
+          if (w < warp) lo += scan[w];
+          before += scan[w];
+        }
+        if (lo <= walk.pos && walk.pos < lo + count) {
+          scan[4] = b;
+          scan[5] = lo;
+        }
+        if (walk.pos < before) break;  // the same for every thread
+      }
+      __syncthreads();
+      walk.b = static_cast<int>(scan[4]);
+      walk.base = scan[5];
+      walk.s = ca_seq<ROWS>(p, walk.b, bad);
+    }
+  }
+
+  bool ok = true;
+  uint32_t phases = 0;  // parity of each stage's next completion
+  CaRun r;
+  CaCut cut{};
+  while (walk.next(p, &r, bad)) {
+    const int keys = walk.s.keys;
+    const int context = keys - walk.s.news;  // key of the first new token; may be negative
+    const int32_t* table = p.pages + walk.b * p.table_stride;
+    uint32_t live = 0;  // stages with copies under way
+    auto issue = [&](int t, int st) {
+      const int key = t * CA_KT + warp * CA_SUB;
+      live &= ~(1u << st);
+      if (t < r.t1 && key < keys && ok) {
+        const int page = __ldg(table + (key >> p.page_shift));
+        if (page >= 0 && page < p.num_pages) {
+          live |= 1u << st;
+          if (lane == 0) {
+            const int64_t cell = ((static_cast<int64_t>(page) * p.Hkv + r.head) << p.page_shift) +
+                                 (key & ((1 << p.page_shift) - 1));
+            uint8_t* to = ring + st * CA_STAGE;
+            float* sc = ring_scale + st * 2 * CA_SUB;
+            mbar_arrive_expect_tx(full + st, CA_STAGE + 2 * CA_SUB * 4);
+            tma_load_2d(to, &tmK, full + st, 0, static_cast<int32_t>(cell));
+            bulk_load(sc, p.k_scale + cell, CA_SUB * 4, full + st);
+            tma_load_2d(to + CA_CODES, &tmV, full + st, 0, static_cast<int32_t>(cell));
+            bulk_load(sc + CA_SUB, p.v_scale + cell, CA_SUB * 4, full + st);
+          }
+        } else {
+          bad |= CA_BAD;  // its keys are not seen
+        }
+      }
+    };
+#pragma unroll 1
+    for (int i = 0; i < ST; ++i) issue(r.t0 + i, i);
+
+    // ---- the tile's queries: rotated, quantised, into shared memory
+    if (p.tree != nullptr && walk.s.news > 64) bad |= CA_BAD;
+#pragma unroll
+    for (int k = 0; k < ROWS / CA_WARPS; ++k) {
+      const int row = warp + k * CA_WARPS;
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      int i = 0;
+      if (row < r.rows) {
+        const int of = r.row0 + row;
+        i = of / p.G;
+        const uint16_t* src = p.q + (walk.s.first + i) * p.qt + (r.head * p.G + (of - i * p.G)) * p.qh;
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + 4 * lane));
+        const float2 a = fwht::widen_pair<F16>(w.x), b = fwht::widen_pair<F16>(w.y);
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+      }
+      fwht::fwht128_warp(v, lane);
+      float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
+      const fwht::CodeFactor f = fwht::code_factor(amax);
+      float c[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = fmaf(v[e] * f.pre, f.ci, fwht::kRoundMagic);
+      *reinterpret_cast<uint32_t*>(qs + row * CA_QPITCH + 4 * lane) = fwht::pack4(c[0], c[1], c[2], c[3]);
+      if (lane == 0) {
+        row_c[row] = fwht::scale_of<128>(amax) * p.c_scale;
+        // keys below the limit are seen, and with a tree the drafted keys whose bit is set
+        const bool tree = p.tree != nullptr;
+        row_lim[row] = tree ? context : context + i + 1;
+        row_bits[row] = tree && row < r.rows ? __ldg(p.tree + walk.s.first + i) : 0ull;
+      }
+    }
+    __syncthreads();
+    uint32_t qa[MT][16];
+    float cr[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int row = m * 16 + 8 * half + g;
+        const uint4 a = *reinterpret_cast<const uint4*>(qs + row * CA_QPITCH + 32 * t4);
+        const uint4 b = *reinterpret_cast<const uint4*>(qs + row * CA_QPITCH + 32 * t4 + 16);
+        qa[m][half] = a.x, qa[m][2 + half] = a.y, qa[m][4 + half] = a.z, qa[m][6 + half] = a.w;
+        qa[m][8 + half] = b.x, qa[m][10 + half] = b.y, qa[m][12 + half] = b.z, qa[m][14 + half] = b.w;
+        cr[m][half] = row_c[row];
+      }
+    }
+    float acc[MT][16][4], mx[MT][2], l[MT][2], inv[MT][2];  // inv: the weights' factor (0: none yet)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.0f;
+      mx[m][0] = mx[m][1] = -INFINITY;
+      l[m][0] = l[m][1] = inv[m][0] = inv[m][1] = 0.0f;
+    }
+
+    // ---- the keys
+    const int clear = p.tree != nullptr ? context : context + 1;  // keys below it are seen by every row
+    int st = 0;
+#pragma unroll 1
+    for (int t = r.t0; t < r.t1; ++t) {
+      const int key0 = t * CA_KT + warp * CA_SUB;
+      if (live >> st & 1) {
+        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(full + st, phases >> st & 1, nullptr, CA_TIMEOUT_NS));
+        if (!ok) break;
+        phases ^= 1u << st;
+        const uint8_t* kc = ring + st * CA_STAGE;
+        const uint8_t* vc = kc + CA_CODES;
+        const float* sk = ring_scale + st * 2 * CA_SUB;
+        float s[MT][2][4];
+        float2 sv[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const uint8_t* row = kc + (8 * n + g) * CA_D;
+          const uint4 a = *reinterpret_cast<const uint4*>(row + (((2 * t4) ^ g) << 4));
+          const uint4 b = *reinterpret_cast<const uint4*>(row + (((2 * t4 + 1) ^ g) << 4));
+          const float2 f2 = *reinterpret_cast<const float2*>(sk + 8 * n + 2 * t4);
+          sv[n] = *reinterpret_cast<const float2*>(sk + CA_SUB + 8 * n + 2 * t4);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            int d[4] = {0, 0, 0, 0};
+            mma_s8(d, qa[m][0], qa[m][1], qa[m][2], qa[m][3], a.x, a.y);
+            mma_s8(d, qa[m][4], qa[m][5], qa[m][6], qa[m][7], a.z, a.w);
+            mma_s8(d, qa[m][8], qa[m][9], qa[m][10], qa[m][11], b.x, b.y);
+            mma_s8(d, qa[m][12], qa[m][13], qa[m][14], qa[m][15], b.z, b.w);
+            s[m][n][0] = code_sum_to_float(d[0]) * (cr[m][0] * f2.x);
+            s[m][n][1] = code_sum_to_float(d[1]) * (cr[m][0] * f2.y);
+            s[m][n][2] = code_sum_to_float(d[2]) * (cr[m][1] * f2.x);
+            s[m][n][3] = code_sum_to_float(d[3]) * (cr[m][1] * f2.y);
+          }
+        }
+        if (key0 + CA_SUB > clear || key0 + CA_SUB > keys) {
+          // keys a row does not see; their scales may be anything, so nothing computed from them is kept
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = key0 + 8 * n + 2 * t4 + e;
+              const int drafted = key - context;
+              if (key >= keys) (e ? sv[n].y : sv[n].x) = 0.0f;
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  const int row = m * 16 + 8 * half + g;
+                  const bool seen = key < keys && (key < row_lim[row] || (drafted >= 0 && drafted < 64 &&
+                                                                          (row_bits[row] >> drafted & 1ull) != 0));
+                  if (!seen) s[m][n][2 * half + e] = -INFINITY;
+                }
+              }
+            }
+          }
+        }
+        uint32_t pw[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          float top[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            top[half] = fmaxf(fmaxf(s[m][0][2 * half], s[m][0][2 * half + 1]),
+                              fmaxf(s[m][1][2 * half], s[m][1][2 * half + 1]));
+          if (__any_sync(0xFFFFFFFFu, top[0] > mx[m][0] + 8.0f || top[1] > mx[m][1] + 8.0f)) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float now = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 1));
+              now = fmaxf(mx[m][half], fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, 2)));
+              if (now > mx[m][half]) {
+                // the sums stay as they are: their unit shrinks with the weights'
+                l[m][half] *= ex2_approx(mx[m][half] - now);
+                inv[m][half] *= ex2_approx(now - mx[m][half]);
+                mx[m][half] = now;
+                if (!(inv[m][half] <= 0x1p100f)) {  // nothing that came before is left beside this key
+                  inv[m][half] = 0.0f;
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) acc[m][i][2 * half] = acc[m][i][2 * half + 1] = 0.0f;
+                }
+              }
+            }
+          }
+          // weights p s_v; a row that has seen nothing has no maximum
+          float x[2][4], big[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float ref = mx[m][half] == -INFINITY ? 0.0f : mx[m][half];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const float p0 = ex2_approx(s[m][n][2 * half] - ref), p1 = ex2_approx(s[m][n][2 * half + 1] - ref);
+              l[m][half] += p0 + p1;
+              x[n][2 * half] = p0 > 0.0f ? p0 * sv[n].x : 0.0f;
+              x[n][2 * half + 1] = p1 > 0.0f ? p1 * sv[n].y : 0.0f;
+            }
+            big[half] = fmaxf(fmaxf(x[0][2 * half], x[0][2 * half + 1]), fmaxf(x[1][2 * half], x[1][2 * half + 1]));
+          }
+          const bool grow = (inv[m][0] == 0.0f ? big[0] > 0.0f : big[0] * inv[m][0] > 4096.0f) ||
+                            (inv[m][1] == 0.0f ? big[1] > 0.0f : big[1] * inv[m][1] > 4096.0f);
+          if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float now = fmaxf(big[half], __shfl_xor_sync(0xFFFFFFFFu, big[half], 1));
+              now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, 2));
+              // 2^-e for the largest weight's exponent e, within float32's normal range
+              const uint32_t e = min(max(__float_as_uint(now) >> 23, 27u), 227u);
+              const float to = __uint_as_float((254u - e) << 23);
+              if (now > 0.0f && (inv[m][half] == 0.0f || to < inv[m][half])) {
+                const float by = inv[m][half] == 0.0f ? 1.0f : to / inv[m][half];
+                inv[m][half] = to;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  acc[m][i][2 * half] *= by;
+                  acc[m][i][2 * half + 1] *= by;
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const __half2 a = __floats2half2_rn(x[n][0] * inv[m][0], x[n][1] * inv[m][0]);
+            const __half2 b = __floats2half2_rn(x[n][2] * inv[m][1], x[n][3] * inv[m][1]);
+            pw[m][2 * n] = *reinterpret_cast<const uint32_t*>(&a);
+            pw[m][2 * n + 1] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+        }
+        // values: keys 2t, 2t + 1, 2t + 8, 2t + 9, channels 16 g .. 16 g + 15
+        uint4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = 2 * t4 + (k & 1) + 8 * (k >> 1);
+          w[k] = *reinterpret_cast<const uint4*>(vc + key * CA_D + ((g ^ (key & 7)) << 4));
+        }
+        const __half2 offset = __floats2half2_rn(1152.0f, 1152.0f);
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          uint32_t u[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            u[k] = (q4 == 0 ? w[k].x : q4 == 1 ? w[k].y : q4 == 2 ? w[k].z : w[k].w) ^ 0x80808080u;
+#pragma unroll
+          for (int pair = 0; pair < 2; ++pair) {
+            // bytes of channels 4 q4 + 2 pair and + 1 of two keys, interleaved
+            const uint32_t z0 = __byte_perm(u[0], u[1], pair ? 0x7362 : 0x5140);
+            const uint32_t z1 = __byte_perm(u[2], u[3], pair ? 0x7362 : 0x5140);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              // fp16 of a code: the byte plus 128 in the low bits of 1024, minus 1152, exactly
+              const uint32_t h0 = __byte_perm(z0, 0x64646464u, e ? 0x4342 : 0x4140);
+              const uint32_t h1 = __byte_perm(z1, 0x64646464u, e ? 0x4342 : 0x4140);
+              const __half2 b0 = __hsub2(*reinterpret_cast<const __half2*>(&h0), offset);
+              const __half2 b1 = __hsub2(*reinterpret_cast<const __half2*>(&h1), offset);
+              const int i = 4 * q4 + 2 * pair + e;
+#pragma unroll
+              for (int m = 0; m < MT; ++m)
+                mma_f16(acc[m][i], pw[m], *reinterpret_cast<const uint32_t*>(&b0),
+                        *reinterpret_cast<const uint32_t*>(&b1));
+            }
+          }
+        }
+      }
+      __syncwarp();  // the stage has been read by every lane
+      issue(t + ST, st);
+      if (++st == ST) st = 0;
+    }
+    if (!ok) {
+      // a wait ran out: every copy already issued lands before the shared memory is used otherwise
+      bad |= CA_TIMEOUT;
+      for (int i = 0; i < ST; ++i)
+        if (live >> i & 1) {
+          mbar_wait_bounded(full + i, phases >> i & 1, nullptr, CA_TIMEOUT_NS);
+          phases ^= 1u << i;
+        }
+    }
+
+    // ---- the four warps joined through the idle ring: 2, 3 into 0, 1, then 1 into 0
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        l[m][half] += __shfl_xor_sync(0xFFFFFFFFu, l[m][half], 1);
+        l[m][half] += __shfl_xor_sync(0xFFFFFFFFu, l[m][half], 2);
+        const float by = inv[m][half] == 0.0f ? 0.0f : 1.0f / inv[m][half];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          acc[m][i][2 * half] *= by;
+          acc[m][i][2 * half + 1] *= by;
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int step = 2; step > 0; step >>= 1) {
+      // warps 2 and 3 use areas 0 and 1; warp 1, which has then read area 1, uses it again
+      if (warp >= step && warp < 2 * step) {
+        float4* to = reinterpret_cast<float4*>(smem + (warp == 2 ? 0 : Shape::kJoinWarp));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            to[(m * 16 + i) * 32 + lane] = make_float4(acc[m][i][0], acc[m][i][1], acc[m][i][2], acc[m][i][3]);
+          to[MT * 512 + m * 32 + lane] = make_float4(mx[m][0], mx[m][1], l[m][0], l[m][1]);
+        }
+      }
+      __syncthreads();
+      if (warp < step) {
+        const float4* from =
+            reinterpret_cast<const float4*>(smem + (step == 2 && warp == 0 ? 0 : Shape::kJoinWarp));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const float4 other = from[MT * 512 + m * 32 + lane];
+          float fa[2], fb[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float mx_b = half ? other.y : other.x, l_b = half ? other.w : other.z;
+            const float now = fmaxf(mx[m][half], mx_b);
+            fa[half] = mx[m][half] == now ? 1.0f : ex2_approx(mx[m][half] - now);
+            fb[half] = mx_b == now ? 1.0f : ex2_approx(mx_b - now);
+            mx[m][half] = now;
+            l[m][half] = l[m][half] * fa[half] + l_b * fb[half];
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float4 o = from[(m * 16 + i) * 32 + lane];
+            acc[m][i][0] = acc[m][i][0] * fa[0] + o.x * fb[0];
+            acc[m][i][1] = acc[m][i][1] * fa[0] + o.y * fb[0];
+            acc[m][i][2] = acc[m][i][2] * fa[1] + o.z * fb[1];
+            acc[m][i][3] = acc[m][i][3] * fa[1] + o.w * fb[1];
+          }
+        }
+      }
+    }
+    fence_proxy_async_smem();  // the next run's copies write where these exchanges were
+    __syncthreads();
+    const bool whole = r.t0 == 0 && r.t1 == walk.s.tiles;
+    if (r.t0 == 0 && !whole) {
+      // the piece ends inside an item that begins in it: it describes the item to the join
+      const int64_t item_end = walk.end - r.t1 + walk.s.tiles;  // one past the item's last tile
+      cut.pieces = static_cast<int>((item_end - 1) / per) - static_cast<int>(blockIdx.x) + 1;
+      cut.rows = r.rows;
+      cut.row0 = r.row0;
+      cut.head = r.head;
+      cut.token0 = walk.s.first;
+    }
+    if (warp == 0) {
+      const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (r.t0 == 0 ? 1 : 0);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int row = m * 16 + 8 * half + g;
+          // the thread's channels 32 t4 + i and 32 t4 + 16 + i
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            v[i] = acc[m][i][2 * half];
+            v[16 + i] = acc[m][i][2 * half + 1];
+          }
+          if (whole) {
+            const float norm = l[m][half] > 0.0f ? fwht::kInvSqrt128 / l[m][half] : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= norm;
+            fwht::reg_stage<32, 1>(v);
+            fwht::reg_stage<32, 2>(v);
+            fwht::reg_stage<32, 4>(v);
+            fwht::reg_stage<32, 8>(v);
+            fwht::reg_stage<32, 16>(v);
+            fwht::lane_stage(v, 1, (t4 & 1) != 0);
+            fwht::lane_stage(v, 2, (t4 & 2) != 0);
+            if (row < r.rows) {
+              const int of = r.row0 + row, i = of / p.G;
+              uint16_t* dst = p.o + (walk.s.first + i) * p.ot + (r.head * p.G + (of - i * p.G)) * p.oh + 32 * t4;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(
+                    fwht::narrow_pair<F16>(v[8 * c], v[8 * c + 1]), fwht::narrow_pair<F16>(v[8 * c + 2], v[8 * c + 3]),
+                    fwht::narrow_pair<F16>(v[8 * c + 4], v[8 * c + 5]),
+                    fwht::narrow_pair<F16>(v[8 * c + 6], v[8 * c + 7]));
+            }
+          } else if (row < r.rows) {
+            float4* dst = reinterpret_cast<float4*>(p.part + (slot * ROWS + row) * CA_D + 32 * t4);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            if (t4 == 0) p.part_ml[slot * ROWS + row] = make_float2(mx[m][half], l[m][half]);
+          }
+        }
+      }
+    }
+  }
+  if (tid == 0) p.cuts[blockIdx.x] = cut;
+  const int any_bad = __syncthreads_or(bad & CA_BAD), any_late = __syncthreads_or(bad & 4);
+  if (tid == 0) p.piece_status[blockIdx.x] = any_late ? CA_TIMEOUT : any_bad ? CA_BAD : 0;
+}
+
+// Joins the parts of the items that were cut: one CTA per (piece, row). The
+// piece in which the item begins describes it.
+constexpr int kJoinThreads = 128;
+
+template <bool F16>
+__global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(const CaParams p, int rows) {
+  __shared__ float weight[CA_MAX_WORKERS];
+  __shared__ float red[2][kJoinThreads / 32];
+  __shared__ float4 partial[kJoinThreads / 32][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_wait();
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    int st = 0;
+    for (int i = tid; i < p.workers; i += kJoinThreads) st |= p.piece_status[i];
+    const int any_bad = __syncthreads_or(st & CA_BAD), any_late = __syncthreads_or(st & 4);
+    if (tid == 0) *p.status = any_late ? CA_TIMEOUT : any_bad ? CA_BAD : 0;
+  }
+  const CaCut cut = p.cuts[blockIdx.x];
+  const int row = blockIdx.y;
+  if (row >= cut.rows || cut.pieces < 1) return;
+  // piece 0 of the item is slot 2 c + 1, the k-th after it slot 2 (c + k)
+  auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(blockIdx.x) + 1 : 2 * (static_cast<int64_t>(blockIdx.x) + k); };
+  float top = -INFINITY;
+  for (int k = tid; k < cut.pieces; k += kJoinThreads) top = fmaxf(top, p.part_ml[slot(k) * rows + row].x);
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+  if (lane == 0) red[0][warp] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  float sum = 0.0f;
+  for (int k = tid; k < cut.pieces; k += kJoinThreads) {
+    const float2 ml = p.part_ml[slot(k) * rows + row];
+    const float w = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - top);
+    weight[k] = w;
+    sum += w * ml.y;
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+  if (lane == 0) red[1][warp] = sum;
+  __syncthreads();
+  sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int k = warp; k < cut.pieces; k += kJoinThreads / 32) {
+    const float4 o = *reinterpret_cast<const float4*>(p.part + (slot(k) * rows + row) * CA_D + 4 * lane);
+    const float w = weight[k];
+    a.x = fmaf(w, o.x, a.x), a.y = fmaf(w, o.y, a.y), a.z = fmaf(w, o.z, a.z), a.w = fmaf(w, o.w, a.w);
+  }
+  partial[warp][lane] = a;
+  __syncthreads();
+  if (warp != 0) return;
+  const float norm = sum > 0.0f ? fwht::kInvSqrt128 / sum : 0.0f;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 32; ++w) {
+    const float4 o = partial[w][lane];
+    v[0] += o.x, v[1] += o.y, v[2] += o.z, v[3] += o.w;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] *= norm;
+  fwht::fwht128_warp(v, lane);
+  const int of = cut.row0 + row, i = of / p.G;
+  uint16_t* dst = p.o + (cut.token0 + i) * p.ot + (cut.head * p.G + (of - i * p.G)) * p.oh + 4 * lane;
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2(fwht::narrow_pair<F16>(v[0], v[1]), fwht::narrow_pair<F16>(v[2], v[3]));
+}
+
+// ------------------------------------------------------------------------ host
+
+struct CaLayout {
+  size_t status, cuts, ml, part, total;
+};
+
+template <class Shape>
+CaLayout ca_layout() {
+  CaLayout w;
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  w.status = 256;
+  w.cuts = up(w.status + CA_MAX_WORKERS * sizeof(int));
+  w.ml = up(w.cuts + CA_MAX_WORKERS * sizeof(CaCut));
+  w.part = up(w.ml + 2 * static_cast<size_t>(CA_MAX_WORKERS) * Shape::kRows * sizeof(float2));
+  w.total = up(w.part + 2 * static_cast<size_t>(CA_MAX_WORKERS) * Shape::kRows * CA_D * sizeof(float));
+  return w;
+}
+
+// The tile of rows by the mean number of rows a sequence has: a wider tile
+// re-reads the keys for fewer tiles, a narrower one wastes fewer rows of the
+// matrix instructions and leaves more CTAs per SM to hide the loads.
+bool ca_wide(int64_t T, int64_t B, int64_t G) { return T * G > 16 * B; }
+
+bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+  return D == CA_D && T >= 0 && B >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hkv <= CONVROT_MAX_CACHE_HEADS &&
+         Hq / Hkv <= CONVROT_MAX_CACHE_HEADS && B <= (int64_t{1} << 24) && T <= (int64_t{1} << 20);
+}
+
+template <class Shape, bool F16>
+cudaError_t ca_launch(const CUtensorMap& tk, const CUtensorMap& tv, CaParams p, uint8_t* ws, int64_t most_rows,
+                      cudaStream_t s) {
+  static std::atomic<int> ready[64];  // SMs of a device whose attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < 64;
+  int sms = known ? ready[dev].load(std::memory_order_acquire) : 0;
+  if (sms == 0) {
+    e = cudaFuncSetAttribute(cache_attention_kernel<Shape, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Shape::kAlloc);
+    if (e != cudaSuccess) return e;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (known) ready[dev].store(sms, std::memory_order_release);
+  }
+  const CaLayout lay = ca_layout<Shape>();
+  p.workers = sms * Shape::kOcc < CA_MAX_WORKERS ? sms * Shape::kOcc : CA_MAX_WORKERS;
+  p.status = reinterpret_cast<int*>(ws);
+  p.piece_status = reinterpret_cast<int*>(ws + lay.status);
+  p.cuts = reinterpret_cast<CaCut*>(ws + lay.cuts);
+  p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
+  p.part = reinterpret_cast<float*>(ws + lay.part);
+  cache_attention_kernel<Shape, F16><<<p.workers, CA_THREADS, Shape::kAlloc, s>>>(tk, tv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.workers, static_cast<unsigned>(most_rows < Shape::kRows ? most_rows : Shape::kRows));
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<F16>, p, static_cast<int>(Shape::kRows));
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 ca_encoder() {
+  static std::atomic<void*> fn{nullptr};
+  void* f = fn.load(std::memory_order_acquire);
+  if (f == nullptr) {
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    fn.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+}
+
+// Codes as rows of 128 bytes, boxes of a warp's 16 keys, 128-byte swizzle.
+bool ca_encode(CUtensorMap* tm, const int8_t* codes, int64_t cells) {
+  const auto enc = ca_encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t dims[2] = {CA_D, static_cast<cuuint64_t>(cells)};
+  const cuuint64_t strides[1] = {CA_D};
+  const cuuint32_t size[2] = {CA_D, CA_SUB};
+  const cuuint32_t step[2] = {1, 1};
+  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(codes), dims, strides, size, step,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+}  // namespace convrot
+
+extern "C" {
+
+size_t convrot_cache_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+  using namespace convrot;
+  if (!ca_sizes_ok(T, B, Hq, Hkv, D)) return 0;
+  if (T == 0 || B == 0) return 256;
+  return ca_wide(T, B, Hq / Hkv) ? ca_layout<Shape32>().total : ca_layout<Shape16>().total;
+}
+
+convrot_status convrot_cache_attention(const void* Q, int dtype, int64_t T, int64_t Hq, int64_t D, int64_t q_token,
+                                       int64_t q_head, const int8_t* k_codes, const int8_t* v_codes,
+                                       const float* k_scale, const float* v_scale, int64_t num_pages,
+                                       int64_t page_size, int64_t Hkv, const int32_t* pages, int64_t B,
+                                       int64_t table_pages, int64_t table_stride, const int32_t* lengths,
+                                       const int32_t* starts, const int64_t* tree, float softmax_scale, void* O,
+                                       int64_t o_token, int64_t o_head, void* ws, size_t ws_bytes,
+                                       convrot_stream_t stream) {
+  using namespace convrot;
+  if (dtype != CONVROT_DTYPE_BF16 && dtype != CONVROT_DTYPE_F16) return CONVROT_ERR_UNSUPPORTED;
+  if (D != CA_D) return CONVROT_ERR_UNSUPPORTED;
+  if (T < 0 || B < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || num_pages < 1 || page_size < 1 || table_pages < 0 ||
+      table_stride < 0)
+    return CONVROT_ERR_INVALID_ARG;
+  if (page_size < CONVROT_MIN_PAGE || page_size > CONVROT_MAX_PAGE || (page_size & (page_size - 1)) != 0)
+    return CONVROT_ERR_UNSUPPORTED;
+  if (!ca_sizes_ok(T, B, Hq, Hkv, D) || num_pages > 0x7FFFFFFF / page_size / Hkv ||
+      table_pages > 0x7FFFF000 / page_size)
+    return CONVROT_ERR_UNSUPPORTED;
+  if (starts == nullptr && T != B) return CONVROT_ERR_INVALID_ARG;
+  if (!(softmax_scale > 0.0f) || !(softmax_scale < 3.0e38f)) return CONVROT_ERR_INVALID_ARG;
+  if (q_token % 8 != 0 || q_head % 8 != 0 || o_token % 8 != 0 || o_head % 8 != 0) return CONVROT_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return CONVROT_OK;  // no queries
+  auto aligned = [](const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; };
+  if (Q == nullptr || O == nullptr || k_codes == nullptr || v_codes == nullptr || k_scale == nullptr ||
+      v_scale == nullptr || lengths == nullptr || (pages == nullptr && table_pages > 0))
+    return CONVROT_ERR_INVALID_ARG;
+  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 16) ||
+      !aligned(v_scale, 16) || !aligned(pages, 4) || !aligned(lengths, 4) || !aligned(starts, 4) || !aligned(tree, 8))
+    return CONVROT_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D))
+    return CONVROT_ERR_WORKSPACE;
+  CaParams p{};
+  p.q = static_cast<const uint16_t*>(Q);
+  p.o = static_cast<uint16_t*>(O);
+  p.qt = q_token, p.qh = q_head, p.ot = o_token, p.oh = o_head;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.pages = pages;
+  p.lengths = lengths;
+  p.starts = starts;
+  p.tree = reinterpret_cast<const unsigned long long*>(tree);
+  p.table_stride = table_stride;
+  p.T = static_cast<int>(T);
+  p.B = static_cast<int>(B);
+  p.Hkv = static_cast<int>(Hkv);
+  p.G = static_cast<int>(Hq / Hkv);
+  p.table_pages = static_cast<int>(table_pages);
+  p.num_pages = static_cast<int>(num_pages);
+  while ((int64_t{1} << p.page_shift) < page_size) ++p.page_shift;
+  p.c_scale = softmax_scale * 1.4426950408889634f;
+  CUtensorMap tk, tv;
+  if (!ca_encode(&tk, k_codes, num_pages * Hkv * page_size) || !ca_encode(&tv, v_codes, num_pages * Hkv * page_size))
+    return CONVROT_ERR_INVALID_ARG;
+  // rows a tile can have at most: all of one sequence's
+  const int64_t rows = (starts == nullptr ? 1 : T) * (Hq / Hkv);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool f16 = dtype == CONVROT_DTYPE_F16;
+  cudaError_t e;
+  if (ca_wide(T, B, Hq / Hkv))
+    e = f16 ? ca_launch<Shape32, true>(tk, tv, p, w, rows, s) : ca_launch<Shape32, false>(tk, tv, p, w, rows, s);
+  else
+    e = f16 ? ca_launch<Shape16, true>(tk, tv, p, w, rows, s) : ca_launch<Shape16, false>(tk, tv, p, w, rows, s);
+  return e == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -474,7 +474,9 @@ convrot_status convrot_read_device_status(const void* ws, convrot_stream_t strea
   if (cudaMemcpyAsync(&host, ws, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess) return CONVROT_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return CONVROT_ERR_CUDA;
   if (host == 0) return CONVROT_OK;
-  return host == CONVROT_ERR_DEVICE_TIMEOUT ? CONVROT_ERR_DEVICE_TIMEOUT : CONVROT_ERR_CUDA;
+  // convrot_cache_attention also reports what it found wrong in its device-side arguments
+  return host == CONVROT_ERR_DEVICE_TIMEOUT || host == CONVROT_ERR_INVALID_ARG ? static_cast<convrot_status>(host)
+                                                                              : CONVROT_ERR_CUDA;
 }
 
 convrot_status convrot_test_wait_timeout(void* ws, size_t ws_bytes, int64_t timeout_ns, convrot_stream_t stream) {

@@ -1,0 +1,242 @@
+// Rotary positions with several axes: pairs of channels of every head vector
+// turned by the angle pos[axis(i)] * freq(i) of pair i.
+//
+//   (y1, y2) = (x1 cos - x2 sin, x2 cos + x1 sin),
+//
+// the pair being channels (i, i + R/2) or, interleaved, (2i, 2i + 1); channels
+// from R on are copied. The inverse turns by -angle: the transpose of the
+// rotation, so it is also the gradient. The angle is a float64 product reduced
+// to one turn before anything is rounded to float32 (positions in the 100000s
+// would otherwise lose the angle's fraction); sine, cosine and the two products
+// are float32 and the output is rounded once.
+//
+// Bound by memory: 2 bytes read and 2 written per channel. A CTA owns a few
+// tokens; hp x (D/16) threads share a token, and a thread keeps the same eight
+// pairs for every head it visits, so their sines and cosines are read from
+// shared memory once. The first four heads' loads are issued before the angles
+// are computed.
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "convrot.h"
+#include "fwht128.cuh"
+
+namespace convrot {
+
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeAhead = 4;         // heads whose loads a thread has in flight
+constexpr int kRopeMaxDim = 512;
+constexpr int kRopeTableMax = 2048;   // sine/cosine pairs a CTA holds (16 KB)
+
+struct RopeParams {
+  const uint16_t* x;
+  uint16_t* y;
+  int64_t tokens;            // B * S
+  int S, H, D, R;
+  int64_t xb, xs, xh, yb, ys, yh;
+  const void* pos;
+  int pos_float, axes;
+  int64_t pa, pb, ps;
+  const double* freq;
+  const int32_t* axis;
+  int interleaved, inverse;
+  int hp;                    // heads a token's threads visit at once
+  int tok;                   // tokens of a CTA
+};
+
+// (cos, sin) of pair i at token n; a pair whose axis is out of [0, axes) is not turned.
+__device__ __forceinline__ float2 rope_turn(const RopeParams& p, int64_t n, int i) {
+  const int a = __ldg(p.axis + i);
+  if (a < 0 || a >= p.axes) return make_float2(1.0f, 0.0f);
+  const uint32_t b = static_cast<uint32_t>(n) / static_cast<uint32_t>(p.S);  // tokens < 2^31
+  const int64_t at = a * p.pa + b * p.pb + (n - static_cast<int64_t>(b) * p.S) * p.ps;
+  const double pos = p.pos_float ? static_cast<double>(__ldg(static_cast<const float*>(p.pos) + at))
+                                 : static_cast<double>(__ldg(static_cast<const int32_t*>(p.pos) + at));
+  const double turns = pos * (__ldg(p.freq + i) * 0.15915494309189533577);
+  const float r = static_cast<float>(turns - rint(turns));
+  float s, c;
+  sincospif(2.0f * r, &s, &c);
+  return make_float2(c, p.inverse ? -s : s);
+}
+
+// Sixteen channels of a head: the two runs of eight that hold pairs 8c .. 8c + 7.
+template <bool F16, bool INTER>
+__device__ __forceinline__ void rope_apply(uint4& lo, uint4& hi, const float2 (&cs)[8]) {
+  uint32_t* a = reinterpret_cast<uint32_t*>(&lo);
+  uint32_t* b = reinterpret_cast<uint32_t*>(&hi);
+  if (INTER) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = fwht::widen_pair<F16>(a[i]), v = fwht::widen_pair<F16>(b[i]);
+      a[i] = fwht::narrow_pair<F16>(fmaf(u.x, cs[i].x, -u.y * cs[i].y), fmaf(u.y, cs[i].x, u.x * cs[i].y));
+      b[i] = fwht::narrow_pair<F16>(fmaf(v.x, cs[4 + i].x, -v.y * cs[4 + i].y), fmaf(v.y, cs[4 + i].x, v.x * cs[4 + i].y));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = fwht::widen_pair<F16>(a[i]), v = fwht::widen_pair<F16>(b[i]);
+      const float2 c0 = cs[2 * i], c1 = cs[2 * i + 1];
+      a[i] = fwht::narrow_pair<F16>(fmaf(u.x, c0.x, -v.x * c0.y), fmaf(u.y, c1.x, -v.y * c1.y));
+      b[i] = fwht::narrow_pair<F16>(fmaf(v.x, c0.x, u.x * c0.y), fmaf(v.y, c1.x, u.y * c1.y));
+    }
+  }
+}
+
+// Sixteen-byte accesses: D and R multiples of 16, pointers and strides of 16 bytes.
+template <bool F16, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+  __shared__ float2 table[kRopeTableMax];
+  const int per_head = p.D >> 4, pairs = p.R >> 1;
+  const int group = p.hp * per_head;  // threads of a token
+  const int slot = threadIdx.x / group, q = threadIdx.x - slot * group;
+  const int h0 = q / per_head, c = q - h0 * per_head;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tok;
+  const int64_t n = first + slot;
+  const bool mine = slot < p.tok && n < p.tokens;
+  const bool turned = 8 * c < pairs;
+  // channels of the thread's two runs of eight
+  const int d_lo = !turned ? 16 * c : INTER ? 16 * c : 8 * c;
+  const int d_hi = !turned || INTER ? d_lo + 8 : pairs + 8 * c;
+  const int64_t b = mine ? static_cast<uint32_t>(n) / static_cast<uint32_t>(p.S) : 0, s = mine ? n - b * p.S : 0;
+  const uint16_t* x = p.x + b * p.xb + s * p.xs;
+  uint16_t* y = p.y + b * p.yb + s * p.ys;
+
+  uint4 lo[kRopeAhead], hi[kRopeAhead];
+#pragma unroll
+  for (int k = 0; k < kRopeAhead; ++k) {
+    const int h = h0 + k * p.hp;
+    if (mine && h < p.H) {
+      lo[k] = *reinterpret_cast<const uint4*>(x + h * p.xh + d_lo);
+      hi[k] = *reinterpret_cast<const uint4*>(x + h * p.xh + d_hi);
+    }
+  }
+  for (int i = threadIdx.x; i < p.tok * pairs; i += kRopeThreads) {
+    const int64_t at = first + i / pairs;
+    if (at < p.tokens) table[i] = rope_turn(p, at, i % pairs);
+  }
+  __syncthreads();
+  if (!mine) return;
+  float2 cs[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cs[i] = turned ? table[slot * pairs + 8 * c + i] : make_float2(1.0f, 0.0f);
+  for (int hb = h0; hb < p.H; hb += kRopeAhead * p.hp) {
+#pragma unroll
+    for (int k = 0; k < kRopeAhead; ++k) {
+      const int h = hb + k * p.hp;
+      if (h < p.H) {
+        if (turned) rope_apply<F16, INTER>(lo[k], hi[k], cs);
+        *reinterpret_cast<uint4*>(y + h * p.yh + d_lo) = lo[k];
+        *reinterpret_cast<uint4*>(y + h * p.yh + d_hi) = hi[k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRopeAhead; ++k) {
+      const int h = hb + (kRopeAhead + k) * p.hp;
+      if (h < p.H) {
+        lo[k] = *reinterpret_cast<const uint4*>(x + h * p.xh + d_lo);
+        hi[k] = *reinterpret_cast<const uint4*>(x + h * p.xh + d_hi);
+      }
+    }
+  }
+}
+
+// Any even R, any strides and alignment of 2 bytes: one CTA per token, one pair
+// (or one copied channel) per thread and step.
+template <bool F16>
+__global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(const RopeParams p) {
+  __shared__ float2 table[kRopeMaxDim / 2];
+  const int pairs = p.R >> 1, steps = p.D - pairs;  // pairs, then the channels that are copied
+  const int64_t n = blockIdx.x, b = n / p.S, s = n - b * p.S;
+  const uint16_t* x = p.x + b * p.xb + s * p.xs;
+  uint16_t* y = p.y + b * p.yb + s * p.ys;
+  for (int i = threadIdx.x; i < pairs; i += kRopeThreads) table[i] = rope_turn(p, n, i);
+  __syncthreads();
+  const int64_t work = static_cast<int64_t>(p.H) * steps;
+  for (int64_t w = threadIdx.x; w < work; w += kRopeThreads) {
+    const int64_t h = w / steps;
+    const int i = static_cast<int>(w - h * steps);
+    if (i < pairs) {
+      const int d1 = p.interleaved ? 2 * i : i, d2 = p.interleaved ? 2 * i + 1 : i + pairs;
+      const float2 u = fwht::widen_pair<F16>(x[h * p.xh + d1] | static_cast<uint32_t>(x[h * p.xh + d2]) << 16);
+      const float2 cs = table[i];
+      const uint32_t o = fwht::narrow_pair<F16>(fmaf(u.x, cs.x, -u.y * cs.y), fmaf(u.y, cs.x, u.x * cs.y));
+      y[h * p.yh + d1] = static_cast<uint16_t>(o);
+      y[h * p.yh + d2] = static_cast<uint16_t>(o >> 16);
+    } else {
+      y[h * p.yh + pairs + i] = x[h * p.xh + pairs + i];
+    }
+  }
+}
+
+}  // namespace
+
+}  // namespace convrot
+
+extern "C" {
+
+convrot_status convrot_rope(const void* X, int dtype, int64_t B, int64_t S, int64_t H, int64_t D, int64_t R,
+                            int64_t x_batch, int64_t x_token, int64_t x_head, const void* positions, int pos_dtype,
+                            int64_t axes, int64_t pos_axis, int64_t pos_batch, int64_t pos_token, const double* freq,
+                            const int32_t* axis, int interleaved, int inverse, void* Y, int64_t y_batch,
+                            int64_t y_token, int64_t y_head, convrot_stream_t stream) {
+  using namespace convrot;
+  if (dtype != CONVROT_DTYPE_BF16 && dtype != CONVROT_DTYPE_F16) return CONVROT_ERR_UNSUPPORTED;
+  if (pos_dtype != CONVROT_POS_I32 && pos_dtype != CONVROT_POS_F32) return CONVROT_ERR_UNSUPPORTED;
+  if (B < 0 || S < 0 || H < 1 || D < 1 || R < 0 || R > D || R % 2 != 0 || axes < 1) return CONVROT_ERR_INVALID_ARG;
+  if (D > kRopeMaxDim || H > 65535 || B > 0x7FFFFFFF || S > 0x7FFFFFFF || (S > 0 && B > 0x7FFFFFFF / S))
+    return CONVROT_ERR_UNSUPPORTED;
+  if (axes > 0x7FFFFFFF) return CONVROT_ERR_UNSUPPORTED;
+  if (B == 0 || S == 0) return CONVROT_OK;  // no tokens
+  if (X == nullptr || Y == nullptr || (R > 0 && (positions == nullptr || freq == nullptr || axis == nullptr)))
+    return CONVROT_ERR_INVALID_ARG;
+  auto aligned = [](const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; };
+  if (!aligned(X, 2) || !aligned(Y, 2) || !aligned(positions, 4) || !aligned(freq, 8) || !aligned(axis, 4))
+    return CONVROT_ERR_INVALID_ARG;
+  RopeParams p{};
+  p.x = static_cast<const uint16_t*>(X);
+  p.y = static_cast<uint16_t*>(Y);
+  p.tokens = B * S;
+  p.S = static_cast<int>(S);
+  p.H = static_cast<int>(H);
+  p.D = static_cast<int>(D);
+  p.R = static_cast<int>(R);
+  p.xb = x_batch, p.xs = x_token, p.xh = x_head;
+  p.yb = y_batch, p.ys = y_token, p.yh = y_head;
+  p.pos = positions;
+  p.pos_float = pos_dtype == CONVROT_POS_F32;
+  p.axes = static_cast<int>(axes);
+  p.pa = pos_axis, p.pb = pos_batch, p.ps = pos_token;
+  p.freq = freq;
+  p.axis = axis;
+  p.interleaved = interleaved != 0;
+  p.inverse = inverse != 0;
+  const bool f16 = dtype == CONVROT_DTYPE_F16;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t odd = x_batch | x_token | x_head | y_batch | y_token | y_head;
+  if (D % 16 != 0 || R % 16 != 0 || odd % 8 != 0 || !aligned(X, 16) || !aligned(Y, 16)) {
+    (f16 ? rope_scalar_kernel<true> : rope_scalar_kernel<false>)<<<static_cast<unsigned>(p.tokens), kRopeThreads, 0,
+                                                                    s>>>(p);
+    return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
+  }
+  // A quarter of the heads at once gives each thread kRopeAhead loads in flight;
+  // few tokens take all threads for each, since only latency counts.
+  const int per_head = p.D / 16, most = kRopeThreads / per_head;
+  const bool few = p.tokens <= 1024;
+  p.hp = few ? p.H : (p.H + kRopeAhead - 1) / kRopeAhead;
+  if (p.hp > most) p.hp = most;
+  p.tok = kRopeThreads / (p.hp * per_head);
+  if (R > 0 && p.tok > kRopeTableMax / (p.R / 2)) p.tok = kRopeTableMax / (p.R / 2);
+  if (few && p.tok > (p.tokens + 147) / 148) p.tok = static_cast<int>((p.tokens + 147) / 148);
+  const unsigned grid = static_cast<unsigned>((p.tokens + p.tok - 1) / p.tok);
+  if (p.interleaved)
+    (f16 ? rope_kernel<true, true> : rope_kernel<false, true>)<<<grid, kRopeThreads, 0, s>>>(p);
+  else
+    (f16 ? rope_kernel<true, false> : rope_kernel<false, false>)<<<grid, kRopeThreads, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
+}
+
+}  // extern "C"
