@@ -406,15 +406,23 @@ CONVROT_API convrot_status convrot_attention_int8(const void* Q, const void* K, 
  *             formed and reduced in double.
  *   axis      [R/2] int32, device: the axis of each pair; a pair whose axis is
  *             outside [0, axes) is not turned.
- * One kernel launch.
+ * One kernel launch. The call reads *args before it returns. The stride of a
+ * dimension of one element is not looked at, here and in the calls below.
  */
 typedef enum { CONVROT_POS_I32 = 0, CONVROT_POS_F32 = 1 } convrot_pos_dtype;
-CONVROT_API convrot_status convrot_rope(const void* X, int dtype, int64_t B, int64_t S, int64_t H, int64_t D,
-                                        int64_t R, int64_t x_batch, int64_t x_token, int64_t x_head,
-                                        const void* positions, int pos_dtype, int64_t axes, int64_t pos_axis,
-                                        int64_t pos_batch, int64_t pos_token, const double* freq,
-                                        const int32_t* axis, int interleaved, int inverse, void* Y,
-                                        int64_t y_batch, int64_t y_token, int64_t y_head, convrot_stream_t stream);
+typedef struct {
+  const void* X;
+  void* Y;
+  const void* positions;
+  const double* freq;
+  const int32_t* axis;
+  int64_t B, S, H, D, R;
+  int64_t x_batch, x_token, x_head;
+  int64_t y_batch, y_token, y_head;
+  int64_t axes, pos_axis, pos_batch, pos_token;
+  int dtype, pos_dtype, interleaved, inverse;
+} convrot_rope_args;
+CONVROT_API convrot_status convrot_rope(const convrot_rope_args* args, convrot_stream_t stream);
 
 /*
  * The rotated int8 key/value cache. A cell holds one token of one key/value
@@ -447,16 +455,25 @@ CONVROT_API convrot_status convrot_rope(const void* X, int dtype, int64_t B, int
 #define CONVROT_MIN_PAGE 16
 #define CONVROT_MAX_PAGE 1024
 #define CONVROT_MAX_CACHE_HEADS 1024
-CONVROT_API convrot_status convrot_cache_append(const void* K, const void* V, int dtype, int64_t T, int64_t H,
-                                                int64_t D, int64_t k_token, int64_t k_head, int64_t v_token,
-                                                int64_t v_head, const int32_t* slots, int8_t* k_codes,
-                                                int8_t* v_codes, float* k_scale, float* v_scale, int64_t num_pages,
-                                                int64_t page_size, int* status, convrot_stream_t stream);
-CONVROT_API convrot_status convrot_cache_read(const int32_t* slots, int64_t T, int64_t H, int64_t D,
-                                              const int8_t* k_codes, const int8_t* v_codes, const float* k_scale,
-                                              const float* v_scale, int64_t num_pages, int64_t page_size, void* K,
-                                              void* V, int dtype, int64_t k_token, int64_t k_head, int64_t v_token,
-                                              int64_t v_head, int* status, convrot_stream_t stream);
+typedef struct {
+  int8_t* k_codes;
+  int8_t* v_codes;
+  float* k_scale;
+  float* v_scale;
+  int64_t num_pages, H, page_size, D;
+} convrot_cells;
+typedef struct {
+  convrot_cells cells;
+  void* K;                /* read by convrot_cache_append, written by convrot_cache_read */
+  void* V;
+  const int32_t* slots;
+  int* status;
+  int64_t T;
+  int64_t k_token, k_head, v_token, v_head;
+  int dtype;
+} convrot_cache_args;
+CONVROT_API convrot_status convrot_cache_append(const convrot_cache_args* args, convrot_stream_t stream);
+CONVROT_API convrot_status convrot_cache_read(const convrot_cache_args* args, convrot_stream_t stream);
 
 /*
  * convrot_cache_attention -- attention of the newest tokens of B sequences over
@@ -500,12 +517,24 @@ CONVROT_API convrot_status convrot_cache_read(const int32_t* slots, int64_t T, i
  * follows from the lengths, and the result does not depend on timing.
  */
 CONVROT_API size_t convrot_cache_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
-CONVROT_API convrot_status convrot_cache_attention(
-    const void* Q, int dtype, int64_t T, int64_t Hq, int64_t D, int64_t q_token, int64_t q_head,
-    const int8_t* k_codes, const int8_t* v_codes, const float* k_scale, const float* v_scale, int64_t num_pages,
-    int64_t page_size, int64_t Hkv, const int32_t* pages, int64_t B, int64_t table_pages, int64_t table_stride,
-    const int32_t* lengths, const int32_t* starts, const int64_t* tree, float softmax_scale, void* O,
-    int64_t o_token, int64_t o_head, void* ws, size_t ws_bytes, convrot_stream_t stream);
+typedef struct {
+  convrot_cells cells;    /* H: key/value heads (Hkv above) */
+  const void* Q;
+  void* O;
+  const int32_t* pages;
+  const int32_t* lengths;
+  const int32_t* starts;
+  const int64_t* tree;
+  void* ws;
+  size_t ws_bytes;
+  int64_t T, Hq, B;
+  int64_t table_pages, table_stride;
+  int64_t q_token, q_head, o_token, o_head;
+  float softmax_scale;
+  int dtype;
+} convrot_cache_attention_args;
+CONVROT_API convrot_status convrot_cache_attention(const convrot_cache_attention_args* args,
+                                                   convrot_stream_t stream);
 
 /*
  * convrot_probe_i8_peak -- measurement aid for the GEMM's roofline (not part

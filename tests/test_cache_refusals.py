@@ -15,62 +15,93 @@ def L():
     return _lib.load()
 
 
-def _caller(fn, names, values):
+def _caller(fn, layout, names, values):
+    """A call of `fn` with a struct of the named fields, some of them other than `values`; its status."""
     names = names.split()
-    assert len(names) == len(values) == len(fn.argtypes)
+    assert len(names) == len(values)
 
     def call(**over):
         assert set(over) <= set(names)
-        return fn(*[over.get(n, v) for n, v in zip(names, values)])
+        return fn(layout.pack(*[over.get(n, v) for n, v in zip(names, values)]), None)
 
     return call
 
 
+CELLS = "kc vc ks vs pages H page D "
+CELLS_OK = [FAKE, FAKE, FAKE, FAKE, 8, 2, 64, 128]
+
+
+def test_structs_are_laid_out_as_the_compiler_does(tmp_path):
+    import os
+    import subprocess
+
+    from w8a8_rotated_int8_token_b200 import _lib, build
+
+    ends = {"convrot_rope_args": ("inverse", _lib.ROPE_ARGS), "convrot_cache_args": ("dtype", _lib.CACHE_ARGS),
+            "convrot_cache_attention_args": ("dtype", _lib.CACHE_ATTENTION_ARGS)}
+    mids = {"convrot_rope_args": ("axes", "@5P5q6q"), "convrot_cache_args": ("T", "@4P4q4P"),
+            "convrot_cache_attention_args": ("ws_bytes", "@4P4q7P")}
+    import struct
+
+    lines = [f'printf("%zu %zu\\n", offsetof({t}, {ends[t][0]}), offsetof({t}, {mids[t][0]}));' for t in ends]
+    src = tmp_path / "layout.c"
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "convrot.h"\nint main(void) {\n' +
+                   "\n".join(lines) + "\nreturn 0;\n}\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-std=c99", "-I", os.path.join(build.ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [[int(v) for v in ln.split()] for ln in subprocess.run([str(exe)], capture_output=True, text=True,
+                                                                 check=True).stdout.splitlines()]
+    assert got == [[ends[t][1].size - 4, struct.calcsize(mids[t][1])] for t in ends]
+
+
+def test_no_arguments(L):
+    for fn in (L.convrot_rope, L.convrot_cache_append, L.convrot_cache_read, L.convrot_cache_attention):
+        assert fn(None, None) == 1
+
+
 def test_rope(L):
-    call = _caller(L.convrot_rope, "X dtype B S H D R xb xs xh pos pos_dtype axes pa pb ps freq axis inter inverse Y yb ys "
-                   "yh stream",
-                   [FAKE, 0, 1, 4, 2, 128, 128, 0, 256, 128, FAKE, 0, 3, 4, 0, 1, FAKE, FAKE, 0, 0, FAKE, 0, 256, 128,
-                    None])
+    from w8a8_rotated_int8_token_b200 import _lib
+
+    call = _caller(L.convrot_rope, _lib.ROPE_ARGS, "X Y pos freq axis B S H D R xb xs xh yb ys yh axes pa pb ps dtype "
+                   "pos_dtype inter inverse",
+                   [FAKE, FAKE, FAKE, FAKE, FAKE, 1, 4, 2, 128, 128, 0, 256, 128, 0, 256, 128, 3, 4, 0, 1, 0, 0, 0, 0])
     assert call(dtype=2) == 2 and call(pos_dtype=2) == 2
     assert call(R=127) == 1 and call(R=130) == 1 and call(R=-2) == 1
     assert call(H=0) == 1 and call(D=0, R=0) == 1 and call(B=-1) == 1 and call(S=-1) == 1 and call(axes=0) == 1
-    assert call(D=514) == 2 and call(H=65536) == 2 and call(B=1 << 20, S=1 << 12) == 2
+    assert call(D=514) == 2 and call(H=65536) == 2 and call(B=1 << 20, S=1 << 12) == 2 and call(axes=1 << 31) == 2
     for name in ("X", "Y", "pos", "freq", "axis"):
-        assert call(**{name: None}) == 1, name
+        assert call(**{name: 0}) == 1, name
     assert call(X=FAKE + 1) == 1 and call(pos=FAKE + 2) == 1 and call(freq=FAKE + 4) == 1 and call(axis=FAKE + 2) == 1
-    assert call(S=0, X=None, Y=None, pos=None) == 0 and call(B=0) == 0
+    assert call(S=0, X=0, Y=0, pos=0) == 0 and call(B=0) == 0
     assert call(S=0, R=127) == 1
 
 
-CELLS = [FAKE, FAKE, FAKE, FAKE]
-
-
 def test_append_and_read(L):
-    append = _caller(L.convrot_cache_append, "K V dtype T H D kt kh vt vh slots kc vc ks vs pages page status stream",
-                     [FAKE, FAKE, 0, 4, 2, 128, 256, 128, 256, 128, FAKE, *CELLS, 8, 64, None, None])
-    read = _caller(L.convrot_cache_read, "slots T H D kc vc ks vs pages page K V dtype kt kh vt vh status stream",
-                   [FAKE, 4, 2, 128, *CELLS, 8, 64, FAKE, FAKE, 0, 256, 128, 256, 128, None, None])
-    for call in (append, read):
+    from w8a8_rotated_int8_token_b200 import _lib
+
+    for fn in (L.convrot_cache_append, L.convrot_cache_read):
+        call = _caller(fn, _lib.CACHE_ARGS, CELLS + "K V slots status T kt kh vt vh dtype",
+                       [*CELLS_OK, FAKE, FAKE, FAKE, 0, 4, 256, 128, 256, 128, 0])
         assert call(dtype=3) == 2 and call(D=64) == 2
         assert call(page=8) == 2 and call(page=48) == 2 and call(page=2048) == 2 and call(page=0) == 1
         assert call(pages=0) == 1 and call(H=0) == 1 and call(T=-1) == 1
         assert call(H=1025) == 2 and call(pages=1 << 25) == 2 and call(T=1 << 30) == 2
         assert call(kt=4) == 1 and call(vh=12) == 1
         for name in ("K", "V", "slots", "kc", "vc", "ks", "vs"):
-            assert call(**{name: None}) == 1, name
+            assert call(**{name: 0}) == 1, name
         assert call(K=FAKE + 8) == 1 and call(slots=FAKE + 2) == 1 and call(kc=FAKE + 8) == 1 and call(vs=FAKE + 8) == 1
         assert call(status=FAKE + 2) == 1
-        assert call(T=0, K=None, V=None, slots=None) == 0 and call(T=0, D=64) == 2
+        assert call(T=0, K=0, V=0, slots=0) == 0 and call(T=0, D=64) == 2
 
 
 def test_attention(L):
-    call = _caller(L.convrot_cache_attention,
-                   "Q dtype T Hq D qt qh kc vc ks vs pages page Hkv table B cols stride lengths starts tree scale O ot oh "
-                   "ws ws_bytes stream",
-                   [FAKE, 0, 4, 8, 128, 1024, 128, *CELLS, 8, 64, 2, FAKE, 4, 3, 3, FAKE, None, None, 0.1, FAKE, 1024,
-                    128, FAKE, 1 << 30, None])
+    from w8a8_rotated_int8_token_b200 import _lib
+
+    call = _caller(L.convrot_cache_attention, _lib.CACHE_ATTENTION_ARGS,
+                   CELLS + "Q O table lengths starts tree ws ws_bytes T Hq B cols stride qt qh ot oh scale dtype",
+                   [*CELLS_OK, FAKE, FAKE, FAKE, FAKE, 0, 0, FAKE, 1 << 30, 4, 8, 4, 3, 3, 1024, 128, 1024, 128, 0.1, 0])
     assert call(dtype=2) == 2 and call(D=64) == 2
-    assert call(Hq=7) == 1 and call(Hkv=0) == 1 and call(Hq=0) == 1 and call(pages=0) == 1 and call(cols=-1) == 1
+    assert call(Hq=7) == 1 and call(H=0) == 1 and call(Hq=0) == 1 and call(pages=0) == 1 and call(cols=-1) == 1
     assert call(stride=-1) == 1 and call(page=24) == 2 and call(page=4096) == 2 and call(page=0) == 1
     assert call(T=5) == 1  # one token per sequence without starts
     assert call(T=5, starts=FAKE, B=(1 << 24) + 1) == 2 and call(T=(1 << 20) + 1, starts=FAKE) == 2
@@ -79,11 +110,11 @@ def test_attention(L):
     assert call(scale=float("nan")) == 1
     assert call(qt=1020) == 1 and call(oh=4) == 1
     for name in ("Q", "O", "kc", "vc", "ks", "vs", "lengths", "table"):
-        assert call(**{name: None}) == 1, name
+        assert call(**{name: 0}) == 1, name
     assert call(Q=FAKE + 8) == 1 and call(lengths=FAKE + 2) == 1 and call(starts=FAKE + 1) == 1
     assert call(tree=FAKE + 4) == 1
-    assert call(ws=None) == 3 and call(ws=FAKE + 16) == 3 and call(ws_bytes=4096) == 3
-    assert call(T=0, B=0, Q=None, O=None, ws=None) == 0 and call(T=0, starts=FAKE, Q=None, O=None, ws=None) == 0
+    assert call(ws=0) == 3 and call(ws=FAKE + 16) == 3 and call(ws_bytes=4096) == 3
+    assert call(T=0, B=0, Q=0, O=0, ws=0) == 0 and call(T=0, starts=FAKE, Q=0, O=0, ws=0) == 0
     assert call(T=0, B=0, Hq=7) == 1
 
 

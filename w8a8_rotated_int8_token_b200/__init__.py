@@ -408,17 +408,24 @@ def convrot_attention_int8(Q, K, V, softmax_scale=None, O=None, ws=None, stream=
     return O
 
 
-def _elsewhere(t, stream):
-    """None if a call on `t` runs where torch is: t's device current, its current stream.
-    Otherwise a context that makes it so, within which buffers are allocated for the
-    stream that uses them."""
+def _raw_stream(index: int) -> int:
+    """The current stream of a device, as convrot_stream_t (a Stream object costs ten times as much)."""
     import torch
 
-    index = t.get_device()
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _elsewhere(index: int, stream):
+    """None if a call on tensors of device `index` runs where torch is: that device current, its
+    current stream. Otherwise a context that makes it so, within which buffers are allocated
+    for the stream that uses them."""
+    import torch
+
+    here = torch.cuda.current_device() == index
     if stream is None:
-        return None if index == torch.cuda.current_device() else torch.cuda.device(index)
+        return None if here else torch.cuda.device(index)
     ptr = _stream_ptr(stream)
-    if index == torch.cuda.current_device() and ptr == _stream_ptr(None):
+    if here and ptr == _raw_stream(index):
         return None
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(ptr, device=index) if ptr else torch.cuda.default_stream(index)
@@ -427,40 +434,42 @@ def _elsewhere(t, stream):
     return torch.cuda.stream(stream)
 
 
-def _beside(t, name, like, dtype, shape):
-    """A contiguous tensor argument of the given type and shape on the device of `like`."""
+def _beside(t, name, index, dtype, shape):
+    """Checks a contiguous tensor argument of the given type and shape on device `index`."""
+    if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.get_device() != like.get_device():
+    if t.get_device() != index:
         raise ValueError(f"{name} must be on the device of the other tensors")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _heads_view(t, name, dims):
-    """The type code of bf16 or fp16 head vectors [..., heads, D] whose channels are contiguous."""
+def _head_vectors(t, name, dims=(3,)):
+    """(type code, device, shape, strides) of bf16 or fp16 head vectors [..., heads, D] on a GPU whose
+    channels are contiguous."""
     code = _dtype_code(t, name)
-    if not t.is_cuda:
+    index, shape, strides = t.get_device(), t.shape, t.stride()
+    if index < 0:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.dim() not in dims:
-        raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dims)} dimensions, got {t.dim()}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if len(shape) not in dims:
+        raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dims)} dimensions, got {len(shape)}")
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the channels of a head must be contiguous")
-    return code
+    return code, index, shape, strides
 
 
-def _strides(t):
-    """Strides in elements, 0 for a dimension of one element (there torch may hold any number)."""
-    return [st if n > 1 else 0 for n, st in zip(t.shape, t.stride())]
-
-
-def _writable(t, name):
-    """Refuses an output whose elements share addresses (an expanded dimension)."""
-    for n, st in zip(t.shape, t.stride()):
-        if n > 1 and st == 0:
-            raise ValueError(f"{name} must not be an expanded tensor")
+def _output(t, name, code, index, shape):
+    """The strides of an output that must be head vectors of this type, device and shape, each
+    element at an address of its own."""
+    code_t, index_t, shape_t, strides = _head_vectors(t, name, (len(shape),))
+    if code_t != code or index_t != index or shape_t != shape:
+        raise ValueError(f"{name} must be {tuple(shape)} in the dtype and on the device of the other tensors")
+    if 0 in strides and any(n > 1 and st == 0 for n, st in zip(shape, strides)):
+        raise ValueError(f"{name} must not be an expanded tensor")
+    return strides
 
 
 def convrot_rope_tables(sections, theta: float = 10000.0, shared: bool = False, device="cuda"):
@@ -488,58 +497,59 @@ def convrot_rope(X, positions, freq, axis, interleaved: bool = False, inverse: b
     Y = buf.transpose(-3, -2) the heads come out as convrot_attention_int8 takes them."""
     import torch
 
-    code = _heads_view(X, "X", (3, 4))
-    where = _elsewhere(X, stream)
+    code, index, shape, xs = _head_vectors(X, "X", (3, 4))
+    where = _elsewhere(index, stream)
     if where is not None:
         with where:
             return convrot_rope(X, positions, freq, axis, interleaved, inverse, Y)
-    S, H, D = X.shape[-3:]
-    B = X.shape[0] if X.dim() == 4 else 1
-    pairs = freq.shape[0] if freq.dim() == 1 else -1
-    if pairs < 0 or 2 * pairs > D:
-        raise ValueError("freq must be [pairs] with at most D / 2 pairs")
-    _beside(freq, "freq", X, torch.float64, (pairs,))
-    _beside(axis, "axis", X, torch.int32, (pairs,))
-    if positions.dtype == torch.int32:
-        pos_code = POS_I32
-    elif positions.dtype == torch.float32:
-        pos_code = POS_F32
+    if len(shape) == 4:
+        B, S, H, D = shape
     else:
-        raise TypeError(f"positions: expected int32 or float32, got {positions.dtype}")
-    if positions.get_device() != X.get_device():
+        (S, H, D), B, xs = shape, 1, (0, *xs)
+    pairs = freq.numel()
+    if 2 * pairs > D:
+        raise ValueError(f"freq holds {pairs} pairs, a head vector {D} channels")
+    _beside(freq, "freq", index, torch.float64, (pairs,))
+    _beside(axis, "axis", index, torch.int32, (pairs,))
+    ptype, pshape, ps = positions.dtype, positions.shape, positions.stride()
+    if ptype is not torch.int32 and ptype is not torch.float32:
+        raise TypeError(f"positions: expected int32 or float32, got {ptype}")
+    if positions.get_device() != index:
         raise ValueError("positions must be on the device of the other tensors")
-    if positions.dim() not in (2, 3) or positions.shape[0] < 1 or positions.shape[-1] != S or \
-            (positions.dim() == 3 and positions.shape[1] != B):
-        raise ValueError(f"positions: expected [axes, {S}] or [axes, {B}, {S}], got {tuple(positions.shape)}")
-    if Y is None:
-        Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    if len(pshape) == 2:
+        pb = 0
+    elif len(pshape) == 3 and pshape[1] == B:
+        pb = ps[1]
     else:
-        if _heads_view(Y, "Y", (X.dim(),)) != code or Y.shape != X.shape or Y.get_device() != X.get_device():
-            raise ValueError("Y must have the shape, dtype and device of X")
-        _writable(Y, "Y")
-    xs, ys, ps = _strides(X), _strides(Y), _strides(positions)
-    batched = X.dim() == 4
-    _check(lib().convrot_rope(_ptr(X), code, B, S, H, D, 2 * pairs, xs[0] if batched else 0, xs[-3], xs[-2],
-                              _ptr(positions), pos_code, positions.shape[0], ps[0], ps[1] if len(ps) == 3 else 0,
-                              ps[-1], _ptr(freq), _ptr(axis), int(interleaved), int(inverse), _ptr(Y),
-                              ys[0] if batched else 0, ys[-3], ys[-2], _stream_ptr(None)), "convrot_rope")
+        pb = None
+    if pb is None or pshape[0] < 1 or pshape[-1] != S:
+        raise ValueError(f"positions: expected [axes, {S}] or [axes, {B}, {S}], got {tuple(pshape)}")
+    if Y is None:
+        Y = X.new_empty(shape)
+        ys = (S * H * D, H * D, D)
+    else:
+        ys = _output(Y, "Y", code, index, shape)
+        ys = ys if len(ys) == 4 else (0, *ys)
+    args = _lib.ROPE_ARGS.pack(X.data_ptr(), Y.data_ptr(), positions.data_ptr(), freq.data_ptr(), axis.data_ptr(),
+                               B, S, H, D, 2 * pairs, xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], pshape[0], ps[0], pb,
+                               ps[-1], code, POS_I32 if ptype is torch.int32 else POS_F32, interleaved, inverse)
+    _check(lib().convrot_rope(args, _raw_stream(index)), "convrot_rope")
     return Y
 
 
-def _cells(like, k_codes, v_codes, k_scale, v_scale):
-    """(pages, heads, page size) of the four cache tensors, on the device of `like`."""
+def _cells(index, k_codes, v_codes, k_scale, v_scale):
+    """Pages, heads and page size of the four cache tensors on device `index`, then their addresses."""
     import torch
 
-    if k_codes.dim() != 4:
-        raise ValueError("k_codes must be [pages, heads, page size, 128]")
     shape = k_codes.shape
-    _beside(k_codes, "k_codes", like, torch.int8, shape)
-    _beside(v_codes, "v_codes", like, torch.int8, shape)
-    _beside(k_scale, "k_scale", like, torch.float32, shape[:3])
-    _beside(v_scale, "v_scale", like, torch.float32, shape[:3])
-    if shape[3] != 128:
-        raise ValueError("the cache holds head vectors of 128 channels")
-    return shape[0], shape[1], shape[2]
+    if len(shape) != 4 or shape[3] != 128:
+        raise ValueError("k_codes must be [pages, heads, page size, 128]")
+    cells = shape[:3]
+    _beside(k_codes, "k_codes", index, torch.int8, shape)
+    _beside(v_codes, "v_codes", index, torch.int8, shape)
+    _beside(k_scale, "k_scale", index, torch.float32, cells)
+    _beside(v_scale, "v_scale", index, torch.float32, cells)
+    return (k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cells, 128)
 
 
 def convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status=None, stream=None):
@@ -549,25 +559,24 @@ def convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status
     page size]. status: an int32 [1] tensor that a slot past the cache sets to 1, or None."""
     import torch
 
-    code = _heads_view(K, "K", (3,))
-    where = _elsewhere(K, stream)
+    code, index, shape, ks = _head_vectors(K, "K")
+    where = _elsewhere(index, stream)
     if where is not None:
         with where:
             return convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status)
-    if _heads_view(V, "V", (3,)) != code or V.shape != K.shape or V.get_device() != K.get_device():
+    code_v, index_v, shape_v, vs = _head_vectors(V, "V")
+    if code_v != code or index_v != index or shape_v != shape:
         raise ValueError("V must have the shape, dtype and device of K")
-    T, H, D = K.shape
-    pages, heads, page = _cells(K, k_codes, v_codes, k_scale, v_scale)
-    if heads != H:
-        raise ValueError(f"K has {H} heads, the cache {heads}")
-    _beside(slots, "slots", K, torch.int32, (T,))
+    T, H, D = shape
+    cells = _cells(index, k_codes, v_codes, k_scale, v_scale)
+    if cells[5] != H or D != 128:
+        raise ValueError(f"K has {H} heads of {D} channels, the cache {cells[5]} of 128")
+    _beside(slots, "slots", index, torch.int32, (T,))
     if status is not None:
-        _beside(status, "status", K, torch.int32, (1,))
-    kt, kh, _ = _strides(K)
-    vt, vh, _ = _strides(V)
-    _check(lib().convrot_cache_append(_ptr(K), _ptr(V), code, T, H, D, kt, kh, vt, vh, _ptr(slots), _ptr(k_codes),
-                                      _ptr(v_codes), _ptr(k_scale), _ptr(v_scale), pages, page, _ptr(status),
-                                      _stream_ptr(None)), "convrot_cache_append")
+        _beside(status, "status", index, torch.int32, (1,))
+    args = _lib.CACHE_ARGS.pack(*cells, K.data_ptr(), V.data_ptr(), slots.data_ptr(),
+                                0 if status is None else status.data_ptr(), T, ks[0], ks[1], vs[0], vs[1], code)
+    _check(lib().convrot_cache_append(args, _raw_stream(index)), "convrot_cache_append")
 
 
 def convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype=None, K=None, V=None, status=None,
@@ -576,35 +585,37 @@ def convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype=None, K=
     fp16); a negative slot reads as zeros. K, V: outputs with strided tokens and heads, or None."""
     import torch
 
-    if not slots.is_cuda:
+    index = slots.get_device()
+    if index < 0:
         raise ValueError("slots must be on a CUDA device")
-    where = _elsewhere(slots, stream)
+    where = _elsewhere(index, stream)
     if where is not None:
         with where:
             return convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype, K, V, status)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [T]")
-    T = slots.shape[0]
-    _beside(slots, "slots", slots, torch.int32, (T,))
-    pages, H, page = _cells(slots, k_codes, v_codes, k_scale, v_scale)
+    T = slots.numel()
+    _beside(slots, "slots", index, torch.int32, (T,))
+    cells = _cells(index, k_codes, v_codes, k_scale, v_scale)
+    H = cells[5]
     if dtype is None:
         dtype = K.dtype if K is not None else V.dtype if V is not None else torch.bfloat16
-    if K is None:
-        K = torch.empty((T, H, 128), dtype=dtype, device=slots.device)
-    if V is None:
-        V = torch.empty((T, H, 128), dtype=dtype, device=slots.device)
-    for t, name in ((K, "K"), (V, "V")):
-        code = _heads_view(t, name, (3,))
-        if t.dtype != dtype or t.shape != (T, H, 128) or t.get_device() != slots.get_device():
-            raise ValueError(f"{name} must be [{T}, {H}, 128] {dtype} on the device of the other tensors")
-        _writable(t, name)
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError(f"dtype: expected bfloat16 or float16, got {dtype}")
+    code = DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_F16
+    shape = (T, H, 128)
+    ks = vs = (H * 128, 128)
+    if K is not None:
+        ks = _output(K, "K", code, index, shape)
+    else:
+        K = slots.new_empty(shape, dtype=dtype)
+    if V is not None:
+        vs = _output(V, "V", code, index, shape)
+    else:
+        V = slots.new_empty(shape, dtype=dtype)
     if status is not None:
-        _beside(status, "status", slots, torch.int32, (1,))
-    kt, kh, _ = _strides(K)
-    vt, vh, _ = _strides(V)
-    _check(lib().convrot_cache_read(_ptr(slots), T, H, 128, _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
-                                    _ptr(v_scale), pages, page, _ptr(K), _ptr(V), code, kt, kh, vt, vh, _ptr(status),
-                                    _stream_ptr(None)), "convrot_cache_read")
+        _beside(status, "status", index, torch.int32, (1,))
+    args = _lib.CACHE_ARGS.pack(*cells, K.data_ptr(), V.data_ptr(), slots.data_ptr(),
+                                0 if status is None else status.data_ptr(), T, ks[0], ks[1], vs[0], vs[1], code)
+    _check(lib().convrot_cache_read(args, _raw_stream(index)), "convrot_cache_read")
     return K, V
 
 
@@ -622,52 +633,50 @@ def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, length
     See include/convrot.h."""
     import torch
 
-    code = _heads_view(Q, "Q", (3,))
-    where = _elsewhere(Q, stream)
+    code, index, shape, qs = _head_vectors(Q, "Q")
+    where = _elsewhere(index, stream)
     if where is not None:
         with where:
             return convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree,
                                            softmax_scale, O, ws)
-    T, Hq, D = Q.shape
-    num_pages, Hkv, page = _cells(Q, k_codes, v_codes, k_scale, v_scale)
-    if Hq % Hkv != 0 or Hq == 0:
-        raise ValueError(f"{Hq} query heads do not divide among {Hkv} key heads")
-    if lengths.dim() != 1:
-        raise ValueError("lengths must be [B]")
-    B = lengths.shape[0]
-    _beside(lengths, "lengths", Q, torch.int32, (B,))
-    if pages.dtype != torch.int32:
+    T, Hq, D = shape
+    cells = _cells(index, k_codes, v_codes, k_scale, v_scale)
+    Hkv = cells[5]
+    if Hkv == 0 or Hq == 0 or Hq % Hkv != 0 or D != 128:
+        raise ValueError(f"{Hq} query heads of {D} channels do not divide among {Hkv} key heads of 128")
+    B = lengths.numel()
+    _beside(lengths, "lengths", index, torch.int32, (B,))
+    if pages.dtype is not torch.int32:
         raise TypeError(f"pages: expected torch.int32, got {pages.dtype}")
-    if pages.dim() != 2 or pages.shape[0] != B or (pages.stride(1) != 1 and pages.shape[1] > 1) or \
-            pages.get_device() != Q.get_device():
+    pshape, ps = pages.shape, pages.stride()
+    if len(pshape) != 2 or pshape[0] != B or (ps[1] != 1 and pshape[1] > 1) or pages.get_device() != index:
         raise ValueError(f"pages must be [{B}, n] with contiguous rows on the device of the other tensors")
     if starts is not None:
-        _beside(starts, "starts", Q, torch.int32, (B + 1,))
+        _beside(starts, "starts", index, torch.int32, (B + 1,))
     elif T != B:
         raise ValueError("without starts Q must hold one token per sequence")
     if tree is not None:
-        _beside(tree, "tree", Q, torch.int64, (T,))
+        _beside(tree, "tree", index, torch.int64, (T,))
     if softmax_scale is None:
         softmax_scale = 0.08838834764831845  # 1 / sqrt(128)
-    if O is None:
-        O = torch.empty((T, Hq, D), dtype=Q.dtype, device=Q.device)
+    os = (Hq * D, D)
+    if O is not None:
+        os = _output(O, "O", code, index, shape)
     else:
-        if _heads_view(O, "O", (3,)) != code or O.shape != Q.shape or O.get_device() != Q.get_device():
-            raise ValueError("O must have the shape, dtype and device of Q")
-        _writable(O, "O")
+        O = Q.new_empty(shape)
     if ws is None:
-        need = convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D)
-        ws = torch.empty((max(need, 256),), dtype=torch.uint8, device=Q.device)
-    elif ws.get_device() != Q.get_device() or not ws.is_contiguous():
-        raise ValueError("ws must be contiguous on the device of the other tensors")
-    qt, qh, _ = _strides(Q)
-    ot, oh, _ = _strides(O)
-    _check(lib().convrot_cache_attention(_ptr(Q), code, T, Hq, D, qt, qh, _ptr(k_codes), _ptr(v_codes), _ptr(k_scale),
-                                         _ptr(v_scale), num_pages, page, Hkv, _ptr(pages), B, pages.shape[1],
-                                         _strides(pages)[0], _ptr(lengths), _ptr(starts), _ptr(tree),
-                                         float(softmax_scale), _ptr(O), ot, oh, _ptr(ws),
-                                         ws.numel() * ws.element_size(), _stream_ptr(None)),
-           "convrot_cache_attention")
+        need = lib().convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D)
+        ws = Q.new_empty((max(need, 256),), dtype=torch.uint8)
+        room = need
+    else:
+        if ws.get_device() != index or not ws.is_contiguous():
+            raise ValueError("ws must be contiguous on the device of the other tensors")
+        room = ws.numel() * ws.element_size()
+    args = _lib.CACHE_ATTENTION_ARGS.pack(
+        *cells, Q.data_ptr(), O.data_ptr(), pages.data_ptr(), lengths.data_ptr(),
+        0 if starts is None else starts.data_ptr(), 0 if tree is None else tree.data_ptr(), ws.data_ptr(), room, T, Hq,
+        B, pshape[1], ps[0], qs[0], qs[1], os[0], os[1], softmax_scale, code)
+    _check(lib().convrot_cache_attention(args, _raw_stream(index)), "convrot_cache_attention")
     return O
 
 

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libconvrot.so")
 
@@ -15,6 +16,13 @@ _c_void_p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _size = ctypes.c_size_t
+_args = ctypes.c_char_p  # a struct of arguments, packed with the format below
+
+# The structs of include/convrot.h in the compiler's own alignment, field by field. Packing one
+# costs a fifth of passing as many arguments through ctypes.
+ROPE_ARGS = struct.Struct("@5P 5q 3q 3q 4q 4i")
+CACHE_ARGS = struct.Struct("@4P 4q 4P q 4q i")
+CACHE_ATTENTION_ARGS = struct.Struct("@4P 4q 7P N 3q 2q 4q f i")
 
 # name -> (restype, argtypes), mirroring include/convrot.h
 SIGNATURES = {
@@ -50,18 +58,11 @@ SIGNATURES = {
     "convrot_attention_workspace_bytes": (_size, [_i64, _i64, _i64, _i64]),
     "convrot_attention_int8": (_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _i64, ctypes.c_float,
                                       _c_void_p, _c_void_p, _size, _c_void_p]),
-    "convrot_rope": (_int, [_c_void_p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _c_void_p, _int, _i64,
-                            _i64, _i64, _i64, _c_void_p, _c_void_p, _int, _int, _c_void_p, _i64, _i64, _i64,
-                            _c_void_p]),
-    "convrot_cache_append": (_int, [_c_void_p, _c_void_p, _int, _i64, _i64, _i64, _i64, _i64, _i64, _i64, _c_void_p,
-                                    _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p]),
-    "convrot_cache_read": (_int, [_c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i64,
-                                  _c_void_p, _c_void_p, _int, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p]),
+    "convrot_rope": (_int, [_args, _c_void_p]),
+    "convrot_cache_append": (_int, [_args, _c_void_p]),
+    "convrot_cache_read": (_int, [_args, _c_void_p]),
     "convrot_cache_attention_workspace_bytes": (_size, [_i64, _i64, _i64, _i64, _i64]),
-    "convrot_cache_attention": (_int, [_c_void_p, _int, _i64, _i64, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
-                                       _c_void_p, _i64, _i64, _i64, _c_void_p, _i64, _i64, _i64, _c_void_p, _c_void_p,
-                                       _c_void_p, ctypes.c_float, _c_void_p, _i64, _i64, _c_void_p, _size,
-                                       _c_void_p]),
+    "convrot_cache_attention": (_int, [_args, _c_void_p]),
     "convrot_probe_i8_peak_ctas": (_int, []),
     "convrot_probe_ex2_peak": (_int, [_i64, _c_void_p, _size, _c_void_p]),
     "convrot_probe_ex2_per_iter": (_i64, []),

@@ -43,6 +43,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <initializer_list>
 
 #include "convrot.h"
 #include "fwht128.cuh"
@@ -65,6 +66,12 @@ constexpr uint64_t CA_TIMEOUT_NS = 2000000000ull;
 constexpr int CA_BAD = CONVROT_ERR_INVALID_ARG;
 constexpr int CA_TIMEOUT = CONVROT_ERR_DEVICE_TIMEOUT;
 constexpr int CA_MAX_WORKERS = 480;        // pieces the workspace has room for
+#ifndef CA_SETUP
+#define CA_SETUP 4
+#endif
+#ifndef CA_LEAST
+#define CA_LEAST 6
+#endif
 
 // A shape of CTA: 16 MT rows, stages of a warp's ring, CTAs per SM.
 template <int MT, int ST, int OCC>
@@ -125,6 +132,15 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma_s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+}
+
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -132,16 +148,27 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// float(acc) for |acc| < 2^22 (128 products of codes up to 127) without a conversion instruction
-__device__ __forceinline__ float code_sum_to_float(int acc) {
-  return __uint_as_float(static_cast<uint32_t>(acc) + 0x4B400000u) - 12582912.0f;
+// Two sums of 128 products of codes up to 127 (|acc| < 2^22) as floats times `by`, without a conversion
+// instruction: the integer added to the bits of 1.5 * 2^23 is exact, and so is subtracting 1.5 * 2^23.
+__device__ __forceinline__ float2 code_sums(int a, int b, float2 by) {
+  const float2 x = make_float2(__uint_as_float(static_cast<uint32_t>(a) + 0x4B400000u),
+                               __uint_as_float(static_cast<uint32_t>(b) + 0x4B400000u));
+  return __fmul2_rn(__fadd2_rn(x, make_float2(-12582912.0f, -12582912.0f)), by);
 }
 
-// A sequence: its keys, its query tokens, and its share of the line of work.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The maximum of a row that has seen no key: below every logit, and finite, so that exponents of
+// differences need no special case.
+constexpr float CA_NONE = -1e30f;
+
+// A sequence: its keys, its query tokens, and its share of the line of work. An item is CA_SETUP
+// units for what every run costs (queries, first loads, the warps' join) and one for each key tile; without keys one
+// unit, in which its rows are zeroed.
 struct CaSeq {
   int keys, first, news;
-  int tiles;        // key tiles of an item (at least one, which writes a row without keys)
-  int64_t count;    // tiles of all its items
+  int tiles, span;  // key tiles and units of an item
+  int64_t count;    // units of all its items
 };
 
 template <int ROWS>
@@ -157,15 +184,17 @@ __device__ __forceinline__ CaSeq ca_seq(const CaParams& p, int b, int& bad) {
   s.keys = keys;
   s.first = lo;
   s.news = hi - lo;
-  const int64_t rows = static_cast<int64_t>(s.news) * p.G;
-  s.tiles = keys > CA_KT ? static_cast<int>((static_cast<int64_t>(keys) + CA_KT - 1) / CA_KT) : 1;
-  s.count = (rows + ROWS - 1) / ROWS * p.Hkv * s.tiles;
+  s.tiles = static_cast<int>((static_cast<uint32_t>(keys) + CA_KT - 1) / CA_KT);
+  s.span = s.tiles > 0 ? s.tiles + CA_SETUP : 1;
+  const uint32_t tall = (static_cast<uint32_t>(s.news) * static_cast<uint32_t>(p.G) + ROWS - 1) / ROWS;  // < 2^30
+  s.count = static_cast<int64_t>(tall * static_cast<uint32_t>(p.Hkv)) * s.span;
   return s;
 }
 
 // A run of one item's tiles within a piece.
 struct CaRun {
   int head, row0, rows, t0, t1;
+  int left;  // units of the item behind the run
 };
 
 // Walks a piece: the runs from `pos` to `end`, the same for every warp.
@@ -175,23 +204,32 @@ struct CaWalk {
   int b;
   CaSeq s;
   __device__ __forceinline__ bool next(const CaParams& p, CaRun* r, int& bad) {
-    if (pos >= end) return false;
-    while (pos >= base + s.count) {
-      base += s.count;
-      ++b;
-      s = ca_seq<ROWS>(p, b, bad);  // pos < total, so a sequence with work follows
+    while (pos < end) {
+      while (pos >= base + s.count) {
+        base += s.count;
+        ++b;
+        s = ca_seq<ROWS>(p, b, bad);  // pos < total, so a sequence with work follows
+      }
+      const int64_t rel = pos - base;
+      int64_t item;
+      if (rel < (int64_t{1} << 32)) item = static_cast<uint32_t>(rel) / static_cast<uint32_t>(s.span);
+      else item = rel / s.span;
+      const int u0 = static_cast<int>(rel - item * s.span);
+      const int take = end - pos < s.span - u0 ? static_cast<int>(end - pos) : s.span - u0;
+      pos += take;
+      const int setup = s.tiles > 0 ? CA_SETUP : 0;
+      r->t0 = u0 > setup ? u0 - setup : 0;
+      r->t1 = u0 + take > setup ? u0 + take - setup : 0;
+      if (r->t1 <= r->t0) continue;  // the piece ends before the item's first tile
+      r->left = s.span - u0 - take;
+      const uint32_t tall = static_cast<uint32_t>(item) / static_cast<uint32_t>(p.Hkv);  // items of a sequence < 2^32
+      r->head = static_cast<int>(static_cast<uint32_t>(item) - tall * p.Hkv);
+      r->row0 = static_cast<int>(tall * ROWS);
+      const int rows = s.news * p.G - r->row0;
+      r->rows = rows < ROWS ? rows : ROWS;
+      return true;
     }
-    const int64_t rel = pos - base, item = rel / s.tiles;
-    r->t0 = static_cast<int>(rel - item * s.tiles);
-    const int64_t left = end - pos, most = s.tiles - r->t0;
-    r->t1 = r->t0 + static_cast<int>(left < most ? left : most);
-    r->head = static_cast<int>(item % p.Hkv);
-    const int64_t row0 = item / p.Hkv * ROWS;
-    r->row0 = static_cast<int>(row0);
-    const int64_t rows = static_cast<int64_t>(s.news) * p.G - row0;
-    r->rows = rows < ROWS ? static_cast<int>(rows) : ROWS;
-    pos += r->t1 - r->t0;
-    return true;
+    return false;
   }
 };
 
@@ -201,7 +239,8 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
                            const CaParams p) {
   constexpr int MT = Shape::kMt, ST = Shape::kStages, ROWS = Shape::kRows;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // aligned by an offset, not through an integer, so that the compiler still knows it is shared memory
+  uint8_t* smem = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u);
   int64_t* scan = reinterpret_cast<int64_t*>(smem + Shape::kOffScan);  // a sum per warp; then found
   uint8_t* qs = smem + Shape::kOffQ;
   unsigned long long* row_bits = reinterpret_cast<unsigned long long*>(smem + Shape::kOffRow);
@@ -240,6 +279,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     __syncthreads();
     const int64_t total = (scan[0] + scan[1]) + (scan[2] + scan[3]);
     per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < CA_LEAST) per = CA_LEAST;
     walk.pos = blockIdx.x * per;
     walk.end = walk.pos + per < total ? walk.pos + per : total;
     if (walk.pos < total) {
@@ -284,23 +324,34 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     const int keys = walk.s.keys;
     const int context = keys - walk.s.news;  // key of the first new token; may be negative
     const int32_t* table = p.pages + walk.b * p.table_stride;
+    if (keys == 0) {  // nothing to see: zeros
+      for (int i = tid; i < r.rows * (CA_D / 8); i += CA_THREADS) {
+        const int of = r.row0 + i / (CA_D / 8), token = of / p.G;
+        *reinterpret_cast<uint4*>(p.o + (walk.s.first + token) * p.ot + (r.head * p.G + (of - token * p.G)) * p.oh +
+                                  8 * (i % (CA_D / 8))) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      continue;
+    }
     uint32_t live = 0;  // stages with copies under way
-    auto issue = [&](int t, int st) {
+    auto lookup = [&](int t) {
+      const int key = t * CA_KT + warp * CA_SUB;
+      return t < r.t1 && key < keys ? __ldg(table + (key >> p.page_shift)) : 0;
+    };
+    auto issue = [&](int t, int st, int page) {
       const int key = t * CA_KT + warp * CA_SUB;
       live &= ~(1u << st);
       if (t < r.t1 && key < keys && ok) {
-        const int page = __ldg(table + (key >> p.page_shift));
         if (page >= 0 && page < p.num_pages) {
           live |= 1u << st;
           if (lane == 0) {
-            const int64_t cell = ((static_cast<int64_t>(page) * p.Hkv + r.head) << p.page_shift) +
-                                 (key & ((1 << p.page_shift) - 1));
+            // cells of a cache are fewer than 2^31
+            const int cell = ((page * p.Hkv + r.head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
             uint8_t* to = ring + st * CA_STAGE;
             float* sc = ring_scale + st * 2 * CA_SUB;
             mbar_arrive_expect_tx(full + st, CA_STAGE + 2 * CA_SUB * 4);
-            tma_load_2d(to, &tmK, full + st, 0, static_cast<int32_t>(cell));
+            tma_load_2d(to, &tmK, full + st, 0, cell);
             bulk_load(sc, p.k_scale + cell, CA_SUB * 4, full + st);
-            tma_load_2d(to + CA_CODES, &tmV, full + st, 0, static_cast<int32_t>(cell));
+            tma_load_2d(to + CA_CODES, &tmV, full + st, 0, cell);
             bulk_load(sc + CA_SUB, p.v_scale + cell, CA_SUB * 4, full + st);
           }
         } else {
@@ -308,8 +359,15 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
         }
       }
     };
-#pragma unroll 1
-    for (int i = 0; i < ST; ++i) issue(r.t0 + i, i);
+    int ahead;  // page of the next tile to issue
+    {
+      int page[ST];
+#pragma unroll
+      for (int i = 0; i < ST; ++i) page[i] = lookup(r.t0 + i);
+      ahead = lookup(r.t0 + ST);
+#pragma unroll
+      for (int i = 0; i < ST; ++i) issue(r.t0 + i, i, page[i]);
+    }
 
     // ---- the tile's queries: rotated, quantised, into shared memory
     if (p.tree != nullptr && walk.s.news > 64) bad |= CA_BAD;
@@ -358,13 +416,15 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
         cr[m][half] = row_c[row];
       }
     }
-    float acc[MT][16][4], mx[MT][2], l[MT][2], inv[MT][2];  // inv: the weights' factor (0: none yet)
+    float acc[MT][16][4], mx[MT][2], inv[MT][2];  // inv: the weights' factor (0: none yet)
+    float2 l2[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.0f;
-      mx[m][0] = mx[m][1] = -INFINITY;
-      l[m][0] = l[m][1] = inv[m][0] = inv[m][1] = 0.0f;
+      mx[m][0] = mx[m][1] = CA_NONE;
+      inv[m][0] = inv[m][1] = 0.0f;
+      l2[m][0] = l2[m][1] = make_float2(0.0f, 0.0f);
     }
 
     // ---- the keys
@@ -380,8 +440,9 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
         const uint8_t* kc = ring + st * CA_STAGE;
         const uint8_t* vc = kc + CA_CODES;
         const float* sk = ring_scale + st * 2 * CA_SUB;
-        float s[MT][2][4];
+        float2 s[MT][2][2];  // logits in base 2: row tile, eight keys, row of the thread
         float2 sv[2];
+        bool wild = false;   // an unseen cell's value scale is not a number
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const uint8_t* row = kc + (8 * n + g) * CA_D;
@@ -391,15 +452,13 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
           sv[n] = *reinterpret_cast<const float2*>(sk + CA_SUB + 8 * n + 2 * t4);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            int d[4] = {0, 0, 0, 0};
-            mma_s8(d, qa[m][0], qa[m][1], qa[m][2], qa[m][3], a.x, a.y);
+            int d[4];
+            mma_s8_first(d, qa[m][0], qa[m][1], qa[m][2], qa[m][3], a.x, a.y);
             mma_s8(d, qa[m][4], qa[m][5], qa[m][6], qa[m][7], a.z, a.w);
             mma_s8(d, qa[m][8], qa[m][9], qa[m][10], qa[m][11], b.x, b.y);
             mma_s8(d, qa[m][12], qa[m][13], qa[m][14], qa[m][15], b.z, b.w);
-            s[m][n][0] = code_sum_to_float(d[0]) * (cr[m][0] * f2.x);
-            s[m][n][1] = code_sum_to_float(d[1]) * (cr[m][0] * f2.y);
-            s[m][n][2] = code_sum_to_float(d[2]) * (cr[m][1] * f2.x);
-            s[m][n][3] = code_sum_to_float(d[3]) * (cr[m][1] * f2.y);
+            s[m][n][0] = code_sums(d[0], d[1], __fmul2_rn(f2, both(cr[m][0])));
+            s[m][n][1] = code_sums(d[2], d[3], __fmul2_rn(f2, both(cr[m][1])));
           }
         }
         if (key0 + CA_SUB > clear || key0 + CA_SUB > keys) {
@@ -418,10 +477,11 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
                   const int row = m * 16 + 8 * half + g;
                   const bool seen = key < keys && (key < row_lim[row] || (drafted >= 0 && drafted < 64 &&
                                                                           (row_bits[row] >> drafted & 1ull) != 0));
-                  if (!seen) s[m][n][2 * half + e] = -INFINITY;
+                  if (!seen) (e ? s[m][n][half].y : s[m][n][half].x) = -INFINITY;
                 }
               }
             }
+            wild |= !(fmaxf(fabsf(sv[n].x), fabsf(sv[n].y)) < INFINITY) || sv[n].x != sv[n].x || sv[n].y != sv[n].y;
           }
         }
         uint32_t pw[MT][4];
@@ -430,8 +490,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
           float top[2];
 #pragma unroll
           for (int half = 0; half < 2; ++half)
-            top[half] = fmaxf(fmaxf(s[m][0][2 * half], s[m][0][2 * half + 1]),
-                              fmaxf(s[m][1][2 * half], s[m][1][2 * half + 1]));
+            top[half] = fwht::fmax3f(s[m][0][half].x, s[m][0][half].y, fmaxf(s[m][1][half].x, s[m][1][half].y));
           if (__any_sync(0xFFFFFFFFu, top[0] > mx[m][0] + 8.0f || top[1] > mx[m][1] + 8.0f)) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -439,7 +498,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
               now = fmaxf(mx[m][half], fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, 2)));
               if (now > mx[m][half]) {
                 // the sums stay as they are: their unit shrinks with the weights'
-                l[m][half] *= ex2_approx(mx[m][half] - now);
+                l2[m][half] = __fmul2_rn(l2[m][half], both(ex2_approx(mx[m][half] - now)));
                 inv[m][half] *= ex2_approx(now - mx[m][half]);
                 mx[m][half] = now;
                 if (!(inv[m][half] <= 0x1p100f)) {  // nothing that came before is left beside this key
@@ -450,22 +509,26 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
               }
             }
           }
-          // weights p s_v; a row that has seen nothing has no maximum
-          float x[2][4], big[2];
+          // weights p s_v
+          float2 x[2][2];
+          float big[2];
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            const float ref = mx[m][half] == -INFINITY ? 0.0f : mx[m][half];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-              const float p0 = ex2_approx(s[m][n][2 * half] - ref), p1 = ex2_approx(s[m][n][2 * half + 1] - ref);
-              l[m][half] += p0 + p1;
-              x[n][2 * half] = p0 > 0.0f ? p0 * sv[n].x : 0.0f;
-              x[n][2 * half + 1] = p1 > 0.0f ? p1 * sv[n].y : 0.0f;
+              const float2 y = __fadd2_rn(s[m][n][half], both(-mx[m][half]));
+              const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+              l2[m][half] = __fadd2_rn(l2[m][half], pr);
+              x[n][half] = __fmul2_rn(pr, sv[n]);
+              if (wild) {
+                if (pr.x == 0.0f) x[n][half].x = 0.0f;
+                if (pr.y == 0.0f) x[n][half].y = 0.0f;
+              }
             }
-            big[half] = fmaxf(fmaxf(x[0][2 * half], x[0][2 * half + 1]), fmaxf(x[1][2 * half], x[1][2 * half + 1]));
+            big[half] = fwht::fmax3f(x[0][half].x, x[0][half].y, fmaxf(x[1][half].x, x[1][half].y));
           }
-          const bool grow = (inv[m][0] == 0.0f ? big[0] > 0.0f : big[0] * inv[m][0] > 4096.0f) ||
-                            (inv[m][1] == 0.0f ? big[1] > 0.0f : big[1] * inv[m][1] > 4096.0f);
+          const bool grow = big[0] * inv[m][0] > 4096.0f || big[1] * inv[m][1] > 4096.0f ||
+                            (inv[m][0] == 0.0f && big[0] > 0.0f) || (inv[m][1] == 0.0f && big[1] > 0.0f);
           if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -487,10 +550,12 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
           }
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const __half2 a = __floats2half2_rn(x[n][0] * inv[m][0], x[n][1] * inv[m][0]);
-            const __half2 b = __floats2half2_rn(x[n][2] * inv[m][1], x[n][3] * inv[m][1]);
-            pw[m][2 * n] = *reinterpret_cast<const uint32_t*>(&a);
-            pw[m][2 * n + 1] = *reinterpret_cast<const uint32_t*>(&b);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const float2 w = __fmul2_rn(x[n][half], both(inv[m][half]));
+              const __half2 h = __floats2half2_rn(w.x, w.y);
+              pw[m][2 * n + half] = *reinterpret_cast<const uint32_t*>(&h);
+            }
           }
         }
         // values: keys 2t, 2t + 1, 2t + 8, 2t + 9, channels 16 g .. 16 g + 15
@@ -529,7 +594,8 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
         }
       }
       __syncwarp();  // the stage has been read by every lane
-      issue(t + ST, st);
+      issue(t + ST, st, ahead);
+      ahead = lookup(t + ST + 1);
       if (++st == ST) st = 0;
     }
     if (!ok) {
@@ -543,10 +609,12 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     }
 
     // ---- the four warps joined through the idle ring: 2, 3 into 0, 1, then 1 into 0
+    float l[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        l[m][half] = l2[m][half].x + l2[m][half].y;
         l[m][half] += __shfl_xor_sync(0xFFFFFFFFu, l[m][half], 1);
         l[m][half] += __shfl_xor_sync(0xFFFFFFFFu, l[m][half], 2);
         const float by = inv[m][half] == 0.0f ? 0.0f : 1.0f / inv[m][half];
@@ -583,8 +651,8 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
           for (int half = 0; half < 2; ++half) {
             const float mx_b = half ? other.y : other.x, l_b = half ? other.w : other.z;
             const float now = fmaxf(mx[m][half], mx_b);
-            fa[half] = mx[m][half] == now ? 1.0f : ex2_approx(mx[m][half] - now);
-            fb[half] = mx_b == now ? 1.0f : ex2_approx(mx_b - now);
+            fa[half] = ex2_approx(mx[m][half] - now);
+            fb[half] = ex2_approx(mx_b - now);
             mx[m][half] = now;
             l[m][half] = l[m][half] * fa[half] + l_b * fb[half];
           }
@@ -604,8 +672,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     const bool whole = r.t0 == 0 && r.t1 == walk.s.tiles;
     if (r.t0 == 0 && !whole) {
       // the piece ends inside an item that begins in it: it describes the item to the join
-      const int64_t item_end = walk.end - r.t1 + walk.s.tiles;  // one past the item's last tile
-      cut.pieces = static_cast<int>((item_end - 1) / per) - static_cast<int>(blockIdx.x) + 1;
+      cut.pieces = static_cast<int>((walk.end + r.left - 1) / per) - static_cast<int>(blockIdx.x) + 1;
       cut.rows = r.rows;
       cut.row0 = r.row0;
       cut.head = r.head;
@@ -683,7 +750,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(cons
   if (row >= cut.rows || cut.pieces < 1) return;
   // piece 0 of the item is slot 2 c + 1, the k-th after it slot 2 (c + k)
   auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(blockIdx.x) + 1 : 2 * (static_cast<int64_t>(blockIdx.x) + k); };
-  float top = -INFINITY;
+  float top = CA_NONE;
   for (int k = tid; k < cut.pieces; k += kJoinThreads) top = fmaxf(top, p.part_ml[slot(k) * rows + row].x);
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
@@ -693,7 +760,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(cons
   float sum = 0.0f;
   for (int k = tid; k < cut.pieces; k += kJoinThreads) {
     const float2 ml = p.part_ml[slot(k) * rows + row];
-    const float w = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - top);
+    const float w = ex2_approx(ml.x - top);
     weight[k] = w;
     sum += w * ml.y;
   }
@@ -834,67 +901,68 @@ size_t convrot_cache_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq,
   return ca_wide(T, B, Hq / Hkv) ? ca_layout<Shape32>().total : ca_layout<Shape16>().total;
 }
 
-convrot_status convrot_cache_attention(const void* Q, int dtype, int64_t T, int64_t Hq, int64_t D, int64_t q_token,
-                                       int64_t q_head, const int8_t* k_codes, const int8_t* v_codes,
-                                       const float* k_scale, const float* v_scale, int64_t num_pages,
-                                       int64_t page_size, int64_t Hkv, const int32_t* pages, int64_t B,
-                                       int64_t table_pages, int64_t table_stride, const int32_t* lengths,
-                                       const int32_t* starts, const int64_t* tree, float softmax_scale, void* O,
-                                       int64_t o_token, int64_t o_head, void* ws, size_t ws_bytes,
-                                       convrot_stream_t stream) {
+convrot_status convrot_cache_attention(const convrot_cache_attention_args* args, convrot_stream_t stream) {
   using namespace convrot;
-  if (dtype != CONVROT_DTYPE_BF16 && dtype != CONVROT_DTYPE_F16) return CONVROT_ERR_UNSUPPORTED;
-  if (D != CA_D) return CONVROT_ERR_UNSUPPORTED;
-  if (T < 0 || B < 0 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || num_pages < 1 || page_size < 1 || table_pages < 0 ||
-      table_stride < 0)
+  if (args == nullptr) return CONVROT_ERR_INVALID_ARG;
+  const convrot_cache_attention_args& a = *args;
+  const convrot_cells& c = a.cells;
+  if (a.dtype != CONVROT_DTYPE_BF16 && a.dtype != CONVROT_DTYPE_F16) return CONVROT_ERR_UNSUPPORTED;
+  if (c.D != CA_D) return CONVROT_ERR_UNSUPPORTED;
+  if (a.T < 0 || a.B < 0 || c.H < 1 || a.Hq < 1 || a.Hq % c.H != 0 || c.num_pages < 1 || c.page_size < 1 ||
+      a.table_pages < 0)
     return CONVROT_ERR_INVALID_ARG;
-  if (page_size < CONVROT_MIN_PAGE || page_size > CONVROT_MAX_PAGE || (page_size & (page_size - 1)) != 0)
+  if (c.page_size < CONVROT_MIN_PAGE || c.page_size > CONVROT_MAX_PAGE || (c.page_size & (c.page_size - 1)) != 0)
     return CONVROT_ERR_UNSUPPORTED;
-  if (!ca_sizes_ok(T, B, Hq, Hkv, D) || num_pages > 0x7FFFFFFF / page_size / Hkv ||
-      table_pages > 0x7FFFF000 / page_size)
+  if (!ca_sizes_ok(a.T, a.B, a.Hq, c.H, c.D) || c.num_pages > 0x7FFFFFFF / c.page_size / c.H ||
+      a.table_pages > 0x7FFFF000 / c.page_size)
     return CONVROT_ERR_UNSUPPORTED;
-  if (starts == nullptr && T != B) return CONVROT_ERR_INVALID_ARG;
-  if (!(softmax_scale > 0.0f) || !(softmax_scale < 3.0e38f)) return CONVROT_ERR_INVALID_ARG;
-  if (q_token % 8 != 0 || q_head % 8 != 0 || o_token % 8 != 0 || o_head % 8 != 0) return CONVROT_ERR_INVALID_ARG;
-  if (T == 0 || B == 0) return CONVROT_OK;  // no queries
-  auto aligned = [](const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; };
-  if (Q == nullptr || O == nullptr || k_codes == nullptr || v_codes == nullptr || k_scale == nullptr ||
-      v_scale == nullptr || lengths == nullptr || (pages == nullptr && table_pages > 0))
-    return CONVROT_ERR_INVALID_ARG;
-  if (!aligned(Q, 16) || !aligned(O, 16) || !aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 16) ||
-      !aligned(v_scale, 16) || !aligned(pages, 4) || !aligned(lengths, 4) || !aligned(starts, 4) || !aligned(tree, 8))
-    return CONVROT_ERR_INVALID_ARG;
-  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D))
-    return CONVROT_ERR_WORKSPACE;
+  if (a.starts == nullptr && a.T != a.B) return CONVROT_ERR_INVALID_ARG;
+  if (!(a.softmax_scale > 0.0f) || !(a.softmax_scale < 3.0e38f)) return CONVROT_ERR_INVALID_ARG;
+  auto stride = [](int64_t n, int64_t st) { return n > 1 ? st : 0; };
   CaParams p{};
-  p.q = static_cast<const uint16_t*>(Q);
-  p.o = static_cast<uint16_t*>(O);
-  p.qt = q_token, p.qh = q_head, p.ot = o_token, p.oh = o_head;
-  p.k_scale = k_scale;
-  p.v_scale = v_scale;
-  p.pages = pages;
-  p.lengths = lengths;
-  p.starts = starts;
-  p.tree = reinterpret_cast<const unsigned long long*>(tree);
-  p.table_stride = table_stride;
-  p.T = static_cast<int>(T);
-  p.B = static_cast<int>(B);
-  p.Hkv = static_cast<int>(Hkv);
-  p.G = static_cast<int>(Hq / Hkv);
-  p.table_pages = static_cast<int>(table_pages);
-  p.num_pages = static_cast<int>(num_pages);
-  while ((int64_t{1} << p.page_shift) < page_size) ++p.page_shift;
-  p.c_scale = softmax_scale * 1.4426950408889634f;
+  p.qt = stride(a.T, a.q_token), p.qh = stride(a.Hq, a.q_head);
+  p.ot = stride(a.T, a.o_token), p.oh = stride(a.Hq, a.o_head);
+  p.table_stride = stride(a.B, a.table_stride);
+  if ((p.qt | p.qh | p.ot | p.oh) % 8 != 0 || p.table_stride < 0) return CONVROT_ERR_INVALID_ARG;
+  if (a.T == 0 || a.B == 0) return CONVROT_OK;  // no queries
+  auto aligned = [](const void* ptr, uintptr_t to) { return (reinterpret_cast<uintptr_t>(ptr) % to) == 0; };
+  for (const void* ptr : {a.Q, static_cast<const void*>(a.O), static_cast<const void*>(c.k_codes),
+                          static_cast<const void*>(c.v_codes), static_cast<const void*>(c.k_scale),
+                          static_cast<const void*>(c.v_scale)})
+    if (ptr == nullptr || !aligned(ptr, 16)) return CONVROT_ERR_INVALID_ARG;
+  if (a.lengths == nullptr || (a.pages == nullptr && a.table_pages > 0) || !aligned(a.pages, 4) ||
+      !aligned(a.lengths, 4) || !aligned(a.starts, 4) || !aligned(a.tree, 8))
+    return CONVROT_ERR_INVALID_ARG;
+  if (a.ws == nullptr || !aligned(a.ws, 256) ||
+      a.ws_bytes < convrot_cache_attention_workspace_bytes(a.T, a.B, a.Hq, c.H, c.D))
+    return CONVROT_ERR_WORKSPACE;
+  p.q = static_cast<const uint16_t*>(a.Q);
+  p.o = static_cast<uint16_t*>(a.O);
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.pages = a.pages;
+  p.lengths = a.lengths;
+  p.starts = a.starts;
+  p.tree = reinterpret_cast<const unsigned long long*>(a.tree);
+  p.T = static_cast<int>(a.T);
+  p.B = static_cast<int>(a.B);
+  p.Hkv = static_cast<int>(c.H);
+  p.G = static_cast<int>(a.Hq / c.H);
+  p.table_pages = static_cast<int>(a.table_pages);
+  p.num_pages = static_cast<int>(c.num_pages);
+  while ((int64_t{1} << p.page_shift) < c.page_size) ++p.page_shift;
+  p.c_scale = a.softmax_scale * 1.4426950408889634f;
   CUtensorMap tk, tv;
-  if (!ca_encode(&tk, k_codes, num_pages * Hkv * page_size) || !ca_encode(&tv, v_codes, num_pages * Hkv * page_size))
+  const int64_t cells = c.num_pages * c.H * c.page_size;
+  if (!ca_encode(&tk, c.k_codes, cells) || !ca_encode(&tv, c.v_codes, cells))
     return CONVROT_ERR_INVALID_ARG;
   // rows a tile can have at most: all of one sequence's
-  const int64_t rows = (starts == nullptr ? 1 : T) * (Hq / Hkv);
-  uint8_t* w = static_cast<uint8_t*>(ws);
+  const int64_t rows = (a.starts == nullptr ? 1 : a.T) * p.G;
+  uint8_t* w = static_cast<uint8_t*>(a.ws);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool f16 = dtype == CONVROT_DTYPE_F16;
+  const bool f16 = a.dtype == CONVROT_DTYPE_F16;
   cudaError_t e;
-  if (ca_wide(T, B, Hq / Hkv))
+  if (ca_wide(a.T, a.B, p.G))
     e = f16 ? ca_launch<Shape32, true>(tk, tv, p, w, rows, s) : ca_launch<Shape32, false>(tk, tv, p, w, rows, s);
   else
     e = f16 ? ca_launch<Shape16, true>(tk, tv, p, w, rows, s) : ca_launch<Shape16, false>(tk, tv, p, w, rows, s);

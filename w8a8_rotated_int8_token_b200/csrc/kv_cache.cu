@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <initializer_list>
 
 #include "convrot.h"
 #include "fwht128.cuh"
@@ -164,39 +165,40 @@ __global__ void __launch_bounds__(kCellThreads) cache_read_kernel(const CellPara
 bool aligned_to(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
 
 // The checks both directions share; CONVROT_OK with p filled in, or an error.
-convrot_status cell_params(const void* K, const void* V, int dtype, int64_t T, int64_t H, int64_t D, int64_t kt,
-                           int64_t kh, int64_t vt, int64_t vh, const int32_t* slots, const int8_t* k_codes,
-                           const int8_t* v_codes, const float* k_scale, const float* v_scale, int64_t num_pages,
-                           int64_t page_size, int* status, CellParams* p) {
-  if (dtype != CONVROT_DTYPE_BF16 && dtype != CONVROT_DTYPE_F16) return CONVROT_ERR_UNSUPPORTED;
-  if (D != kCellDim) return CONVROT_ERR_UNSUPPORTED;
-  if (T < 0 || H < 1 || num_pages < 1 || page_size < 1) return CONVROT_ERR_INVALID_ARG;
-  if (page_size < CONVROT_MIN_PAGE || page_size > CONVROT_MAX_PAGE || (page_size & (page_size - 1)) != 0)
+convrot_status cell_params(const convrot_cache_args* args, CellParams* p) {
+  if (args == nullptr) return CONVROT_ERR_INVALID_ARG;
+  const convrot_cache_args& a = *args;
+  const convrot_cells& c = a.cells;
+  if (a.dtype != CONVROT_DTYPE_BF16 && a.dtype != CONVROT_DTYPE_F16) return CONVROT_ERR_UNSUPPORTED;
+  if (c.D != kCellDim) return CONVROT_ERR_UNSUPPORTED;
+  if (a.T < 0 || c.H < 1 || c.num_pages < 1 || c.page_size < 1) return CONVROT_ERR_INVALID_ARG;
+  if (c.page_size < CONVROT_MIN_PAGE || c.page_size > CONVROT_MAX_PAGE || (c.page_size & (c.page_size - 1)) != 0)
     return CONVROT_ERR_UNSUPPORTED;
-  if (H > CONVROT_MAX_CACHE_HEADS || num_pages > 0x7FFFFFFF / page_size || T > 0x3FFFFFFF / H)
+  if (c.H > CONVROT_MAX_CACHE_HEADS || c.num_pages > 0x7FFFFFFF / c.page_size || a.T > 0x3FFFFFFF / c.H)
     return CONVROT_ERR_UNSUPPORTED;
-  if (kt % 8 != 0 || kh % 8 != 0 || vt % 8 != 0 || vh % 8 != 0) return CONVROT_ERR_INVALID_ARG;
-  if (T == 0) return CONVROT_OK;
-  if (K == nullptr || V == nullptr || slots == nullptr || k_codes == nullptr || v_codes == nullptr ||
-      k_scale == nullptr || v_scale == nullptr)
-    return CONVROT_ERR_INVALID_ARG;
-  if (!aligned_to(K, 16) || !aligned_to(V, 16) || !aligned_to(slots, 4) || !aligned_to(k_codes, 16) ||
-      !aligned_to(v_codes, 16) || !aligned_to(k_scale, 16) || !aligned_to(v_scale, 16) || !aligned_to(status, 4))
-    return CONVROT_ERR_INVALID_ARG;
-  p->k = const_cast<uint16_t*>(static_cast<const uint16_t*>(K));
-  p->v = const_cast<uint16_t*>(static_cast<const uint16_t*>(V));
-  p->kt = kt, p->kh = kh, p->vt = vt, p->vh = vh;
-  p->slots = slots;
-  p->k_codes = const_cast<int8_t*>(k_codes);
-  p->v_codes = const_cast<int8_t*>(v_codes);
-  p->k_scale = const_cast<float*>(k_scale);
-  p->v_scale = const_cast<float*>(v_scale);
-  p->vectors = 2 * T * H;
-  p->H = static_cast<int>(H);
+  auto stride = [](int64_t n, int64_t st) { return n > 1 ? st : 0; };
+  p->kt = stride(a.T, a.k_token), p->kh = stride(c.H, a.k_head);
+  p->vt = stride(a.T, a.v_token), p->vh = stride(c.H, a.v_head);
+  if ((p->kt | p->kh | p->vt | p->vh) % 8 != 0) return CONVROT_ERR_INVALID_ARG;
+  if (a.T == 0) return CONVROT_OK;
+  for (const void* ptr : {static_cast<const void*>(a.K), static_cast<const void*>(a.V),
+                          static_cast<const void*>(c.k_codes), static_cast<const void*>(c.v_codes),
+                          static_cast<const void*>(c.k_scale), static_cast<const void*>(c.v_scale)})
+    if (ptr == nullptr || !aligned_to(ptr, 16)) return CONVROT_ERR_INVALID_ARG;
+  if (a.slots == nullptr || !aligned_to(a.slots, 4) || !aligned_to(a.status, 4)) return CONVROT_ERR_INVALID_ARG;
+  p->k = static_cast<uint16_t*>(a.K);
+  p->v = static_cast<uint16_t*>(a.V);
+  p->slots = a.slots;
+  p->k_codes = c.k_codes;
+  p->v_codes = c.v_codes;
+  p->k_scale = c.k_scale;
+  p->v_scale = c.v_scale;
+  p->vectors = 2 * a.T * c.H;
+  p->H = static_cast<int>(c.H);
   p->page_shift = 0;
-  while ((int64_t{1} << p->page_shift) < page_size) ++p->page_shift;
-  p->capacity = static_cast<int>(num_pages * page_size);
-  p->status = status;
+  while ((int64_t{1} << p->page_shift) < c.page_size) ++p->page_shift;
+  p->capacity = static_cast<int>(c.num_pages * c.page_size);
+  p->status = a.status;
   return CONVROT_OK;
 }
 
@@ -210,32 +212,22 @@ unsigned cell_grid(const CellParams& p) {
 
 extern "C" {
 
-convrot_status convrot_cache_append(const void* K, const void* V, int dtype, int64_t T, int64_t H, int64_t D,
-                                    int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head,
-                                    const int32_t* slots, int8_t* k_codes, int8_t* v_codes, float* k_scale,
-                                    float* v_scale, int64_t num_pages, int64_t page_size, int* status,
-                                    convrot_stream_t stream) {
+convrot_status convrot_cache_append(const convrot_cache_args* args, convrot_stream_t stream) {
   using namespace convrot;
   CellParams p{};
-  const convrot_status st = cell_params(K, V, dtype, T, H, D, k_token, k_head, v_token, v_head, slots, k_codes, v_codes,
-                                        k_scale, v_scale, num_pages, page_size, status, &p);
-  if (st != CONVROT_OK || T == 0) return st;
-  (dtype == CONVROT_DTYPE_F16 ? cache_append_kernel<true> : cache_append_kernel<false>)<<<
+  const convrot_status st = cell_params(args, &p);
+  if (st != CONVROT_OK || args->T == 0) return st;
+  (args->dtype == CONVROT_DTYPE_F16 ? cache_append_kernel<true> : cache_append_kernel<false>)<<<
       cell_grid(p), kCellThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
 }
 
-convrot_status convrot_cache_read(const int32_t* slots, int64_t T, int64_t H, int64_t D, const int8_t* k_codes,
-                                  const int8_t* v_codes, const float* k_scale, const float* v_scale,
-                                  int64_t num_pages, int64_t page_size, void* K, void* V, int dtype, int64_t k_token,
-                                  int64_t k_head, int64_t v_token, int64_t v_head, int* status,
-                                  convrot_stream_t stream) {
+convrot_status convrot_cache_read(const convrot_cache_args* args, convrot_stream_t stream) {
   using namespace convrot;
   CellParams p{};
-  const convrot_status st = cell_params(K, V, dtype, T, H, D, k_token, k_head, v_token, v_head, slots, k_codes, v_codes,
-                                        k_scale, v_scale, num_pages, page_size, status, &p);
-  if (st != CONVROT_OK || T == 0) return st;
-  (dtype == CONVROT_DTYPE_F16 ? cache_read_kernel<true> : cache_read_kernel<false>)<<<
+  const convrot_status st = cell_params(args, &p);
+  if (st != CONVROT_OK || args->T == 0) return st;
+  (args->dtype == CONVROT_DTYPE_F16 ? cache_read_kernel<true> : cache_read_kernel<false>)<<<
       cell_grid(p), kCellThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
 }

@@ -178,46 +178,48 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(const RopePar
 
 extern "C" {
 
-convrot_status convrot_rope(const void* X, int dtype, int64_t B, int64_t S, int64_t H, int64_t D, int64_t R,
-                            int64_t x_batch, int64_t x_token, int64_t x_head, const void* positions, int pos_dtype,
-                            int64_t axes, int64_t pos_axis, int64_t pos_batch, int64_t pos_token, const double* freq,
-                            const int32_t* axis, int interleaved, int inverse, void* Y, int64_t y_batch,
-                            int64_t y_token, int64_t y_head, convrot_stream_t stream) {
+convrot_status convrot_rope(const convrot_rope_args* args, convrot_stream_t stream) {
   using namespace convrot;
-  if (dtype != CONVROT_DTYPE_BF16 && dtype != CONVROT_DTYPE_F16) return CONVROT_ERR_UNSUPPORTED;
-  if (pos_dtype != CONVROT_POS_I32 && pos_dtype != CONVROT_POS_F32) return CONVROT_ERR_UNSUPPORTED;
-  if (B < 0 || S < 0 || H < 1 || D < 1 || R < 0 || R > D || R % 2 != 0 || axes < 1) return CONVROT_ERR_INVALID_ARG;
-  if (D > kRopeMaxDim || H > 65535 || B > 0x7FFFFFFF || S > 0x7FFFFFFF || (S > 0 && B > 0x7FFFFFFF / S))
+  if (args == nullptr) return CONVROT_ERR_INVALID_ARG;
+  const convrot_rope_args& a = *args;
+  if ((a.dtype != CONVROT_DTYPE_BF16 && a.dtype != CONVROT_DTYPE_F16) ||
+      (a.pos_dtype != CONVROT_POS_I32 && a.pos_dtype != CONVROT_POS_F32))
     return CONVROT_ERR_UNSUPPORTED;
-  if (axes > 0x7FFFFFFF) return CONVROT_ERR_UNSUPPORTED;
-  if (B == 0 || S == 0) return CONVROT_OK;  // no tokens
-  if (X == nullptr || Y == nullptr || (R > 0 && (positions == nullptr || freq == nullptr || axis == nullptr)))
+  if (a.B < 0 || a.S < 0 || a.H < 1 || a.D < 1 || a.R < 0 || a.R > a.D || a.R % 2 != 0 || a.axes < 1)
     return CONVROT_ERR_INVALID_ARG;
-  auto aligned = [](const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; };
-  if (!aligned(X, 2) || !aligned(Y, 2) || !aligned(positions, 4) || !aligned(freq, 8) || !aligned(axis, 4))
+  if (a.D > kRopeMaxDim || a.H > 65535 || a.B > 0x7FFFFFFF || a.S > 0x7FFFFFFF || a.axes > 0x7FFFFFFF ||
+      (a.S > 0 && a.B > 0x7FFFFFFF / a.S))
+    return CONVROT_ERR_UNSUPPORTED;
+  if (a.B == 0 || a.S == 0) return CONVROT_OK;  // no tokens
+  if (a.X == nullptr || a.Y == nullptr ||
+      (a.R > 0 && (a.positions == nullptr || a.freq == nullptr || a.axis == nullptr)))
     return CONVROT_ERR_INVALID_ARG;
+  auto aligned = [](const void* ptr, uintptr_t to) { return (reinterpret_cast<uintptr_t>(ptr) % to) == 0; };
+  if (!aligned(a.X, 2) || !aligned(a.Y, 2) || !aligned(a.positions, 4) || !aligned(a.freq, 8) || !aligned(a.axis, 4))
+    return CONVROT_ERR_INVALID_ARG;
+  auto stride = [](int64_t n, int64_t st) { return n > 1 ? st : 0; };
   RopeParams p{};
-  p.x = static_cast<const uint16_t*>(X);
-  p.y = static_cast<uint16_t*>(Y);
-  p.tokens = B * S;
-  p.S = static_cast<int>(S);
-  p.H = static_cast<int>(H);
-  p.D = static_cast<int>(D);
-  p.R = static_cast<int>(R);
-  p.xb = x_batch, p.xs = x_token, p.xh = x_head;
-  p.yb = y_batch, p.ys = y_token, p.yh = y_head;
-  p.pos = positions;
-  p.pos_float = pos_dtype == CONVROT_POS_F32;
-  p.axes = static_cast<int>(axes);
-  p.pa = pos_axis, p.pb = pos_batch, p.ps = pos_token;
-  p.freq = freq;
-  p.axis = axis;
-  p.interleaved = interleaved != 0;
-  p.inverse = inverse != 0;
-  const bool f16 = dtype == CONVROT_DTYPE_F16;
+  p.x = static_cast<const uint16_t*>(a.X);
+  p.y = static_cast<uint16_t*>(a.Y);
+  p.tokens = a.B * a.S;
+  p.S = static_cast<int>(a.S);
+  p.H = static_cast<int>(a.H);
+  p.D = static_cast<int>(a.D);
+  p.R = static_cast<int>(a.R);
+  p.xb = stride(a.B, a.x_batch), p.xs = stride(a.S, a.x_token), p.xh = stride(a.H, a.x_head);
+  p.yb = stride(a.B, a.y_batch), p.ys = stride(a.S, a.y_token), p.yh = stride(a.H, a.y_head);
+  p.pos = a.positions;
+  p.pos_float = a.pos_dtype == CONVROT_POS_F32;
+  p.axes = static_cast<int>(a.axes);
+  p.pa = stride(a.axes, a.pos_axis), p.pb = stride(a.B, a.pos_batch), p.ps = stride(a.S, a.pos_token);
+  p.freq = a.freq;
+  p.axis = a.axis;
+  p.interleaved = a.interleaved != 0;
+  p.inverse = a.inverse != 0;
+  const bool f16 = a.dtype == CONVROT_DTYPE_F16;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t odd = x_batch | x_token | x_head | y_batch | y_token | y_head;
-  if (D % 16 != 0 || R % 16 != 0 || odd % 8 != 0 || !aligned(X, 16) || !aligned(Y, 16)) {
+  const int64_t strides = p.xb | p.xs | p.xh | p.yb | p.ys | p.yh;
+  if (p.D % 16 != 0 || p.R % 16 != 0 || strides % 8 != 0 || !aligned(p.x, 16) || !aligned(p.y, 16)) {
     (f16 ? rope_scalar_kernel<true> : rope_scalar_kernel<false>)<<<static_cast<unsigned>(p.tokens), kRopeThreads, 0,
                                                                     s>>>(p);
     return cudaGetLastError() == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
@@ -229,7 +231,7 @@ convrot_status convrot_rope(const void* X, int dtype, int64_t B, int64_t S, int6
   p.hp = few ? p.H : (p.H + kRopeAhead - 1) / kRopeAhead;
   if (p.hp > most) p.hp = most;
   p.tok = kRopeThreads / (p.hp * per_head);
-  if (R > 0 && p.tok > kRopeTableMax / (p.R / 2)) p.tok = kRopeTableMax / (p.R / 2);
+  if (p.R > 0 && p.tok > kRopeTableMax / (p.R / 2)) p.tok = kRopeTableMax / (p.R / 2);
   if (few && p.tok > (p.tokens + 147) / 148) p.tok = static_cast<int>((p.tokens + 147) / 148);
   const unsigned grid = static_cast<unsigned>((p.tokens + p.tok - 1) / p.tok);
   if (p.interleaved)
