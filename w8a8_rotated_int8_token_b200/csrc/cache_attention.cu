@@ -19,27 +19,26 @@
 // joins them in a fixed order, so the result does not depend on timing.
 //
 // One CTA is four warps; warp w takes keys 16 w .. 16 w + 15 of every 64-key tile
-// for all 16 MT rows. Each warp feeds itself: one lane streams its keys' codes by
-// TMA (boxes of 16 keys, 128-byte swizzle, so that a box never crosses a page)
-// and their scales by bulk copies into the warp's own ring of stages, so no warp
-// waits for another before the end of a run. A warp that issued no copies of
-// others' keys needs no producer warp beside it: with a fifth warp a quarter of
-// an SM would hold three of them at two CTAs and leave 168 registers a thread.
+// for all 16 MT rows. Each warp feeds itself: its lanes copy its keys' codes and
+// scales (16 bytes a lane, asynchronously, swizzled against bank conflicts) into
+// the warp's own ring of stages, so no warp waits for another before the end of a
+// run, and 16 keys never cross a page. TMA boxes and bulk copies of the same 16
+// keys under mbarriers took about 200 instructions a stage where these take 40,
+// as many as the softmax and P V together: 268 against XXX us for 64 sequences of
+// up to 16384 keys.
 //   S     int8 mma m16n8k32 on fragments read from shared memory, with the
 //         channels permuted alike on both sides so that a thread reads 32
 //         consecutive bytes of a key;
 //   P V   fp16 mma m16n8k16, the codes widened exactly to fp16 in registers. The
 //         weights p s_v are brought to fp16's range by a factor per row, kept so
-//         that the largest weight so far lies between 1 and 2^12: rounding one to
+//         that the largest weight so far lies between 1 and 2^15: rounding one to
 //         fp16 costs at most 2^-11 of it or 2^-25 of the largest, whatever the
 //         range of the value scales.
-// The running maximum and that factor move only when a key passes them by 2^8
-// and 2^12; a vote of the warp is all it costs otherwise.
+// The reference maximum and that factor move only when a key passes them by far;
+// a vote of the warp is all it costs otherwise.
 
-#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <atomic>
 #include <cstdint>
@@ -62,9 +61,7 @@ constexpr int CA_KT = CA_SUB * CA_WARPS;   // keys of a tile
 constexpr int CA_CODES = CA_SUB * CA_D;    // key (or value) codes of a stage
 constexpr int CA_STAGE = 2 * CA_CODES;
 constexpr int CA_QPITCH = CA_D + 16;       // bytes between query rows in shared memory
-constexpr uint64_t CA_TIMEOUT_NS = 2000000000ull;
 constexpr int CA_BAD = CONVROT_ERR_INVALID_ARG;
-constexpr int CA_TIMEOUT = CONVROT_ERR_DEVICE_TIMEOUT;
 constexpr int CA_MAX_WORKERS = 480;        // pieces the workspace has room for
 #ifndef CA_SETUP
 #define CA_SETUP 4
@@ -82,9 +79,7 @@ struct CaShape {
   static constexpr int kOffQ = kOffScale + CA_WARPS * ST * 2 * CA_SUB * 4;
   static constexpr int kOffRow = kOffQ + kRows * CA_QPITCH;   // per row: tree bits, factor, first key not seen
   static constexpr int kOffScan = kOffRow + kRows * 16;
-  static constexpr int kOffBar = kOffScan + 64;
-  static constexpr int kBytes = kOffBar + CA_WARPS * ST * 8;
-  static constexpr int kAlloc = kBytes + 1024;                // slack to align the base to 1024 bytes
+  static constexpr int kBytes = kOffScan + 64;
   // the end of a run exchanges sums through the (then idle) ring: per warp 8 KB and statistics per 16 rows
   static constexpr int kJoinWarp = MT * 16 * 32 * 16 + MT * 32 * 16;
   static_assert(2 * kJoinWarp <= kOffScale, "exchange fits the ring");
@@ -107,6 +102,8 @@ struct CaParams {
   const uint16_t* q;
   uint16_t* o;
   int64_t qt, qh, ot, oh;
+  const int8_t* k_codes;
+  const int8_t* v_codes;
   const float* k_scale;
   const float* v_scale;
   const int32_t* pages;
@@ -126,7 +123,7 @@ struct CaParams {
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -135,14 +132,14 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
 // The same with a zero accumulator.
 __device__ __forceinline__ void mma_s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
       : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -156,11 +153,28 @@ __device__ __forceinline__ float2 code_sums(int a, int b, float2 by) {
   return __fmul2_rn(__fadd2_rn(x, make_float2(-12582912.0f, -12582912.0f)), by);
 }
 
+// Sixteen bytes global -> shared, past L1.
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {  // all but the last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // The maximum of a row that has seen no key: below every logit, and finite, so that exponents of
 // differences need no special case.
 constexpr float CA_NONE = -1e30f;
+// The reference of a row moves when a logit passes it by 24 (exponentials of up to 2^24 cost float32 no
+// precision), and the factor when a weight passes 2^15 of fp16's 65504: with 8 and 2^12 a tile of 32 rows moved one of
+// them at every other step of a short run.
+constexpr float CA_RISE = 24.0f;
+constexpr float CA_MOST = 32768.0f;
+// The weights' factor of a row without a weight, and the largest there is: the first weight brings it down.
+constexpr float CA_UNSET = 0x1p100f;
 
 // A sequence: its keys, its query tokens, and its share of the line of work. An item is CA_SETUP
 // units for what every run costs (queries, first loads, the warps' join) and one for each key tile; without keys one
@@ -235,12 +249,9 @@ struct CaWalk {
 
 template <class Shape, bool F16>
 __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
-    cache_attention_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                           const CaParams p) {
+    cache_attention_kernel(const CaParams p) {
   constexpr int MT = Shape::kMt, ST = Shape::kStages, ROWS = Shape::kRows;
-  extern __shared__ uint8_t smem_raw[];
-  // aligned by an offset, not through an integer, so that the compiler still knows it is shared memory
-  uint8_t* smem = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u);
+  extern __shared__ __align__(128) uint8_t smem[];
   int64_t* scan = reinterpret_cast<int64_t*>(smem + Shape::kOffScan);  // a sum per warp; then found
   uint8_t* qs = smem + Shape::kOffQ;
   unsigned long long* row_bits = reinterpret_cast<unsigned long long*>(smem + Shape::kOffRow);
@@ -250,17 +261,14 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
   const int g = lane >> 2, t4 = lane & 3;
   uint8_t* ring = smem + warp * ST * CA_STAGE;
   float* ring_scale = reinterpret_cast<float*>(smem + Shape::kOffScale) + warp * ST * 2 * CA_SUB;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Shape::kOffBar) + warp * ST;
+  // a lane copies 16-byte chunk lane % 8 of keys lane / 8 + 4 i; chunk c of key j lies at c ^ (j % 8)
+  const uint32_t ring_to = smem_addr(ring) + (lane >> 3) * CA_D + (((lane & 7) ^ (lane >> 3)) << 4);
+  const uint32_t scale_to = smem_addr(ring_scale) + lane * 16;
+  const int8_t* k_from = p.k_codes + lane * 16;
+  const int8_t* v_from = p.v_codes + lane * 16;
+  const float* scale_from = (lane < 4 ? p.k_scale : p.v_scale) + (lane & 3) * 4;
 
   griddep_launch_dependents();  // the join's CTAs may take their places; they wait for this grid
-  if (lane == 0) {
-    for (int i = 0; i < ST; ++i) mbar_init(full + i, 1);
-    fence_mbar_init();
-  }
-  if (tid == 0) {
-    prefetch_tensormap(&tmK);
-    prefetch_tensormap(&tmV);
-  }
 
   // The piece: all tiles summed over the sequences, then the sequence it starts in.
   int bad = 0;
@@ -316,8 +324,6 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     }
   }
 
-  bool ok = true;
-  uint32_t phases = 0;  // parity of each stage's next completion
   CaRun r;
   CaCut cut{};
   while (walk.next(p, &r, bad)) {
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
       }
       continue;
     }
-    uint32_t live = 0;  // stages with copies under way
+    uint32_t live = 0;  // stages that hold keys
     auto lookup = [&](int t) {
       const int key = t * CA_KT + warp * CA_SUB;
       return t < r.t1 && key < keys ? __ldg(table + (key >> p.page_shift)) : 0;
@@ -340,24 +346,27 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     auto issue = [&](int t, int st, int page) {
       const int key = t * CA_KT + warp * CA_SUB;
       live &= ~(1u << st);
-      if (t < r.t1 && key < keys && ok) {
+      if (t < r.t1 && key < keys) {
         if (page >= 0 && page < p.num_pages) {
           live |= 1u << st;
-          if (lane == 0) {
-            // cells of a cache are fewer than 2^31
-            const int cell = ((page * p.Hkv + r.head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
-            uint8_t* to = ring + st * CA_STAGE;
-            float* sc = ring_scale + st * 2 * CA_SUB;
-            mbar_arrive_expect_tx(full + st, CA_STAGE + 2 * CA_SUB * 4);
-            tma_load_2d(to, &tmK, full + st, 0, cell);
-            bulk_load(sc, p.k_scale + cell, CA_SUB * 4, full + st);
-            tma_load_2d(to + CA_CODES, &tmV, full + st, 0, cell);
-            bulk_load(sc + CA_SUB, p.v_scale + cell, CA_SUB * 4, full + st);
+          // cells of a cache are fewer than 2^31
+          const int cell = ((page * p.Hkv + r.head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+          const int8_t* kf = k_from + static_cast<int64_t>(cell) * CA_D;
+          const int8_t* vf = v_from + static_cast<int64_t>(cell) * CA_D;
+          const uint32_t to = ring_to + st * CA_STAGE;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // four keys on, key % 8 differs in its top bit
+            const uint32_t at = ((i & 1) ? to ^ 64u : to) + i * 4 * CA_D;
+            copy_async(at, kf + i * 512);
+            copy_async(at + CA_CODES, vf + i * 512);
           }
+          if (lane < 8) copy_async(scale_to + st * (2 * CA_SUB * 4), scale_from + cell);
         } else {
           bad |= CA_BAD;  // its keys are not seen
         }
       }
+      copy_commit();
     };
     int ahead;  // page of the next tile to issue
     {
@@ -416,14 +425,14 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
         cr[m][half] = row_c[row];
       }
     }
-    float acc[MT][16][4], mx[MT][2], inv[MT][2];  // inv: the weights' factor (0: none yet)
+    float acc[MT][16][4], mx[MT][2], inv[MT][2];  // inv: the weights' factor
     float2 l2[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.0f;
       mx[m][0] = mx[m][1] = CA_NONE;
-      inv[m][0] = inv[m][1] = 0.0f;
+      inv[m][0] = inv[m][1] = CA_UNSET;
       l2[m][0] = l2[m][1] = make_float2(0.0f, 0.0f);
     }
 
@@ -433,16 +442,14 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
 #pragma unroll 1
     for (int t = r.t0; t < r.t1; ++t) {
       const int key0 = t * CA_KT + warp * CA_SUB;
+      copy_wait<ST - 1>();
+      __syncwarp();  // every lane's copies
       if (live >> st & 1) {
-        if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(full + st, phases >> st & 1, nullptr, CA_TIMEOUT_NS));
-        if (!ok) break;
-        phases ^= 1u << st;
         const uint8_t* kc = ring + st * CA_STAGE;
         const uint8_t* vc = kc + CA_CODES;
         const float* sk = ring_scale + st * 2 * CA_SUB;
         float2 s[MT][2][2];  // logits in base 2: row tile, eight keys, row of the thread
         float2 sv[2];
-        bool wild = false;   // an unseen cell's value scale is not a number
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
           const uint8_t* row = kc + (8 * n + g) * CA_D;
@@ -469,7 +476,10 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
             for (int e = 0; e < 2; ++e) {
               const int key = key0 + 8 * n + 2 * t4 + e;
               const int drafted = key - context;
-              if (key >= keys) (e ? sv[n].y : sv[n].x) = 0.0f;
+              float& f = e ? sv[n].y : sv[n].x;
+              // a value scale that is no number stays with the rows that see it, through their logit
+              const bool wild = !(fabsf(f) < INFINITY);
+              if (wild || key >= keys) f = 0.0f;
 #pragma unroll
               for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -477,11 +487,12 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
                   const int row = m * 16 + 8 * half + g;
                   const bool seen = key < keys && (key < row_lim[row] || (drafted >= 0 && drafted < 64 &&
                                                                           (row_bits[row] >> drafted & 1ull) != 0));
-                  if (!seen) (e ? s[m][n][half].y : s[m][n][half].x) = -INFINITY;
+                  float& logit = e ? s[m][n][half].y : s[m][n][half].x;
+                  if (!seen) logit = -INFINITY;
+                  else if (wild) logit = __uint_as_float(0x7FFFFFFFu);
                 }
               }
             }
-            wild |= !(fmaxf(fabsf(sv[n].x), fabsf(sv[n].y)) < INFINITY) || sv[n].x != sv[n].x || sv[n].y != sv[n].y;
           }
         }
         uint32_t pw[MT][4];
@@ -491,7 +502,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
 #pragma unroll
           for (int half = 0; half < 2; ++half)
             top[half] = fwht::fmax3f(s[m][0][half].x, s[m][0][half].y, fmaxf(s[m][1][half].x, s[m][1][half].y));
-          if (__any_sync(0xFFFFFFFFu, top[0] > mx[m][0] + 8.0f || top[1] > mx[m][1] + 8.0f)) {
+          if (__any_sync(0xFFFFFFFFu, top[0] > mx[m][0] + CA_RISE || top[1] > mx[m][1] + CA_RISE)) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
               float now = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 1));
@@ -501,8 +512,8 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
                 l2[m][half] = __fmul2_rn(l2[m][half], both(ex2_approx(mx[m][half] - now)));
                 inv[m][half] *= ex2_approx(now - mx[m][half]);
                 mx[m][half] = now;
-                if (!(inv[m][half] <= 0x1p100f)) {  // nothing that came before is left beside this key
-                  inv[m][half] = 0.0f;
+                if (!(inv[m][half] <= CA_UNSET)) {  // nothing that came before is left beside this key
+                  inv[m][half] = CA_UNSET;
 #pragma unroll
                   for (int i = 0; i < 16; ++i) acc[m][i][2 * half] = acc[m][i][2 * half + 1] = 0.0f;
                 }
@@ -520,15 +531,10 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
               const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
               l2[m][half] = __fadd2_rn(l2[m][half], pr);
               x[n][half] = __fmul2_rn(pr, sv[n]);
-              if (wild) {
-                if (pr.x == 0.0f) x[n][half].x = 0.0f;
-                if (pr.y == 0.0f) x[n][half].y = 0.0f;
-              }
             }
             big[half] = fwht::fmax3f(x[0][half].x, x[0][half].y, fmaxf(x[1][half].x, x[1][half].y));
           }
-          const bool grow = big[0] * inv[m][0] > 4096.0f || big[1] * inv[m][1] > 4096.0f ||
-                            (inv[m][0] == 0.0f && big[0] > 0.0f) || (inv[m][1] == 0.0f && big[1] > 0.0f);
+          const bool grow = big[0] * inv[m][0] > CA_MOST || big[1] * inv[m][1] > CA_MOST;
           if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -537,8 +543,8 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
               // 2^-e for the largest weight's exponent e, within float32's normal range
               const uint32_t e = min(max(__float_as_uint(now) >> 23, 27u), 227u);
               const float to = __uint_as_float((254u - e) << 23);
-              if (now > 0.0f && (inv[m][half] == 0.0f || to < inv[m][half])) {
-                const float by = inv[m][half] == 0.0f ? 1.0f : to / inv[m][half];
+              if (to < inv[m][half] && now > 0.0f) {
+                const float by = to / inv[m][half];
                 inv[m][half] = to;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -598,15 +604,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
       ahead = lookup(t + ST + 1);
       if (++st == ST) st = 0;
     }
-    if (!ok) {
-      // a wait ran out: every copy already issued lands before the shared memory is used otherwise
-      bad |= CA_TIMEOUT;
-      for (int i = 0; i < ST; ++i)
-        if (live >> i & 1) {
-          mbar_wait_bounded(full + i, phases >> i & 1, nullptr, CA_TIMEOUT_NS);
-          phases ^= 1u << i;
-        }
-    }
+    copy_wait<0>();
 
     // ---- the four warps joined through the idle ring: 2, 3 into 0, 1, then 1 into 0
     float l[MT][2];
@@ -617,7 +615,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
         l[m][half] = l2[m][half].x + l2[m][half].y;
         l[m][half] += __shfl_xor_sync(0xFFFFFFFFu, l[m][half], 1);
         l[m][half] += __shfl_xor_sync(0xFFFFFFFFu, l[m][half], 2);
-        const float by = inv[m][half] == 0.0f ? 0.0f : 1.0f / inv[m][half];
+        const float by = 1.0f / inv[m][half];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           acc[m][i][2 * half] *= by;
@@ -667,8 +665,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
         }
       }
     }
-    fence_proxy_async_smem();  // the next run's copies write where these exchanges were
-    __syncthreads();
+    __syncthreads();  // the next run's copies write where these exchanges were
     const bool whole = r.t0 == 0 && r.t1 == walk.s.tiles;
     if (r.t0 == 0 && !whole) {
       // the piece ends inside an item that begins in it: it describes the item to the join
@@ -724,8 +721,8 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     }
   }
   if (tid == 0) p.cuts[blockIdx.x] = cut;
-  const int any_bad = __syncthreads_or(bad & CA_BAD), any_late = __syncthreads_or(bad & 4);
-  if (tid == 0) p.piece_status[blockIdx.x] = any_late ? CA_TIMEOUT : any_bad ? CA_BAD : 0;
+  bad = __syncthreads_or(bad);
+  if (tid == 0) p.piece_status[blockIdx.x] = bad ? CA_BAD : 0;
 }
 
 // Joins the parts of the items that were cut: one CTA per (piece, row). The
@@ -742,8 +739,8 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(cons
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     int st = 0;
     for (int i = tid; i < p.workers; i += kJoinThreads) st |= p.piece_status[i];
-    const int any_bad = __syncthreads_or(st & CA_BAD), any_late = __syncthreads_or(st & 4);
-    if (tid == 0) *p.status = any_late ? CA_TIMEOUT : any_bad ? CA_BAD : 0;
+    st = __syncthreads_or(st);
+    if (tid == 0) *p.status = st ? CA_BAD : 0;
   }
   const CaCut cut = p.cuts[blockIdx.x];
   const int row = blockIdx.y;
@@ -824,7 +821,7 @@ bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
 }
 
 template <class Shape, bool F16>
-cudaError_t ca_launch(const CUtensorMap& tk, const CUtensorMap& tv, CaParams p, uint8_t* ws, int64_t most_rows,
+cudaError_t ca_launch(CaParams p, uint8_t* ws, int64_t most_rows,
                       cudaStream_t s) {
   static std::atomic<int> ready[64];  // SMs of a device whose attribute is set
   int dev = 0;
@@ -834,7 +831,7 @@ cudaError_t ca_launch(const CUtensorMap& tk, const CUtensorMap& tv, CaParams p, 
   int sms = known ? ready[dev].load(std::memory_order_acquire) : 0;
   if (sms == 0) {
     e = cudaFuncSetAttribute(cache_attention_kernel<Shape, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shape::kAlloc);
+                             Shape::kBytes);
     if (e != cudaSuccess) return e;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
@@ -847,7 +844,7 @@ cudaError_t ca_launch(const CUtensorMap& tk, const CUtensorMap& tv, CaParams p, 
   p.cuts = reinterpret_cast<CaCut*>(ws + lay.cuts);
   p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   p.part = reinterpret_cast<float*>(ws + lay.part);
-  cache_attention_kernel<Shape, F16><<<p.workers, CA_THREADS, Shape::kAlloc, s>>>(tk, tv, p);
+  cache_attention_kernel<Shape, F16><<<p.workers, CA_THREADS, Shape::kBytes, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
@@ -860,32 +857,6 @@ cudaError_t ca_launch(const CUtensorMap& tk, const CUtensorMap& tv, CaParams p, 
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<F16>, p, static_cast<int>(Shape::kRows));
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 ca_encoder() {
-  static std::atomic<void*> fn{nullptr};
-  void* f = fn.load(std::memory_order_acquire);
-  if (f == nullptr) {
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-}
-
-// Codes as rows of 128 bytes, boxes of a warp's 16 keys, 128-byte swizzle.
-bool ca_encode(CUtensorMap* tm, const int8_t* codes, int64_t cells) {
-  const auto enc = ca_encoder();
-  if (enc == nullptr) return false;
-  const cuuint64_t dims[2] = {CA_D, static_cast<cuuint64_t>(cells)};
-  const cuuint64_t strides[1] = {CA_D};
-  const cuuint32_t size[2] = {CA_D, CA_SUB};
-  const cuuint32_t step[2] = {1, 1};
-  return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(codes), dims, strides, size, step,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -938,6 +909,8 @@ convrot_status convrot_cache_attention(const convrot_cache_attention_args* args,
     return CONVROT_ERR_WORKSPACE;
   p.q = static_cast<const uint16_t*>(a.Q);
   p.o = static_cast<uint16_t*>(a.O);
+  p.k_codes = c.k_codes;
+  p.v_codes = c.v_codes;
   p.k_scale = c.k_scale;
   p.v_scale = c.v_scale;
   p.pages = a.pages;
@@ -952,10 +925,6 @@ convrot_status convrot_cache_attention(const convrot_cache_attention_args* args,
   p.num_pages = static_cast<int>(c.num_pages);
   while ((int64_t{1} << p.page_shift) < c.page_size) ++p.page_shift;
   p.c_scale = a.softmax_scale * 1.4426950408889634f;
-  CUtensorMap tk, tv;
-  const int64_t cells = c.num_pages * c.H * c.page_size;
-  if (!ca_encode(&tk, c.k_codes, cells) || !ca_encode(&tv, c.v_codes, cells))
-    return CONVROT_ERR_INVALID_ARG;
   // rows a tile can have at most: all of one sequence's
   const int64_t rows = (a.starts == nullptr ? 1 : a.T) * p.G;
   uint8_t* w = static_cast<uint8_t*>(a.ws);
@@ -963,9 +932,9 @@ convrot_status convrot_cache_attention(const convrot_cache_attention_args* args,
   const bool f16 = a.dtype == CONVROT_DTYPE_F16;
   cudaError_t e;
   if (ca_wide(a.T, a.B, p.G))
-    e = f16 ? ca_launch<Shape32, true>(tk, tv, p, w, rows, s) : ca_launch<Shape32, false>(tk, tv, p, w, rows, s);
+    e = f16 ? ca_launch<Shape32, true>(p, w, rows, s) : ca_launch<Shape32, false>(p, w, rows, s);
   else
-    e = f16 ? ca_launch<Shape16, true>(tk, tv, p, w, rows, s) : ca_launch<Shape16, false>(tk, tv, p, w, rows, s);
+    e = f16 ? ca_launch<Shape16, true>(p, w, rows, s) : ca_launch<Shape16, false>(p, w, rows, s);
   return e == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
 }
 
