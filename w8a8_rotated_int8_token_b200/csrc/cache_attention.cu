@@ -19,21 +19,22 @@
 // joins them in a fixed order, so the result does not depend on timing.
 //
 // One CTA is four warps; warp w takes keys 16 w .. 16 w + 15 of every 64-key tile
-// for all 16 MT rows. Each warp feeds itself: its lanes copy its keys' codes and
+// for all 8 NT rows. Each warp feeds itself: its lanes copy its keys' codes and
 // scales (16 bytes a lane, asynchronously, swizzled against bank conflicts) into
 // the warp's own ring of stages, so no warp waits for another before the end of a
 // run, and 16 keys never cross a page. TMA boxes and bulk copies of the same 16
-// keys under mbarriers took about 200 instructions a stage where these take 40,
-// as many as the softmax and P V together: 268 against XXX us for 64 sequences of
-// up to 16384 keys.
-//   S     int8 mma m16n8k32 on fragments read from shared memory, with the
-//         channels permuted alike on both sides so that a thread reads 32
-//         consecutive bytes of a key;
-//   P V   fp16 mma m16n8k16, the codes widened exactly to fp16 in registers. The
-//         weights p s_v are brought to fp16's range by a factor per row, kept so
-//         that the largest weight so far lies between 1 and 2^15: rounding one to
-//         fp16 costs at most 2^-11 of it or 2^-25 of the largest, whatever the
-//         range of the value scales.
+// keys under mbarriers took three times the instructions a stage and 268 us where
+// these took 251 (64 sequences of up to 16384 keys).
+// The keys and channels are the long side of the matrix instructions, the rows
+// the short one (8), so a tile of 8 rows, the usual one of single tokens, wastes
+// no more than it must:
+//   S^T = K Q^T      int8 m16n8k32, the key codes through ldmatrix;
+//   O^T = V^T P^T    fp16 m16n8k16: the value codes widened exactly to fp16 in
+//         registers, the weights transposed by movmatrix. The weights p s_v are
+//         brought to fp16's range by a factor per row, kept so that the largest
+//         weight so far lies between 1 and 2^15: rounding one to fp16 costs at
+//         most 2^-11 of it or 2^-25 of the largest, whatever the range of the
+//         value scales.
 // The reference maximum and that factor move only when a key passes them by far;
 // a vote of the warp is all it costs otherwise.
 
@@ -62,7 +63,7 @@ constexpr int CA_CODES = CA_SUB * CA_D;    // key (or value) codes of a stage
 constexpr int CA_STAGE = 2 * CA_CODES;
 constexpr int CA_QPITCH = CA_D + 16;       // bytes between query rows in shared memory
 constexpr int CA_BAD = CONVROT_ERR_INVALID_ARG;
-constexpr int CA_MAX_WORKERS = 480;        // pieces the workspace has room for
+constexpr int CA_MAX_WORKERS = 640;        // pieces the workspace has room for
 #ifndef CA_SETUP
 #define CA_SETUP 4
 #endif
@@ -70,23 +71,33 @@ constexpr int CA_MAX_WORKERS = 480;        // pieces the workspace has room for
 #define CA_LEAST 6
 #endif
 
-// A shape of CTA: 16 MT rows, stages of a warp's ring, CTAs per SM.
-template <int MT, int ST, int OCC>
+// A shape of CTA: 8 NT rows, stages of a warp's ring, CTAs per SM.
+template <int NT, int ST, int OCC>
 struct CaShape {
-  static constexpr int kMt = MT, kStages = ST, kOcc = OCC;
-  static constexpr int kRows = 16 * MT;
+  static constexpr int kNt = NT, kStages = ST, kOcc = OCC;
+  static constexpr int kRows = 8 * NT;
   static constexpr int kOffScale = CA_WARPS * ST * CA_STAGE;  // per stage: 16 key, 16 value scales
   static constexpr int kOffQ = kOffScale + CA_WARPS * ST * 2 * CA_SUB * 4;
   static constexpr int kOffRow = kOffQ + kRows * CA_QPITCH;   // per row: tree bits, factor, first key not seen
   static constexpr int kOffScan = kOffRow + kRows * 16;
   static constexpr int kBytes = kOffScan + 64;
-  // the end of a run exchanges sums through the (then idle) ring: per warp 8 KB and statistics per 16 rows
-  static constexpr int kJoinWarp = MT * 16 * 32 * 16 + MT * 32 * 16;
+  // the end of a run exchanges sums through the (then idle) ring: per warp 4 KB and statistics per 8 rows
+  static constexpr int kJoinWarp = NT * 8 * 32 * 16 + NT * 32 * 16;
   static_assert(2 * kJoinWarp <= kOffScale, "exchange fits the ring");
 };
 
-using Shape16 = CaShape<1, 4, 3>;
-using Shape32 = CaShape<2, 6, 2>;
+#ifndef CA_S8
+#define CA_S8 3, 4
+#endif
+#ifndef CA_S16
+#define CA_S16 4, 3
+#endif
+#ifndef CA_S32
+#define CA_S32 6, 2
+#endif
+using Shape8 = CaShape<1, CA_S8>;
+using Shape16 = CaShape<2, CA_S16>;
+using Shape32 = CaShape<4, CA_S32>;
 
 // What a piece leaves for the join: its last item, if that goes on in the next pieces.
 struct CaCut {
@@ -121,28 +132,38 @@ struct CaParams {
   int workers;
 };
 
-__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+__device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // The same with a zero accumulator.
-__device__ __forceinline__ void mma_s8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                             uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+__device__ __forceinline__ void mma_s8_first(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
       : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(0));
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four 8 x 16-byte matrices; each lane names a row of one.
+__device__ __forceinline__ void load_matrices(uint32_t (&a)[4], uint32_t from) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+               : "r"(from)
+               : "memory");
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit values.
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
 // Two sums of 128 products of codes up to 127 (|acc| < 2^22) as floats times `by`, without a conversion
@@ -153,9 +174,11 @@ __device__ __forceinline__ float2 code_sums(int a, int b, float2 by) {
   return __fmul2_rn(__fadd2_rn(x, make_float2(-12582912.0f, -12582912.0f)), by);
 }
 
-// Sixteen bytes global -> shared, past L1.
+// Sixteen bytes global -> shared, past L1, at constant offsets.
+template <int TO, int FROM>
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;" ::"r"(to), "l"(from), "n"(TO), "n"(FROM)
+               : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -175,6 +198,22 @@ constexpr float CA_RISE = 24.0f;
 constexpr float CA_MOST = 32768.0f;
 // The weights' factor of a row without a weight, and the largest there is: the first weight brings it down.
 constexpr float CA_UNSET = 0x1p100f;
+
+// The maximum of each row over the lanes that hold its keys.
+__device__ __forceinline__ float2 row_max(float2 v) {
+#pragma unroll
+  for (int m = 4; m < 32; m <<= 1) {
+    v.x = fmaxf(v.x, __shfl_xor_sync(0xFFFFFFFFu, v.x, m));
+    v.y = fmaxf(v.y, __shfl_xor_sync(0xFFFFFFFFu, v.y, m));
+  }
+  return v;
+}
+
+// 2^-e for the exponent e of a row's largest weight, within float32's normal range: it brings that weight to [1, 2).
+__device__ __forceinline__ float weight_factor(float weight) {
+  const uint32_t e = min(max(__float_as_uint(weight) >> 23, 27u), 227u);
+  return __uint_as_float((254u - e) << 23);
+}
 
 // A sequence: its keys, its query tokens, and its share of the line of work. An item is CA_SETUP
 // units for what every run costs (queries, first loads, the warps' join) and one for each key tile; without keys one
@@ -250,7 +289,7 @@ struct CaWalk {
 template <class Shape, bool F16>
 __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     cache_attention_kernel(const CaParams p) {
-  constexpr int MT = Shape::kMt, ST = Shape::kStages, ROWS = Shape::kRows;
+  constexpr int NT = Shape::kNt, ST = Shape::kStages, ROWS = Shape::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   int64_t* scan = reinterpret_cast<int64_t*>(smem + Shape::kOffScan);  // a sum per warp; then found
   uint8_t* qs = smem + Shape::kOffQ;
@@ -260,13 +299,18 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t4 = lane & 3;
   uint8_t* ring = smem + warp * ST * CA_STAGE;
-  float* ring_scale = reinterpret_cast<float*>(smem + Shape::kOffScale) + warp * ST * 2 * CA_SUB;
+  const float* ring_scale = reinterpret_cast<const float*>(smem + Shape::kOffScale) + warp * ST * 2 * CA_SUB;
   // a lane copies 16-byte chunk lane % 8 of keys lane / 8 + 4 i; chunk c of key j lies at c ^ (j % 8)
   const uint32_t ring_to = smem_addr(ring) + (lane >> 3) * CA_D + (((lane & 7) ^ (lane >> 3)) << 4);
   const uint32_t scale_to = smem_addr(ring_scale) + lane * 16;
   const int8_t* k_from = p.k_codes + lane * 16;
   const int8_t* v_from = p.v_codes + lane * 16;
   const float* scale_from = (lane < 4 ? p.k_scale : p.v_scale) + (lane & 3) * 4;
+  // the row this lane names to ldmatrix: key lane % 16, chunk lane / 16 of each pair
+  const uint32_t key_at = smem_addr(ring) + (lane & 15) * CA_D + (((lane >> 4) ^ (lane & 7)) << 4);
+  // the value chunks of a lane: channels 16 g .. 16 g + 15 of keys 2 t, 2 t + 1 (and 8 more)
+  const uint8_t* value_at = ring + CA_CODES + 2 * t4 * CA_D + ((g ^ (2 * t4)) << 4);
+  const uint8_t* value_at1 = ring + CA_CODES + (2 * t4 + 1) * CA_D + ((g ^ (2 * t4 + 1)) << 4);
 
   griddep_launch_dependents();  // the join's CTAs may take their places; they wait for this grid
 
@@ -339,29 +383,32 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
       continue;
     }
     uint32_t live = 0;  // stages that hold keys
+    // tiles of the run in which this warp has keys end before `last`
+    const int with_keys = (keys - warp * CA_SUB + CA_KT - 1) / CA_KT;
+    const int last = r.t1 < with_keys ? r.t1 : with_keys;
     auto lookup = [&](int t) {
-      const int key = t * CA_KT + warp * CA_SUB;
-      return t < r.t1 && key < keys ? __ldg(table + (key >> p.page_shift)) : 0;
+      return t < last ? __ldg(table + ((t * CA_KT + warp * CA_SUB) >> p.page_shift)) : 0;
     };
     auto issue = [&](int t, int st, int page) {
-      const int key = t * CA_KT + warp * CA_SUB;
       live &= ~(1u << st);
-      if (t < r.t1 && key < keys) {
-        if (page >= 0 && page < p.num_pages) {
+      if (t < last) {
+        if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages)) {
           live |= 1u << st;
           // cells of a cache are fewer than 2^31
-          const int cell = ((page * p.Hkv + r.head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+          const int cell = ((page * p.Hkv + r.head) << p.page_shift) +
+                           ((t * CA_KT + warp * CA_SUB) & ((1 << p.page_shift) - 1));
           const int8_t* kf = k_from + static_cast<int64_t>(cell) * CA_D;
           const int8_t* vf = v_from + static_cast<int64_t>(cell) * CA_D;
-          const uint32_t to = ring_to + st * CA_STAGE;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            // four keys on, key % 8 differs in its top bit
-            const uint32_t at = ((i & 1) ? to ^ 64u : to) + i * 4 * CA_D;
-            copy_async(at, kf + i * 512);
-            copy_async(at + CA_CODES, vf + i * 512);
-          }
-          if (lane < 8) copy_async(scale_to + st * (2 * CA_SUB * 4), scale_from + cell);
+          const uint32_t to = ring_to + st * CA_STAGE, to4 = to ^ 64u;  // four keys on, key % 8 differs in its top bit
+          copy_async<0, 0>(to, kf);
+          copy_async<512, 512>(to4, kf);
+          copy_async<1024, 1024>(to, kf);
+          copy_async<1536, 1536>(to4, kf);
+          copy_async<CA_CODES, 0>(to, vf);
+          copy_async<CA_CODES + 512, 512>(to4, vf);
+          copy_async<CA_CODES + 1024, 1024>(to, vf);
+          copy_async<CA_CODES + 1536, 1536>(to4, vf);
+          if (lane < 8) copy_async<0, 0>(scale_to + st * (2 * CA_SUB * 4), scale_from + cell);
         } else {
           bad |= CA_BAD;  // its keys are not seen
         }
@@ -411,29 +458,25 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
       }
     }
     __syncthreads();
-    uint32_t qa[MT][16];
-    float cr[MT][2];
+    uint32_t qb[NT][8];  // row g of each 8: bytes 4 t .. of every 16
+    float2 cr[NT];       // factors of rows 2 t, 2 t + 1
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int row = m * 16 + 8 * half + g;
-        const uint4 a = *reinterpret_cast<const uint4*>(qs + row * CA_QPITCH + 32 * t4);
-        const uint4 b = *reinterpret_cast<const uint4*>(qs + row * CA_QPITCH + 32 * t4 + 16);
-        qa[m][half] = a.x, qa[m][2 + half] = a.y, qa[m][4 + half] = a.z, qa[m][6 + half] = a.w;
-        qa[m][8 + half] = b.x, qa[m][10 + half] = b.y, qa[m][12 + half] = b.z, qa[m][14 + half] = b.w;
-        cr[m][half] = row_c[row];
-      }
+      for (int i = 0; i < 8; ++i)
+        qb[n][i] = *reinterpret_cast<const uint32_t*>(qs + (8 * n + g) * CA_QPITCH + 16 * i + 4 * t4);
+      cr[n] = *reinterpret_cast<const float2*>(row_c + 8 * n + 2 * t4);
     }
-    float acc[MT][16][4], mx[MT][2], inv[MT][2];  // inv: the weights' factor
-    float2 l2[MT][2];
+    // acc[n][i]: channels 16 g + 2 i (rows 2 t, 2 t + 1 of the 8), then 16 g + 2 i + 1
+    float acc[NT][8][4];
+    float2 mx[NT], l[NT], inv[NT];  // maximum, sum and weights' factor of rows 2 t, 2 t + 1
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.0f;
-      mx[m][0] = mx[m][1] = CA_NONE;
-      inv[m][0] = inv[m][1] = CA_UNSET;
-      l2[m][0] = l2[m][1] = make_float2(0.0f, 0.0f);
+      for (int i = 0; i < 8; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.0f;
+      mx[n] = both(CA_NONE);
+      inv[n] = both(CA_UNSET);
+      l[n] = make_float2(0.0f, 0.0f);
     }
 
     // ---- the keys
@@ -441,136 +484,114 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     int st = 0;
 #pragma unroll 1
     for (int t = r.t0; t < r.t1; ++t) {
-      const int key0 = t * CA_KT + warp * CA_SUB;
       copy_wait<ST - 1>();
       __syncwarp();  // every lane's copies
       if (live >> st & 1) {
-        const uint8_t* kc = ring + st * CA_STAGE;
-        const uint8_t* vc = kc + CA_CODES;
-        const float* sk = ring_scale + st * 2 * CA_SUB;
-        float2 s[MT][2][2];  // logits in base 2: row tile, eight keys, row of the thread
-        float2 sv[2];
+        const int key0 = t * CA_KT + warp * CA_SUB;
+        int d[NT][4];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const uint8_t* row = kc + (8 * n + g) * CA_D;
-          const uint4 a = *reinterpret_cast<const uint4*>(row + (((2 * t4) ^ g) << 4));
-          const uint4 b = *reinterpret_cast<const uint4*>(row + (((2 * t4 + 1) ^ g) << 4));
-          const float2 f2 = *reinterpret_cast<const float2*>(sk + 8 * n + 2 * t4);
-          sv[n] = *reinterpret_cast<const float2*>(sk + CA_SUB + 8 * n + 2 * t4);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t a[4];  // channels 32 k .. 32 k + 31 of the 16 keys
+          load_matrices(a, (key_at + st * CA_STAGE) ^ (k << 5));
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            int d[4];
-            mma_s8_first(d, qa[m][0], qa[m][1], qa[m][2], qa[m][3], a.x, a.y);
-            mma_s8(d, qa[m][4], qa[m][5], qa[m][6], qa[m][7], a.z, a.w);
-            mma_s8(d, qa[m][8], qa[m][9], qa[m][10], qa[m][11], b.x, b.y);
-            mma_s8(d, qa[m][12], qa[m][13], qa[m][14], qa[m][15], b.z, b.w);
-            s[m][n][0] = code_sums(d[0], d[1], __fmul2_rn(f2, both(cr[m][0])));
-            s[m][n][1] = code_sums(d[2], d[3], __fmul2_rn(f2, both(cr[m][1])));
+          for (int n = 0; n < NT; ++n) {
+            if (k == 0) mma_s8_first(d[n], a, qb[n][0], qb[n][1]);
+            else mma_s8(d[n], a, qb[n][2 * k], qb[n][2 * k + 1]);
           }
+        }
+        // keys g and g + 8
+        const float* sk = ring_scale + st * 2 * CA_SUB + g;
+        const float fk[2] = {sk[0], sk[8]};
+        float fv[2] = {sk[CA_SUB], sk[CA_SUB + 8]};
+        float2 s[NT][2];  // logits in base 2 of rows 2 t, 2 t + 1
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          s[n][0] = code_sums(d[n][0], d[n][1], __fmul2_rn(cr[n], both(fk[0])));
+          s[n][1] = code_sums(d[n][2], d[n][3], __fmul2_rn(cr[n], both(fk[1])));
         }
         if (key0 + CA_SUB > clear || key0 + CA_SUB > keys) {
           // keys a row does not see; their scales may be anything, so nothing computed from them is kept
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int e = 0; e < 2; ++e) {
+            const int key = key0 + g + 8 * e;
+            const int drafted = key - context;
+            // a value scale that is no number stays with the rows that see it, through their logit
+            const bool wild = !(fabsf(fv[e]) < INFINITY);
+            if (wild || key >= keys) fv[e] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int key = key0 + 8 * n + 2 * t4 + e;
-              const int drafted = key - context;
-              float& f = e ? sv[n].y : sv[n].x;
-              // a value scale that is no number stays with the rows that see it, through their logit
-              const bool wild = !(fabsf(f) < INFINITY);
-              if (wild || key >= keys) f = 0.0f;
+            for (int n = 0; n < NT; ++n) {
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  const int row = m * 16 + 8 * half + g;
-                  const bool seen = key < keys && (key < row_lim[row] || (drafted >= 0 && drafted < 64 &&
-                                                                          (row_bits[row] >> drafted & 1ull) != 0));
-                  float& logit = e ? s[m][n][half].y : s[m][n][half].x;
-                  if (!seen) logit = -INFINITY;
-                  else if (wild) logit = __uint_as_float(0x7FFFFFFFu);
-                }
+              for (int y = 0; y < 2; ++y) {
+                const int row = 8 * n + 2 * t4 + y;
+                const bool seen = key < keys && (key < row_lim[row] || (drafted >= 0 && drafted < 64 &&
+                                                                        (row_bits[row] >> drafted & 1ull) != 0));
+                float& logit = y ? s[n][e].y : s[n][e].x;
+                if (!seen) logit = -INFINITY;
+                else if (wild) logit = __uint_as_float(0x7FFFFFFFu);
               }
             }
           }
         }
-        uint32_t pw[MT][4];
+        uint32_t pw[NT][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          float top[2];
+        for (int n = 0; n < NT; ++n) {
+          float2 top = make_float2(fmaxf(s[n][0].x, s[n][1].x), fmaxf(s[n][0].y, s[n][1].y));
+          if (__any_sync(0xFFFFFFFFu, top.x > mx[n].x + CA_RISE || top.y > mx[n].y + CA_RISE)) {
+            top = row_max(top);
+            // the sums stay as they are: their unit shrinks with the weights'
+            const float2 now = make_float2(fmaxf(mx[n].x, top.x), fmaxf(mx[n].y, top.y));
+            const float2 by = make_float2(ex2_approx(mx[n].x - now.x), ex2_approx(mx[n].y - now.y));
+            l[n] = __fmul2_rn(l[n], by);
+            inv[n].x *= ex2_approx(now.x - mx[n].x);
+            inv[n].y *= ex2_approx(now.y - mx[n].y);
+            mx[n] = now;
+            // nothing that came before is left beside such a key
+            const bool fresh_x = !(inv[n].x <= CA_UNSET), fresh_y = !(inv[n].y <= CA_UNSET);
+            if (fresh_x) inv[n].x = CA_UNSET;
+            if (fresh_y) inv[n].y = CA_UNSET;
 #pragma unroll
-          for (int half = 0; half < 2; ++half)
-            top[half] = fwht::fmax3f(s[m][0][half].x, s[m][0][half].y, fmaxf(s[m][1][half].x, s[m][1][half].y));
-          if (__any_sync(0xFFFFFFFFu, top[0] > mx[m][0] + CA_RISE || top[1] > mx[m][1] + CA_RISE)) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              float now = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 1));
-              now = fmaxf(mx[m][half], fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, 2)));
-              if (now > mx[m][half]) {
-                // the sums stay as they are: their unit shrinks with the weights'
-                l2[m][half] = __fmul2_rn(l2[m][half], both(ex2_approx(mx[m][half] - now)));
-                inv[m][half] *= ex2_approx(now - mx[m][half]);
-                mx[m][half] = now;
-                if (!(inv[m][half] <= CA_UNSET)) {  // nothing that came before is left beside this key
-                  inv[m][half] = CA_UNSET;
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) acc[m][i][2 * half] = acc[m][i][2 * half + 1] = 0.0f;
-                }
-              }
+            for (int i = 0; i < 8; ++i) {
+              if (fresh_x) acc[n][i][0] = acc[n][i][2] = 0.0f;
+              if (fresh_y) acc[n][i][1] = acc[n][i][3] = 0.0f;
             }
           }
           // weights p s_v
-          float2 x[2][2];
-          float big[2];
+          const float2 away = make_float2(-mx[n].x, -mx[n].y);
+          float2 x[2];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const float2 y = __fadd2_rn(s[m][n][half], both(-mx[m][half]));
-              const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-              l2[m][half] = __fadd2_rn(l2[m][half], pr);
-              x[n][half] = __fmul2_rn(pr, sv[n]);
-            }
-            big[half] = fwht::fmax3f(x[0][half].x, x[0][half].y, fmaxf(x[1][half].x, x[1][half].y));
+          for (int e = 0; e < 2; ++e) {
+            const float2 y = __fadd2_rn(s[n][e], away);
+            const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            l[n] = __fadd2_rn(l[n], pr);
+            x[e] = __fmul2_rn(pr, both(fv[e]));
           }
-          const bool grow = big[0] * inv[m][0] > CA_MOST || big[1] * inv[m][1] > CA_MOST;
-          if (__any_sync(0xFFFFFFFFu, grow)) {
+          float2 big = make_float2(fmaxf(x[0].x, x[1].x), fmaxf(x[0].y, x[1].y));
+          if (__any_sync(0xFFFFFFFFu, big.x * inv[n].x > CA_MOST || big.y * inv[n].y > CA_MOST)) {
+            big = row_max(big);
+            const float2 to = make_float2(fminf(inv[n].x, weight_factor(big.x)), fminf(inv[n].y, weight_factor(big.y)));
+            const float2 by = make_float2(to.x / inv[n].x, to.y / inv[n].y);
+            inv[n] = to;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              float now = fmaxf(big[half], __shfl_xor_sync(0xFFFFFFFFu, big[half], 1));
-              now = fmaxf(now, __shfl_xor_sync(0xFFFFFFFFu, now, 2));
-              // 2^-e for the largest weight's exponent e, within float32's normal range
-              const uint32_t e = min(max(__float_as_uint(now) >> 23, 27u), 227u);
-              const float to = __uint_as_float((254u - e) << 23);
-              if (to < inv[m][half] && now > 0.0f) {
-                const float by = to / inv[m][half];
-                inv[m][half] = to;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  acc[m][i][2 * half] *= by;
-                  acc[m][i][2 * half + 1] *= by;
-                }
-              }
+            for (int i = 0; i < 8; ++i) {
+              acc[n][i][0] *= by.x;
+              acc[n][i][1] *= by.y;
+              acc[n][i][2] *= by.x;
+              acc[n][i][3] *= by.y;
             }
           }
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const float2 w = __fmul2_rn(x[n][half], both(inv[m][half]));
-              const __half2 h = __floats2half2_rn(w.x, w.y);
-              pw[m][2 * n + half] = *reinterpret_cast<const uint32_t*>(&h);
-            }
+          for (int e = 0; e < 2; ++e) {
+            const float2 w = __fmul2_rn(x[e], inv[n]);
+            const __half2 h = __floats2half2_rn(w.x, w.y);
+            pw[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
           }
         }
-        // values: keys 2t, 2t + 1, 2t + 8, 2t + 9, channels 16 g .. 16 g + 15
+        // values: channels 16 g .. 16 g + 15 of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
         uint4 w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = 2 * t4 + (k & 1) + 8 * (k >> 1);
-          w[k] = *reinterpret_cast<const uint4*>(vc + key * CA_D + ((g ^ (key & 7)) << 4));
-        }
+        w[0] = *reinterpret_cast<const uint4*>(value_at + st * CA_STAGE);
+        w[1] = *reinterpret_cast<const uint4*>(value_at1 + st * CA_STAGE);
+        w[2] = *reinterpret_cast<const uint4*>(value_at + st * CA_STAGE + 8 * CA_D);
+        w[3] = *reinterpret_cast<const uint4*>(value_at1 + st * CA_STAGE + 8 * CA_D);
         const __half2 offset = __floats2half2_rn(1152.0f, 1152.0f);
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
@@ -581,21 +602,18 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
 #pragma unroll
           for (int pair = 0; pair < 2; ++pair) {
             // bytes of channels 4 q4 + 2 pair and + 1 of two keys, interleaved
-            const uint32_t z0 = __byte_perm(u[0], u[1], pair ? 0x7362 : 0x5140);
-            const uint32_t z1 = __byte_perm(u[2], u[3], pair ? 0x7362 : 0x5140);
+            const uint32_t z[2] = {__byte_perm(u[0], u[1], pair ? 0x7362 : 0x5140),
+                                   __byte_perm(u[2], u[3], pair ? 0x7362 : 0x5140)};
+            uint32_t a[4];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < 4; ++e) {
               // fp16 of a code: the byte plus 128 in the low bits of 1024, minus 1152, exactly
-              const uint32_t h0 = __byte_perm(z0, 0x64646464u, e ? 0x4342 : 0x4140);
-              const uint32_t h1 = __byte_perm(z1, 0x64646464u, e ? 0x4342 : 0x4140);
-              const __half2 b0 = __hsub2(*reinterpret_cast<const __half2*>(&h0), offset);
-              const __half2 b1 = __hsub2(*reinterpret_cast<const __half2*>(&h1), offset);
-              const int i = 4 * q4 + 2 * pair + e;
-#pragma unroll
-              for (int m = 0; m < MT; ++m)
-                mma_f16(acc[m][i], pw[m], *reinterpret_cast<const uint32_t*>(&b0),
-                        *reinterpret_cast<const uint32_t*>(&b1));
+              const uint32_t h = __byte_perm(z[e >> 1], 0x64646464u, e & 1 ? 0x4342 : 0x4140);
+              const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&h), offset);
+              a[e] = *reinterpret_cast<const uint32_t*>(&c);
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(acc[n][2 * q4 + pair], a, pw[n][0], pw[n][1]);
           }
         }
       }
@@ -607,20 +625,20 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     copy_wait<0>();
 
     // ---- the four warps joined through the idle ring: 2, 3 into 0, 1, then 1 into 0
-    float l[MT][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        l[m][half] = l2[m][half].x + l2[m][half].y;
-        l[m][half] += __shfl_xor_sync(0xFFFFFFFFu, l[m][half], 1);
-        l[m][half] += __shfl_xor_sync(0xFFFFFFFFu, l[m][half], 2);
-        const float by = 1.0f / inv[m][half];
+      for (int m = 4; m < 32; m <<= 1) {
+        l[n].x += __shfl_xor_sync(0xFFFFFFFFu, l[n].x, m);
+        l[n].y += __shfl_xor_sync(0xFFFFFFFFu, l[n].y, m);
+      }
+      const float2 by = make_float2(1.0f / inv[n].x, 1.0f / inv[n].y);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          acc[m][i][2 * half] *= by;
-          acc[m][i][2 * half + 1] *= by;
-        }
+      for (int i = 0; i < 8; ++i) {
+        acc[n][i][0] *= by.x;
+        acc[n][i][1] *= by.y;
+        acc[n][i][2] *= by.x;
+        acc[n][i][3] *= by.y;
       }
     }
     __syncthreads();
@@ -630,11 +648,11 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
       if (warp >= step && warp < 2 * step) {
         float4* to = reinterpret_cast<float4*>(smem + (warp == 2 ? 0 : Shape::kJoinWarp));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            to[(m * 16 + i) * 32 + lane] = make_float4(acc[m][i][0], acc[m][i][1], acc[m][i][2], acc[m][i][3]);
-          to[MT * 512 + m * 32 + lane] = make_float4(mx[m][0], mx[m][1], l[m][0], l[m][1]);
+          for (int i = 0; i < 8; ++i)
+            to[(n * 8 + i) * 32 + lane] = make_float4(acc[n][i][0], acc[n][i][1], acc[n][i][2], acc[n][i][3]);
+          to[NT * 256 + n * 32 + lane] = make_float4(mx[n].x, mx[n].y, l[n].x, l[n].y);
         }
       }
       __syncthreads();
@@ -642,25 +660,20 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
         const float4* from =
             reinterpret_cast<const float4*>(smem + (step == 2 && warp == 0 ? 0 : Shape::kJoinWarp));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const float4 other = from[MT * 512 + m * 32 + lane];
-          float fa[2], fb[2];
+        for (int n = 0; n < NT; ++n) {
+          const float4 other = from[NT * 256 + n * 32 + lane];
+          const float2 now = make_float2(fmaxf(mx[n].x, other.x), fmaxf(mx[n].y, other.y));
+          const float2 fa = make_float2(ex2_approx(mx[n].x - now.x), ex2_approx(mx[n].y - now.y));
+          const float2 fb = make_float2(ex2_approx(other.x - now.x), ex2_approx(other.y - now.y));
+          mx[n] = now;
+          l[n] = make_float2(l[n].x * fa.x + other.z * fb.x, l[n].y * fa.y + other.w * fb.y);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float mx_b = half ? other.y : other.x, l_b = half ? other.w : other.z;
-            const float now = fmaxf(mx[m][half], mx_b);
-            fa[half] = ex2_approx(mx[m][half] - now);
-            fb[half] = ex2_approx(mx_b - now);
-            mx[m][half] = now;
-            l[m][half] = l[m][half] * fa[half] + l_b * fb[half];
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float4 o = from[(m * 16 + i) * 32 + lane];
-            acc[m][i][0] = acc[m][i][0] * fa[0] + o.x * fb[0];
-            acc[m][i][1] = acc[m][i][1] * fa[0] + o.y * fb[0];
-            acc[m][i][2] = acc[m][i][2] * fa[1] + o.z * fb[1];
-            acc[m][i][3] = acc[m][i][3] * fa[1] + o.w * fb[1];
+          for (int i = 0; i < 8; ++i) {
+            const float4 o = from[(n * 8 + i) * 32 + lane];
+            acc[n][i][0] = acc[n][i][0] * fa.x + o.x * fb.x;
+            acc[n][i][1] = acc[n][i][1] * fa.y + o.y * fb.y;
+            acc[n][i][2] = acc[n][i][2] * fa.x + o.z * fb.x;
+            acc[n][i][3] = acc[n][i][3] * fa.y + o.w * fb.y;
           }
         }
       }
@@ -678,43 +691,43 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     if (warp == 0) {
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (r.t0 == 0 ? 1 : 0);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int row = m * 16 + 8 * half + g;
-          // the thread's channels 32 t4 + i and 32 t4 + 16 + i
-          float v[32];
+        for (int y = 0; y < 2; ++y) {
+          const int row = 8 * n + 2 * t4 + y;
+          const float sum = y ? l[n].y : l[n].x;
+          float v[16];  // channels 16 g .. 16 g + 15
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            v[i] = acc[m][i][2 * half];
-            v[16 + i] = acc[m][i][2 * half + 1];
+          for (int i = 0; i < 8; ++i) {
+            v[2 * i] = acc[n][i][y];
+            v[2 * i + 1] = acc[n][i][2 + y];
           }
           if (whole) {
-            const float norm = l[m][half] > 0.0f ? fwht::kInvSqrt128 / l[m][half] : 0.0f;
+            const float norm = sum == 0.0f ? 0.0f : fwht::kInvSqrt128 / sum;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= norm;
-            fwht::reg_stage<32, 1>(v);
-            fwht::reg_stage<32, 2>(v);
-            fwht::reg_stage<32, 4>(v);
-            fwht::reg_stage<32, 8>(v);
-            fwht::reg_stage<32, 16>(v);
-            fwht::lane_stage(v, 1, (t4 & 1) != 0);
-            fwht::lane_stage(v, 2, (t4 & 2) != 0);
+            for (int i = 0; i < 16; ++i) v[i] *= norm;
+            fwht::reg_stage<16, 1>(v);
+            fwht::reg_stage<16, 2>(v);
+            fwht::reg_stage<16, 4>(v);
+            fwht::reg_stage<16, 8>(v);
+            fwht::lane_stage(v, 4, (g & 1) != 0);
+            fwht::lane_stage(v, 8, (g & 2) != 0);
+            fwht::lane_stage(v, 16, (g & 4) != 0);
             if (row < r.rows) {
               const int of = r.row0 + row, i = of / p.G;
-              uint16_t* dst = p.o + (walk.s.first + i) * p.ot + (r.head * p.G + (of - i * p.G)) * p.oh + 32 * t4;
+              uint16_t* dst = p.o + (walk.s.first + i) * p.ot + (r.head * p.G + (of - i * p.G)) * p.oh + 16 * g;
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 2; ++c)
                 *reinterpret_cast<uint4*>(dst + 8 * c) = make_uint4(
                     fwht::narrow_pair<F16>(v[8 * c], v[8 * c + 1]), fwht::narrow_pair<F16>(v[8 * c + 2], v[8 * c + 3]),
                     fwht::narrow_pair<F16>(v[8 * c + 4], v[8 * c + 5]),
                     fwht::narrow_pair<F16>(v[8 * c + 6], v[8 * c + 7]));
             }
           } else if (row < r.rows) {
-            float4* dst = reinterpret_cast<float4*>(p.part + (slot * ROWS + row) * CA_D + 32 * t4);
+            float4* dst = reinterpret_cast<float4*>(p.part + (slot * ROWS + row) * CA_D + 16 * g);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-            if (t4 == 0) p.part_ml[slot * ROWS + row] = make_float2(mx[m][half], l[m][half]);
+            for (int c = 0; c < 4; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            if (g == 0) p.part_ml[slot * ROWS + row] = make_float2(y ? mx[n].y : mx[n].x, sum);
           }
         }
       }
@@ -776,7 +789,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(cons
   partial[warp][lane] = a;
   __syncthreads();
   if (warp != 0) return;
-  const float norm = sum > 0.0f ? fwht::kInvSqrt128 / sum : 0.0f;
+  const float norm = sum == 0.0f ? 0.0f : fwht::kInvSqrt128 / sum;
   float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int w = 0; w < kJoinThreads / 32; ++w) {
@@ -813,7 +826,7 @@ CaLayout ca_layout() {
 // The tile of rows by the mean number of rows a sequence has: a wider tile
 // re-reads the keys for fewer tiles, a narrower one wastes fewer rows of the
 // matrix instructions and leaves more CTAs per SM to hide the loads.
-bool ca_wide(int64_t T, int64_t B, int64_t G) { return T * G > 16 * B; }
+int ca_rows(int64_t T, int64_t B, int64_t G) { return T * G <= 8 * B ? 8 : T * G <= 16 * B ? 16 : 32; }
 
 bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   return D == CA_D && T >= 0 && B >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hkv <= CONVROT_MAX_CACHE_HEADS &&
@@ -869,7 +882,8 @@ size_t convrot_cache_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq,
   using namespace convrot;
   if (!ca_sizes_ok(T, B, Hq, Hkv, D)) return 0;
   if (T == 0 || B == 0) return 256;
-  return ca_wide(T, B, Hq / Hkv) ? ca_layout<Shape32>().total : ca_layout<Shape16>().total;
+  const int rows = ca_rows(T, B, Hq / Hkv);
+  return rows == 8 ? ca_layout<Shape8>().total : rows == 16 ? ca_layout<Shape16>().total : ca_layout<Shape32>().total;
 }
 
 convrot_status convrot_cache_attention(const convrot_cache_attention_args* args, convrot_stream_t stream) {
@@ -931,10 +945,11 @@ convrot_status convrot_cache_attention(const convrot_cache_attention_args* args,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool f16 = a.dtype == CONVROT_DTYPE_F16;
   cudaError_t e;
-  if (ca_wide(a.T, a.B, p.G))
-    e = f16 ? ca_launch<Shape32, true>(p, w, rows, s) : ca_launch<Shape32, false>(p, w, rows, s);
-  else
-    e = f16 ? ca_launch<Shape16, true>(p, w, rows, s) : ca_launch<Shape16, false>(p, w, rows, s);
+  switch (ca_rows(a.T, a.B, p.G)) {
+    case 8: e = f16 ? ca_launch<Shape8, true>(p, w, rows, s) : ca_launch<Shape8, false>(p, w, rows, s); break;
+    case 16: e = f16 ? ca_launch<Shape16, true>(p, w, rows, s) : ca_launch<Shape16, false>(p, w, rows, s); break;
+    default: e = f16 ? ca_launch<Shape32, true>(p, w, rows, s) : ca_launch<Shape32, false>(p, w, rows, s);
+  }
   return e == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
 }
 
