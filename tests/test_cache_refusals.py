@@ -122,9 +122,9 @@ def test_attention_workspace(L):
     size = L.convrot_cache_attention_workspace_bytes
     assert size(0, 0, 8, 2, 128) == 256
     assert size(4, 4, 8, 2, 64) == 0 and size(4, 4, 7, 2, 128) == 0 and size(-1, 4, 8, 2, 128) == 0
-    # a row of sums per piece's two ends: 480 pieces, tiles of 16 or 32 rows
-    assert size(4, 4, 8, 2, 128) >= 2 * 480 * 16 * 128 * 4
-    assert size(64, 4, 8, 2, 128) >= 2 * 480 * 32 * 128 * 4
+    # a row of sums per piece's two ends: 640 pieces, tiles of 8 or 16 rows
+    assert size(4, 4, 8, 2, 128) >= 2 * 640 * 8 * 128 * 4
+    assert size(64, 4, 8, 2, 128) >= 2 * 640 * 16 * 128 * 4
 
 
 def test_binding_refuses_before_the_library():

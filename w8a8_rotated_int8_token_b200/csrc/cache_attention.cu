@@ -64,12 +64,10 @@ constexpr int CA_STAGE = 2 * CA_CODES;
 constexpr int CA_QPITCH = CA_D + 16;       // bytes between query rows in shared memory
 constexpr int CA_BAD = CONVROT_ERR_INVALID_ARG;
 constexpr int CA_MAX_WORKERS = 640;        // pieces the workspace has room for
-#ifndef CA_SETUP
-#define CA_SETUP 4
-#endif
-#ifndef CA_LEAST
-#define CA_LEAST 6
-#endif
+// What a run costs beside its tiles, and the least a piece takes, in tiles: with 6 and 6 the trees of 8 sequences took
+// 74 us against 83 with 4 and 102 with none, and one sequence of 4224 keys 12.6 us against 14.1 with a least of 8.
+constexpr int CA_SETUP = 6;
+constexpr int CA_LEAST = 6;
 
 // A shape of CTA: 8 NT rows, stages of a warp's ring, CTAs per SM.
 template <int NT, int ST, int OCC>
@@ -86,18 +84,11 @@ struct CaShape {
   static_assert(2 * kJoinWarp <= kOffScale, "exchange fits the ring");
 };
 
-#ifndef CA_S8
-#define CA_S8 3, 4
-#endif
-#ifndef CA_S16
-#define CA_S16 4, 3
-#endif
-#ifndef CA_S32
-#define CA_S32 6, 2
-#endif
-using Shape8 = CaShape<1, CA_S8>;
-using Shape16 = CaShape<2, CA_S16>;
-using Shape32 = CaShape<4, CA_S32>;
+// Two stages of 16 keys a warp at four CTAs per SM keep 130 KB of copies in flight; three stages took 3 % longer (64
+// long sequences), five CTAs with 96 registers 9 %. A tile of 32 rows with 255 registers and two CTAs took 1.1 times
+// as long as two of 16 rows on a tree of 64 drafts.
+using Shape8 = CaShape<1, 2, 4>;
+using Shape16 = CaShape<2, 3, 3>;
 
 // What a piece leaves for the join: its last item, if that goes on in the next pieces.
 struct CaCut {
@@ -738,71 +729,67 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
   if (tid == 0) p.piece_status[blockIdx.x] = bad ? CA_BAD : 0;
 }
 
-// Joins the parts of the items that were cut: one CTA per (piece, row). The
-// piece in which the item begins describes it.
-constexpr int kJoinThreads = 128;
+// Joins the parts of the items that were cut: one CTA per piece, a warp per row of
+// the item that begins in the piece (and goes on in the next ones), four channels
+// per lane.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinAhead = 8;  // parts whose loads a lane has in flight
 
 template <bool F16>
-__global__ void __launch_bounds__(kJoinThreads) cache_attention_join_kernel(const CaParams p, int rows) {
-  __shared__ float weight[CA_MAX_WORKERS];
-  __shared__ float red[2][kJoinThreads / 32];
-  __shared__ float4 partial[kJoinThreads / 32][32];
+__global__ void __launch_bounds__(32 * kJoinWarps) cache_attention_join_kernel(const CaParams p, int rows) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
+  if (blockIdx.x == 0) {
     int st = 0;
-    for (int i = tid; i < p.workers; i += kJoinThreads) st |= p.piece_status[i];
+    for (int i = tid; i < p.workers; i += 32 * kJoinWarps) st |= p.piece_status[i];
     st = __syncthreads_or(st);
     if (tid == 0) *p.status = st ? CA_BAD : 0;
   }
   const CaCut cut = p.cuts[blockIdx.x];
-  const int row = blockIdx.y;
-  if (row >= cut.rows || cut.pieces < 1) return;
-  // piece 0 of the item is slot 2 c + 1, the k-th after it slot 2 (c + k)
-  auto slot = [&](int k) { return k == 0 ? 2 * static_cast<int64_t>(blockIdx.x) + 1 : 2 * (static_cast<int64_t>(blockIdx.x) + k); };
-  float top = CA_NONE;
-  for (int k = tid; k < cut.pieces; k += kJoinThreads) top = fmaxf(top, p.part_ml[slot(k) * rows + row].x);
+  if (cut.pieces < 1) return;
+  // part 0 of the item is slot 2 c + 1, the k-th after it slot 2 (c + k)
+  auto slot = [&](int k) { return 2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? 1 : 0); };
+  for (int row = warp; row < cut.rows; row += kJoinWarps) {
+    float top = CA_NONE;
+    for (int k = lane; k < cut.pieces; k += 32) top = fmaxf(top, p.part_ml[slot(k) * rows + row].x);
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-  if (lane == 0) red[0][warp] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  float sum = 0.0f;
-  for (int k = tid; k < cut.pieces; k += kJoinThreads) {
-    const float2 ml = p.part_ml[slot(k) * rows + row];
-    const float w = ex2_approx(ml.x - top);
-    weight[k] = w;
-    sum += w * ml.y;
+    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+    float sum = 0.0f;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = 0; k0 < cut.pieces; k0 += 32) {
+      const int here = cut.pieces - k0 < 32 ? cut.pieces - k0 : 32;
+      float weight = 0.0f;
+      if (lane < here) {
+        const float2 ml = p.part_ml[slot(k0 + lane) * rows + row];
+        weight = ex2_approx(ml.x - top);
+        sum += weight * ml.y;
+      }
+      for (int j0 = 0; j0 < here; j0 += kJoinAhead) {
+        float4 o[kJoinAhead];
+#pragma unroll
+        for (int j = 0; j < kJoinAhead; ++j)
+          o[j] = j0 + j < here ? *reinterpret_cast<const float4*>(
+                                     p.part + (static_cast<int64_t>(slot(k0 + j0 + j)) * rows + row) * CA_D + 4 * lane)
+                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < kJoinAhead; ++j) {
+          const float w = __shfl_sync(0xFFFFFFFFu, weight, (j0 + j) & 31);
+          v[0] = fmaf(w, o[j].x, v[0]), v[1] = fmaf(w, o[j].y, v[1]);
+          v[2] = fmaf(w, o[j].z, v[2]), v[3] = fmaf(w, o[j].w, v[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+    const float norm = sum == 0.0f ? 0.0f : fwht::kInvSqrt128 / sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= norm;
+    fwht::fwht128_warp(v, lane);
+    const int of = cut.row0 + row, i = of / p.G;
+    uint16_t* dst = p.o + (cut.token0 + i) * p.ot + (cut.head * p.G + (of - i * p.G)) * p.oh + 4 * lane;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(fwht::narrow_pair<F16>(v[0], v[1]), fwht::narrow_pair<F16>(v[2], v[3]));
   }
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
-  if (lane == 0) red[1][warp] = sum;
-  __syncthreads();
-  sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-  for (int k = warp; k < cut.pieces; k += kJoinThreads / 32) {
-    const float4 o = *reinterpret_cast<const float4*>(p.part + (slot(k) * rows + row) * CA_D + 4 * lane);
-    const float w = weight[k];
-    a.x = fmaf(w, o.x, a.x), a.y = fmaf(w, o.y, a.y), a.z = fmaf(w, o.z, a.z), a.w = fmaf(w, o.w, a.w);
-  }
-  partial[warp][lane] = a;
-  __syncthreads();
-  if (warp != 0) return;
-  const float norm = sum == 0.0f ? 0.0f : fwht::kInvSqrt128 / sum;
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) {
-    const float4 o = partial[w][lane];
-    v[0] += o.x, v[1] += o.y, v[2] += o.z, v[3] += o.w;
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] *= norm;
-  fwht::fwht128_warp(v, lane);
-  const int of = cut.row0 + row, i = of / p.G;
-  uint16_t* dst = p.o + (cut.token0 + i) * p.ot + (cut.head * p.G + (of - i * p.G)) * p.oh + 4 * lane;
-  *reinterpret_cast<uint2*>(dst) =
-      make_uint2(fwht::narrow_pair<F16>(v[0], v[1]), fwht::narrow_pair<F16>(v[2], v[3]));
 }
 
 // ------------------------------------------------------------------------ host
@@ -826,7 +813,7 @@ CaLayout ca_layout() {
 // The tile of rows by the mean number of rows a sequence has: a wider tile
 // re-reads the keys for fewer tiles, a narrower one wastes fewer rows of the
 // matrix instructions and leaves more CTAs per SM to hide the loads.
-int ca_rows(int64_t T, int64_t B, int64_t G) { return T * G <= 8 * B ? 8 : T * G <= 16 * B ? 16 : 32; }
+int ca_rows(int64_t T, int64_t B, int64_t G) { return T * G <= 8 * B ? 8 : 16; }
 
 bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   return D == CA_D && T >= 0 && B >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hkv <= CONVROT_MAX_CACHE_HEADS &&
@@ -834,7 +821,7 @@ bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
 }
 
 template <class Shape, bool F16>
-cudaError_t ca_launch(CaParams p, uint8_t* ws, int64_t most_rows,
+cudaError_t ca_launch(CaParams p, uint8_t* ws,
                       cudaStream_t s) {
   static std::atomic<int> ready[64];  // SMs of a device whose attribute is set
   int dev = 0;
@@ -861,8 +848,8 @@ cudaError_t ca_launch(CaParams p, uint8_t* ws, int64_t most_rows,
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.workers, static_cast<unsigned>(most_rows < Shape::kRows ? most_rows : Shape::kRows));
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.gridDim = dim3(p.workers);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -882,8 +869,7 @@ size_t convrot_cache_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq,
   using namespace convrot;
   if (!ca_sizes_ok(T, B, Hq, Hkv, D)) return 0;
   if (T == 0 || B == 0) return 256;
-  const int rows = ca_rows(T, B, Hq / Hkv);
-  return rows == 8 ? ca_layout<Shape8>().total : rows == 16 ? ca_layout<Shape16>().total : ca_layout<Shape32>().total;
+  return ca_rows(T, B, Hq / Hkv) == 8 ? ca_layout<Shape8>().total : ca_layout<Shape16>().total;
 }
 
 convrot_status convrot_cache_attention(const convrot_cache_attention_args* args, convrot_stream_t stream) {
@@ -939,17 +925,14 @@ convrot_status convrot_cache_attention(const convrot_cache_attention_args* args,
   p.num_pages = static_cast<int>(c.num_pages);
   while ((int64_t{1} << p.page_shift) < c.page_size) ++p.page_shift;
   p.c_scale = a.softmax_scale * 1.4426950408889634f;
-  // rows a tile can have at most: all of one sequence's
-  const int64_t rows = (a.starts == nullptr ? 1 : a.T) * p.G;
   uint8_t* w = static_cast<uint8_t*>(a.ws);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool f16 = a.dtype == CONVROT_DTYPE_F16;
   cudaError_t e;
-  switch (ca_rows(a.T, a.B, p.G)) {
-    case 8: e = f16 ? ca_launch<Shape8, true>(p, w, rows, s) : ca_launch<Shape8, false>(p, w, rows, s); break;
-    case 16: e = f16 ? ca_launch<Shape16, true>(p, w, rows, s) : ca_launch<Shape16, false>(p, w, rows, s); break;
-    default: e = f16 ? ca_launch<Shape32, true>(p, w, rows, s) : ca_launch<Shape32, false>(p, w, rows, s);
-  }
+  if (ca_rows(a.T, a.B, p.G) == 8)
+    e = f16 ? ca_launch<Shape8, true>(p, w, s) : ca_launch<Shape8, false>(p, w, s);
+  else
+    e = f16 ? ca_launch<Shape16, true>(p, w, s) : ca_launch<Shape16, false>(p, w, s);
   return e == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
 }
 
