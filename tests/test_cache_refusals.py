@@ -85,7 +85,7 @@ def test_append_and_read(L):
         assert call(dtype=3) == 2 and call(D=64) == 2
         assert call(page=8) == 2 and call(page=48) == 2 and call(page=2048) == 2 and call(page=0) == 1
         assert call(pages=0) == 1 and call(H=0) == 1 and call(T=-1) == 1
-        assert call(H=1025) == 2 and call(pages=1 << 25) == 2 and call(T=1 << 30) == 2
+        assert call(H=1025) == 2 and call(pages=1 << 25) == 2 and call(T=1 << 29) == 2
         assert call(kt=4) == 1 and call(vh=12) == 1
         for name in ("K", "V", "slots", "kc", "vc", "ks", "vs"):
             assert call(**{name: 0}) == 1, name

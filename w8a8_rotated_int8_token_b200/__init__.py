@@ -13,6 +13,8 @@ CUDA kernels; there is no CPU path.
 
 from __future__ import annotations
 
+import functools
+
 from . import _lib
 
 __all__ = [
@@ -408,24 +410,37 @@ def convrot_attention_int8(Q, K, V, softmax_scale=None, O=None, ws=None, stream=
     return O
 
 
-def _raw_stream(index: int) -> int:
-    """The current stream of a device, as convrot_stream_t (a Stream object costs ten times as much)."""
-    import torch
+class _Torch:
+    """What the calls below use of torch, bound at the first of them: a call of a few microseconds
+    notices every import statement and attribute on its way."""
 
-    return torch._C._cuda_getCurrentRawStream(index)
+    def __getattr__(self, name):
+        import torch
+
+        self.module = torch
+        self.code = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+        self.int8, self.int32, self.int64, self.uint8 = torch.int8, torch.int32, torch.int64, torch.uint8
+        self.float32, self.float64 = torch.float32, torch.float64
+        self.dense = torch.contiguous_format
+        self.empty_like, self.empty = torch.empty_like, torch.empty
+        self.device = torch._C._cuda_getDevice
+        self.stream = torch._C._cuda_getCurrentRawStream  # a Stream object costs ten times as much
+        return object.__getattribute__(self, name)
+
+
+_T = _Torch()
 
 
 def _elsewhere(index: int, stream):
     """None if a call on tensors of device `index` runs where torch is: that device current, its
     current stream. Otherwise a context that makes it so, within which buffers are allocated
     for the stream that uses them."""
-    import torch
-
-    here = torch.cuda.current_device() == index
+    here = _T.device() == index
+    torch = _T.module
     if stream is None:
         return None if here else torch.cuda.device(index)
     ptr = _stream_ptr(stream)
-    if here and ptr == _raw_stream(index):
+    if here and ptr == _T.stream(index):
         return None
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(ptr, device=index) if ptr else torch.cuda.default_stream(index)
@@ -435,9 +450,9 @@ def _elsewhere(index: int, stream):
 
 
 def _beside(t, name, index, dtype, shape):
-    """Checks a contiguous tensor argument of the given type and shape on device `index`."""
+    """Checks a contiguous tensor argument of the given type and shape on device `index`; its address."""
     if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
-        return
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.get_device() != index:
@@ -450,15 +465,17 @@ def _beside(t, name, index, dtype, shape):
 def _head_vectors(t, name, dims=(3,)):
     """(type code, device, shape, strides) of bf16 or fp16 head vectors [..., heads, D] on a GPU whose
     channels are contiguous."""
-    code = _dtype_code(t, name)
+    code = _T.code.get(t.dtype)
     index, shape, strides = t.get_device(), t.shape, t.stride()
+    if code is not None and index >= 0 and len(shape) in dims and (strides[-1] == 1 or shape[-1] <= 1):
+        return code, index, shape, strides
+    if code is None:
+        raise TypeError(f"{name}: expected bfloat16 or float16, got {t.dtype}")
     if index < 0:
         raise ValueError(f"{name} must be on a CUDA device")
     if len(shape) not in dims:
         raise ValueError(f"{name}: expected {' or '.join(str(d) for d in dims)} dimensions, got {len(shape)}")
-    if strides[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name}: the channels of a head must be contiguous")
-    return code, index, shape, strides
+    raise ValueError(f"{name}: the channels of a head must be contiguous")
 
 
 def _output(t, name, code, index, shape):
@@ -495,13 +512,12 @@ def convrot_rope(X, positions, freq, axis, interleaved: bool = False, inverse: b
     freq float64 (radians), axis int32. `inverse` turns back, which is also the gradient.
     Y: an output of X's shape and any strides (X itself works in place); with
     Y = buf.transpose(-3, -2) the heads come out as convrot_attention_int8 takes them."""
-    import torch
-
     code, index, shape, xs = _head_vectors(X, "X", (3, 4))
-    where = _elsewhere(index, stream)
-    if where is not None:
-        with where:
-            return convrot_rope(X, positions, freq, axis, interleaved, inverse, Y)
+    if stream is not None or _T.device() != index:
+        where = _elsewhere(index, stream)
+        if where is not None:
+            with where:
+                return convrot_rope(X, positions, freq, axis, interleaved, inverse, Y)
     if len(shape) == 4:
         B, S, H, D = shape
     else:
@@ -509,10 +525,14 @@ def convrot_rope(X, positions, freq, axis, interleaved: bool = False, inverse: b
     pairs = freq.numel()
     if 2 * pairs > D:
         raise ValueError(f"freq holds {pairs} pairs, a head vector {D} channels")
-    _beside(freq, "freq", index, torch.float64, (pairs,))
-    _beside(axis, "axis", index, torch.int32, (pairs,))
+    freq_ptr = _beside(freq, "freq", index, _T.float64, (pairs,))
+    axis_ptr = _beside(axis, "axis", index, _T.int32, (pairs,))
     ptype, pshape, ps = positions.dtype, positions.shape, positions.stride()
-    if ptype is not torch.int32 and ptype is not torch.float32:
+    if ptype is _T.int32:
+        pos_code = POS_I32
+    elif ptype is _T.float32:
+        pos_code = POS_F32
+    else:
         raise TypeError(f"positions: expected int32 or float32, got {ptype}")
     if positions.get_device() != index:
         raise ValueError("positions must be on the device of the other tensors")
@@ -525,31 +545,30 @@ def convrot_rope(X, positions, freq, axis, interleaved: bool = False, inverse: b
     if pb is None or pshape[0] < 1 or pshape[-1] != S:
         raise ValueError(f"positions: expected [axes, {S}] or [axes, {B}, {S}], got {tuple(pshape)}")
     if Y is None:
-        Y = X.new_empty(shape)
-        ys = (S * H * D, H * D, D)
+        Y = _T.empty_like(X, memory_format=_T.dense)
+        yb, ys, yh = S * H * D, H * D, D
     else:
-        ys = _output(Y, "Y", code, index, shape)
-        ys = ys if len(ys) == 4 else (0, *ys)
-    args = _lib.ROPE_ARGS.pack(X.data_ptr(), Y.data_ptr(), positions.data_ptr(), freq.data_ptr(), axis.data_ptr(),
-                               B, S, H, D, 2 * pairs, xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], pshape[0], ps[0], pb,
-                               ps[-1], code, POS_I32 if ptype is torch.int32 else POS_F32, interleaved, inverse)
-    _check(lib().convrot_rope(args, _raw_stream(index)), "convrot_rope")
+        yt = _output(Y, "Y", code, index, shape)
+        yb, ys, yh = yt[:3] if len(yt) == 4 else (0, yt[0], yt[1])
+    args = _lib.ROPE_ARGS.pack(X.data_ptr(), Y.data_ptr(), positions.data_ptr(), freq_ptr, axis_ptr, B, S, H, D,
+                               2 * pairs, xs[0], xs[1], xs[2], yb, ys, yh, pshape[0], ps[0], pb, ps[-1], code, pos_code,
+                               interleaved, inverse)
+    status = (_lib._lib or lib()).convrot_rope(args, _T.stream(index))
+    if status != 0:
+        raise ConvRotError(status, "convrot_rope")
     return Y
 
 
 def _cells(index, k_codes, v_codes, k_scale, v_scale):
-    """Pages, heads and page size of the four cache tensors on device `index`, then their addresses."""
-    import torch
-
+    """The fields of convrot_cells for the four cache tensors on device `index`."""
     shape = k_codes.shape
     if len(shape) != 4 or shape[3] != 128:
         raise ValueError("k_codes must be [pages, heads, page size, 128]")
-    cells = shape[:3]
-    _beside(k_codes, "k_codes", index, torch.int8, shape)
-    _beside(v_codes, "v_codes", index, torch.int8, shape)
-    _beside(k_scale, "k_scale", index, torch.float32, cells)
-    _beside(v_scale, "v_scale", index, torch.float32, cells)
-    return (k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cells, 128)
+    pages, heads, page, _ = shape
+    cells = (pages, heads, page)
+    return (_beside(k_codes, "k_codes", index, _T.int8, shape), _beside(v_codes, "v_codes", index, _T.int8, shape),
+            _beside(k_scale, "k_scale", index, _T.float32, cells), _beside(v_scale, "v_scale", index, _T.float32, cells),
+            pages, heads, page, 128)
 
 
 def convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status=None, stream=None):
@@ -557,13 +576,12 @@ def convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status
     rotated int8 cache: token t to slot slots[t] (int32; page * page size + place; negative: skipped;
     the others must differ). Cache: codes int8 [pages, H, page size, 128], scales float32 [pages, H,
     page size]. status: an int32 [1] tensor that a slot past the cache sets to 1, or None."""
-    import torch
-
     code, index, shape, ks = _head_vectors(K, "K")
-    where = _elsewhere(index, stream)
-    if where is not None:
-        with where:
-            return convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status)
+    if stream is not None or _T.device() != index:
+        where = _elsewhere(index, stream)
+        if where is not None:
+            with where:
+                return convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status)
     code_v, index_v, shape_v, vs = _head_vectors(V, "V")
     if code_v != code or index_v != index or shape_v != shape:
         raise ValueError("V must have the shape, dtype and device of K")
@@ -571,36 +589,36 @@ def convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status
     cells = _cells(index, k_codes, v_codes, k_scale, v_scale)
     if cells[5] != H or D != 128:
         raise ValueError(f"K has {H} heads of {D} channels, the cache {cells[5]} of 128")
-    _beside(slots, "slots", index, torch.int32, (T,))
-    if status is not None:
-        _beside(status, "status", index, torch.int32, (1,))
-    args = _lib.CACHE_ARGS.pack(*cells, K.data_ptr(), V.data_ptr(), slots.data_ptr(),
-                                0 if status is None else status.data_ptr(), T, ks[0], ks[1], vs[0], vs[1], code)
-    _check(lib().convrot_cache_append(args, _raw_stream(index)), "convrot_cache_append")
+    slots_ptr = _beside(slots, "slots", index, _T.int32, (T,))
+    status_ptr = 0 if status is None else _beside(status, "status", index, _T.int32, (1,))
+    args = _lib.CACHE_ARGS.pack(*cells, K.data_ptr(), V.data_ptr(), slots_ptr, status_ptr, T, ks[0], ks[1], vs[0],
+                                vs[1], code)
+    status = (_lib._lib or lib()).convrot_cache_append(args, _T.stream(index))
+    if status != 0:
+        raise ConvRotError(status, "convrot_cache_append")
 
 
 def convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype=None, K=None, V=None, status=None,
                        stream=None):
     """Read the keys and values of slots [T] back: (K, V) [T, H, 128] in `dtype` (bf16 by default, or
     fp16); a negative slot reads as zeros. K, V: outputs with strided tokens and heads, or None."""
-    import torch
-
     index = slots.get_device()
     if index < 0:
         raise ValueError("slots must be on a CUDA device")
-    where = _elsewhere(index, stream)
-    if where is not None:
-        with where:
-            return convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype, K, V, status)
+    if stream is not None or _T.device() != index:
+        where = _elsewhere(index, stream)
+        if where is not None:
+            with where:
+                return convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype, K, V, status)
     T = slots.numel()
-    _beside(slots, "slots", index, torch.int32, (T,))
+    slots_ptr = _beside(slots, "slots", index, _T.int32, (T,))
     cells = _cells(index, k_codes, v_codes, k_scale, v_scale)
     H = cells[5]
     if dtype is None:
-        dtype = K.dtype if K is not None else V.dtype if V is not None else torch.bfloat16
-    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        dtype = K.dtype if K is not None else V.dtype if V is not None else _T.module.bfloat16
+    code = _T.code.get(dtype)
+    if code is None:
         raise TypeError(f"dtype: expected bfloat16 or float16, got {dtype}")
-    code = DTYPE_BF16 if dtype is torch.bfloat16 else DTYPE_F16
     shape = (T, H, 128)
     ks = vs = (H * 128, 128)
     if K is not None:
@@ -610,15 +628,17 @@ def convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype=None, K=
     if V is not None:
         vs = _output(V, "V", code, index, shape)
     else:
-        V = slots.new_empty(shape, dtype=dtype)
-    if status is not None:
-        _beside(status, "status", index, torch.int32, (1,))
-    args = _lib.CACHE_ARGS.pack(*cells, K.data_ptr(), V.data_ptr(), slots.data_ptr(),
-                                0 if status is None else status.data_ptr(), T, ks[0], ks[1], vs[0], vs[1], code)
-    _check(lib().convrot_cache_read(args, _raw_stream(index)), "convrot_cache_read")
+        V = _T.empty_like(K, memory_format=_T.dense)
+    status_ptr = 0 if status is None else _beside(status, "status", index, _T.int32, (1,))
+    args = _lib.CACHE_ARGS.pack(*cells, K.data_ptr(), V.data_ptr(), slots_ptr, status_ptr, T, ks[0], ks[1], vs[0],
+                                vs[1], code)
+    status = (_lib._lib or lib()).convrot_cache_read(args, _T.stream(index))
+    if status != 0:
+        raise ConvRotError(status, "convrot_cache_read")
     return K, V
 
 
+@functools.lru_cache(maxsize=1024)
 def convrot_cache_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int = 128) -> int:
     return int(lib().convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D))
 
@@ -631,52 +651,52 @@ def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, length
     (None: token b belongs to sequence b). Among its new tokens a query sees the earlier ones and
     itself, or, with tree [T] int64, those whose bit is set in its mask (at most 64 a sequence).
     See include/convrot.h."""
-    import torch
-
     code, index, shape, qs = _head_vectors(Q, "Q")
-    where = _elsewhere(index, stream)
-    if where is not None:
-        with where:
-            return convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree,
-                                           softmax_scale, O, ws)
+    if stream is not None or _T.device() != index:
+        where = _elsewhere(index, stream)
+        if where is not None:
+            with where:
+                return convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree,
+                                               softmax_scale, O, ws)
     T, Hq, D = shape
     cells = _cells(index, k_codes, v_codes, k_scale, v_scale)
     Hkv = cells[5]
     if Hkv == 0 or Hq == 0 or Hq % Hkv != 0 or D != 128:
         raise ValueError(f"{Hq} query heads of {D} channels do not divide among {Hkv} key heads of 128")
     B = lengths.numel()
-    _beside(lengths, "lengths", index, torch.int32, (B,))
-    if pages.dtype is not torch.int32:
+    lengths_ptr = _beside(lengths, "lengths", index, _T.int32, (B,))
+    if pages.dtype is not _T.int32:
         raise TypeError(f"pages: expected torch.int32, got {pages.dtype}")
     pshape, ps = pages.shape, pages.stride()
     if len(pshape) != 2 or pshape[0] != B or (ps[1] != 1 and pshape[1] > 1) or pages.get_device() != index:
         raise ValueError(f"pages must be [{B}, n] with contiguous rows on the device of the other tensors")
+    starts_ptr = tree_ptr = 0
     if starts is not None:
-        _beside(starts, "starts", index, torch.int32, (B + 1,))
+        starts_ptr = _beside(starts, "starts", index, _T.int32, (B + 1,))
     elif T != B:
         raise ValueError("without starts Q must hold one token per sequence")
     if tree is not None:
-        _beside(tree, "tree", index, torch.int64, (T,))
+        tree_ptr = _beside(tree, "tree", index, _T.int64, (T,))
     if softmax_scale is None:
         softmax_scale = 0.08838834764831845  # 1 / sqrt(128)
-    os = (Hq * D, D)
+    ot, oh = Hq * D, D
     if O is not None:
-        os = _output(O, "O", code, index, shape)
+        ot, oh, _ = _output(O, "O", code, index, shape)
     else:
-        O = Q.new_empty(shape)
+        O = _T.empty_like(Q, memory_format=_T.dense)
     if ws is None:
-        need = lib().convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D)
-        ws = Q.new_empty((max(need, 256),), dtype=torch.uint8)
-        room = need
+        room = convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D)
+        ws = Q.new_empty(room if room > 256 else 256, dtype=_T.uint8)
     else:
         if ws.get_device() != index or not ws.is_contiguous():
             raise ValueError("ws must be contiguous on the device of the other tensors")
         room = ws.numel() * ws.element_size()
     args = _lib.CACHE_ATTENTION_ARGS.pack(
-        *cells, Q.data_ptr(), O.data_ptr(), pages.data_ptr(), lengths.data_ptr(),
-        0 if starts is None else starts.data_ptr(), 0 if tree is None else tree.data_ptr(), ws.data_ptr(), room, T, Hq,
-        B, pshape[1], ps[0], qs[0], qs[1], os[0], os[1], softmax_scale, code)
-    _check(lib().convrot_cache_attention(args, _raw_stream(index)), "convrot_cache_attention")
+        *cells, Q.data_ptr(), O.data_ptr(), pages.data_ptr(), lengths_ptr, starts_ptr, tree_ptr, ws.data_ptr(), room,
+        T, Hq, B, pshape[1], ps[0], qs[0], qs[1], ot, oh, softmax_scale, code)
+    status = (_lib._lib or lib()).convrot_cache_attention(args, _T.stream(index))
+    if status != 0:
+        raise ConvRotError(status, "convrot_cache_attention")
     return O
 
 

@@ -12,6 +12,8 @@
 
 #include <cstdint>
 
+#include "fwht_dev.cuh"
+
 namespace convrot {
 
 namespace fwht {
@@ -56,15 +58,40 @@ __device__ __forceinline__ void reg_stage(float (&v)[N]) {
   }
 }
 
-// Lane l (0..3) of a vector holds channels 32 j + 8 l + e as v[8 j + e].
-__device__ __forceinline__ void fwht128_quad(float (&v)[32], int l) {
-  reg_stage<32, 16>(v);
-  reg_stage<32, 1>(v);
-  reg_stage<32, 2>(v);
-  reg_stage<32, 4>(v);
-  lane_stage(v, 2, (l & 2) != 0);
-  reg_stage<32, 8>(v);
-  lane_stage(v, 1, (l & 1) != 0);
+// One stage between lanes on packed pairs.
+template <int N>
+__device__ __forceinline__ void lane_stage2(float2 (&v)[N], int mask, bool upper) {
+  const float own = upper ? -1.0f : 1.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 q = make_float2(__shfl_xor_sync(0xFFFFFFFFu, v[i].x, mask), __shfl_xor_sync(0xFFFFFFFFu, v[i].y, mask));
+    v[i] = __ffma2_rn(make_float2(own, own), v[i], q);
+  }
+}
+
+// One stage between the packed pairs a thread holds, on index bit H.
+template <int N, int H>
+__device__ __forceinline__ void reg_stage2(float2 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if ((i & H) == 0) {
+      const float2 a = v[i], b = v[i + H];
+      v[i] = bfly_sum(a, b);
+      v[i + H] = bfly_diff(a, b);
+    }
+  }
+}
+
+// Lane l (0..3) of a vector holds channels 32 j + 8 l + e (.x) and 64 more (.y) in
+// v[8 j + e], j in {0, 1}. The stage on index bit 6, between .x and .y, has been
+// done where the pairs were made; this does the other six.
+__device__ __forceinline__ void fwht128_quad(float2 (&v)[16], int l) {
+  reg_stage2<16, 1>(v);
+  reg_stage2<16, 2>(v);
+  reg_stage2<16, 4>(v);
+  lane_stage2(v, 2, (l & 2) != 0);
+  reg_stage2<16, 8>(v);
+  lane_stage2(v, 1, (l & 1) != 0);
 }
 
 // Lane l (0..31) holds channels 4 l .. 4 l + 3.

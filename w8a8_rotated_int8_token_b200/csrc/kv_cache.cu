@@ -7,10 +7,14 @@
 // g = 128. Reading gives (c s) R, since R is its own inverse.
 //
 // Bound by memory: 256 bytes on the dense side and 132 in the cell per vector.
-// Four lanes share a vector, 32 channels each: five of the seven butterfly
-// stages stay in registers and two cross lanes (64 shuffles a lane; with 16
-// lanes a vector it would be twice the shuffles per vector), and every access
-// is 16 bytes a lane on the dense side with 64-byte runs per vector.
+// Four lanes share a key and its value, 32 channels each: five of the seven
+// butterfly stages stay in registers, packed two to an instruction, and two cross
+// lanes (64 shuffles a lane and vector; with 16 lanes it would be twice as many per
+// vector); every access on the dense side is 16 bytes a lane in runs of 64 per
+// vector. Both vectors' loads are issued before either is transformed: 32768
+// scattered tokens of 8 heads are read in 40.9 us against 47.3 with a thread per
+// vector (204 MB, 77 % of the copy bandwidth; the scales of scattered cells cost a
+// 32-byte sector each, 17 MB more).
 
 #include <cuda_runtime.h>
 
@@ -25,7 +29,7 @@ namespace convrot {
 
 namespace {
 
-constexpr int kCellThreads = 128;
+constexpr int kCellThreads = 64;
 constexpr int kCellDim = 128;
 constexpr int kBadSlot = CONVROT_ERR_INVALID_ARG;
 
@@ -38,28 +42,23 @@ struct CellParams {
   int8_t* v_codes;
   float* k_scale;            // [P, H, page]
   float* v_scale;
-  int64_t vectors;           // 2 T H
+  int pairs;                 // T H
   int H, page_shift;
   int capacity;              // P * page
   int* status;
 };
 
-// The vector of a thread: token t, head h, keys or values; its cell, or -1.
+// The key and the value of a thread: token t, head h; their cell, or -1.
 struct CellPlace {
-  int64_t t;
+  int64_t t, cell;
   int h;
-  bool value;
-  int64_t cell;
 };
 
-__device__ __forceinline__ CellPlace cell_place(const CellParams& p, int64_t vec) {
+__device__ __forceinline__ CellPlace cell_place(const CellParams& p, int pair) {
   CellPlace c;
-  const uint32_t two_h = 2u * static_cast<uint32_t>(p.H);
-  const uint32_t t = static_cast<uint32_t>(vec) / two_h;  // vectors < 2^31
-  const uint32_t rest = static_cast<uint32_t>(vec) - t * two_h;
+  const uint32_t t = static_cast<uint32_t>(pair) / static_cast<uint32_t>(p.H);
   c.t = t;
-  c.value = rest >= static_cast<uint32_t>(p.H);
-  c.h = static_cast<int>(c.value ? rest - p.H : rest);
+  c.h = pair - static_cast<int>(t) * p.H;
   const int slot = __ldg(p.slots + t);
   c.cell = -1;
   if (slot >= 0 && slot < p.capacity) {
@@ -71,95 +70,128 @@ __device__ __forceinline__ CellPlace cell_place(const CellParams& p, int64_t vec
   return c;
 }
 
+// A vector's four 16-byte pieces of a lane (channels 32 j + 8 l .. + 7) into its cell.
 template <bool F16>
-__global__ void __launch_bounds__(kCellThreads) cache_append_kernel(const CellParams p) {
-  const int64_t vec = (static_cast<int64_t>(blockIdx.x) * kCellThreads + threadIdx.x) >> 2;
-  const int l = threadIdx.x & 3;
-  const bool there = vec < p.vectors;
-  CellPlace c{};
-  c.cell = -1;
-  float v[32];
+__device__ __forceinline__ void write_cell(const uint4 (&w)[4], int l, int64_t cell, int8_t* codes, float* scales) {
+  float2 v[16];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-  if (there) {
-    c = cell_place(p, vec);
-    const uint16_t* src = c.value ? p.v + c.t * p.vt + c.h * p.vh : p.k + c.t * p.kt + c.h * p.kh;
-    uint4 w[4];
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t a[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+    const uint32_t b[4] = {w[2 + j].x, w[2 + j].y, w[2 + j].z, w[2 + j].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = __ldg(reinterpret_cast<const uint4*>(src + 32 * j + 8 * l));
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t* u = reinterpret_cast<const uint32_t*>(&w[j]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = fwht::widen_pair<F16>(u[e]);
-        v[8 * j + 2 * e] = f.x;
-        v[8 * j + 2 * e + 1] = f.y;
-      }
-    }
+    for (int e = 0; e < 4; ++e)
+      fwht::fwht_first_pair<F16>(a[e], fwht::widen_pair<F16>(b[e]), v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
   }
   fwht::fwht128_quad(v, l);
   float m[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    m[i] = fwht::fmax3f(fabsf(v[4 * i]), fabsf(v[4 * i + 1]), fmaxf(fabsf(v[4 * i + 2]), fabsf(v[4 * i + 3])));
+    m[i] = fwht::fmax3f(fabsf(v[2 * i].x), fabsf(v[2 * i].y), fmaxf(fabsf(v[2 * i + 1].x), fabsf(v[2 * i + 1].y)));
   float amax = fwht::fmax3f(fwht::fmax3f(m[0], m[1], m[2]), fwht::fmax3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
   amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-  if (c.cell < 0) return;
+  if (cell < 0) return;
   const fwht::CodeFactor f = fwht::code_factor(amax);
-  int8_t* dst = (c.value ? p.v_codes : p.k_codes) + c.cell * kCellDim;
+  const float2 ci = make_float2(f.ci, f.ci), magic = make_float2(fwht::kRoundMagic, fwht::kRoundMagic);
+  const float2 pre = make_float2(f.pre, f.pre);
+  int8_t* dst = codes + cell * kCellDim + 8 * l;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float r[8];
+  for (int j = 0; j < 2; ++j) {
+    float2 r[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = fmaf(v[8 * j + e] * f.pre, f.ci, fwht::kRoundMagic);
-    *reinterpret_cast<uint2*>(dst + 32 * j + 8 * l) =
-        make_uint2(fwht::pack4(r[0], r[1], r[2], r[3]), fwht::pack4(r[4], r[5], r[6], r[7]));
+    for (int e = 0; e < 8; ++e) r[e] = __ffma2_rn(__fmul2_rn(v[8 * j + e], pre), ci, magic);
+    *reinterpret_cast<uint2*>(dst + 32 * j) =
+        make_uint2(fwht::pack4(r[0].x, r[1].x, r[2].x, r[3].x), fwht::pack4(r[4].x, r[5].x, r[6].x, r[7].x));
+    *reinterpret_cast<uint2*>(dst + 64 + 32 * j) =
+        make_uint2(fwht::pack4(r[0].y, r[1].y, r[2].y, r[3].y), fwht::pack4(r[4].y, r[5].y, r[6].y, r[7].y));
   }
-  if (l == 0) (c.value ? p.v_scale : p.k_scale)[c.cell] = fwht::scale_of<128>(amax);
+  if (l == 0) scales[cell] = fwht::scale_of<128>(amax);
+}
+
+template <bool F16>
+__global__ void __launch_bounds__(kCellThreads) cache_append_kernel(const CellParams p) {
+  const int pair = (blockIdx.x * kCellThreads + threadIdx.x) >> 2;
+  const int l = threadIdx.x & 3;
+  CellPlace c{};
+  c.cell = -1;
+  uint4 k[4], v[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) k[j] = v[j] = make_uint4(0u, 0u, 0u, 0u);
+  if (pair < p.pairs) {
+    c = cell_place(p, pair);
+    const uint16_t* kf = p.k + c.t * p.kt + c.h * p.kh + 8 * l;
+    const uint16_t* vf = p.v + c.t * p.vt + c.h * p.vh + 8 * l;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) k[j] = __ldg(reinterpret_cast<const uint4*>(kf + 32 * j));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __ldg(reinterpret_cast<const uint4*>(vf + 32 * j));
+  }
+  write_cell<F16>(k, l, c.cell, p.k_codes, p.k_scale);
+  write_cell<F16>(v, l, c.cell, p.v_codes, p.v_scale);
+}
+
+// Byte e of a word of codes with the sign bits flipped, as a float plus 2^23 + 128.
+__device__ __forceinline__ float code_plus(uint32_t flipped, int e) {
+  return __uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7440 + e));
+}
+
+// A lane's four 8-byte pieces of codes to its channels of the vector; zeros where there is no cell.
+template <bool F16>
+__device__ __forceinline__ void read_cell(const uint2 (&w)[4], int l, float scale, bool there, bool any, uint16_t* dst) {
+  // sums of 128 codes: every stage is exact in float32
+  float2 v[16];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float a = code_plus((e < 4 ? w[j].x : w[j].y) ^ 0x80808080u, e & 3);
+      const float b = code_plus((e < 4 ? w[2 + j].x : w[2 + j].y) ^ 0x80808080u, e & 3);
+      const float2 ab = __fadd2_rn(make_float2(a, b), make_float2(-8388736.0f, -8388736.0f));
+      v[8 * j + e] = make_float2(ab.x + ab.y, ab.x - ab.y);
+    }
+  }
+  fwht::fwht128_quad(v, l);
+  if (!there) return;
+  const float by1 = scale * fwht::kInvSqrt128;
+  const float2 by = make_float2(by1, by1);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint32_t lo[4], hi[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = __fmul2_rn(v[8 * j + 2 * e], by), b = __fmul2_rn(v[8 * j + 2 * e + 1], by);
+      lo[e] = any ? fwht::narrow_pair<F16>(a.x, b.x) : 0u;
+      hi[e] = any ? fwht::narrow_pair<F16>(a.y, b.y) : 0u;
+    }
+    *reinterpret_cast<uint4*>(dst + 32 * j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    *reinterpret_cast<uint4*>(dst + 64 + 32 * j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  }
 }
 
 template <bool F16>
 __global__ void __launch_bounds__(kCellThreads) cache_read_kernel(const CellParams p) {
-  const int64_t vec = (static_cast<int64_t>(blockIdx.x) * kCellThreads + threadIdx.x) >> 2;
+  const int pair = (blockIdx.x * kCellThreads + threadIdx.x) >> 2;
   const int l = threadIdx.x & 3;
-  const bool there = vec < p.vectors;
+  const bool there = pair < p.pairs;
   CellPlace c{};
   c.cell = -1;
-  if (there) c = cell_place(p, vec);
-  float v[32];
+  if (there) c = cell_place(p, pair);
+  uint2 k[4], v[4];
+  float ks = 0.0f, vs = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-  float scale = 0.0f;
+  for (int j = 0; j < 4; ++j) k[j] = v[j] = make_uint2(0u, 0u);
   if (c.cell >= 0) {
-    const int8_t* src = (c.value ? p.v_codes : p.k_codes) + c.cell * kCellDim;
-    scale = __ldg((c.value ? p.v_scale : p.k_scale) + c.cell) * fwht::kInvSqrt128;
-    uint2 w[4];
+    const int8_t* kf = p.k_codes + c.cell * kCellDim + 8 * l;
+    const int8_t* vf = p.v_codes + c.cell * kCellDim + 8 * l;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = __ldg(reinterpret_cast<const uint2*>(src + 32 * j + 8 * l));
+    for (int j = 0; j < 4; ++j) k[j] = __ldg(reinterpret_cast<const uint2*>(kf + 32 * j));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // float of a signed byte: the byte plus 128 in the low bits of 2^23, exactly
-        const uint32_t u = (e < 4 ? w[j].x : w[j].y) ^ 0x80808080u;
-        v[8 * j + e] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440 + (e & 3))) - 8388736.0f;
-      }
-    }
+    for (int j = 0; j < 4; ++j) v[j] = __ldg(reinterpret_cast<const uint2*>(vf + 32 * j));
+    ks = __ldg(p.k_scale + c.cell);
+    vs = __ldg(p.v_scale + c.cell);
   }
-  fwht::fwht128_quad(v, l);  // sums of 128 codes: exact in float32
-  if (!there) return;
-  uint16_t* dst = c.value ? p.v + c.t * p.vt + c.h * p.vh : p.k + c.t * p.kt + c.h * p.kh;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint4 o;
-    uint32_t* u = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      u[e] = c.cell < 0 ? 0u : fwht::narrow_pair<F16>(v[8 * j + 2 * e] * scale, v[8 * j + 2 * e + 1] * scale);
-    *reinterpret_cast<uint4*>(dst + 32 * j + 8 * l) = o;
-  }
+  read_cell<F16>(k, l, ks, there, c.cell >= 0, p.k + c.t * p.kt + c.h * p.kh + 8 * l);
+  read_cell<F16>(v, l, vs, there, c.cell >= 0, p.v + c.t * p.vt + c.h * p.vh + 8 * l);
 }
 
 bool aligned_to(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
@@ -174,7 +206,7 @@ convrot_status cell_params(const convrot_cache_args* args, CellParams* p) {
   if (a.T < 0 || c.H < 1 || c.num_pages < 1 || c.page_size < 1) return CONVROT_ERR_INVALID_ARG;
   if (c.page_size < CONVROT_MIN_PAGE || c.page_size > CONVROT_MAX_PAGE || (c.page_size & (c.page_size - 1)) != 0)
     return CONVROT_ERR_UNSUPPORTED;
-  if (c.H > CONVROT_MAX_CACHE_HEADS || c.num_pages > 0x7FFFFFFF / c.page_size || a.T > 0x3FFFFFFF / c.H)
+  if (c.H > CONVROT_MAX_CACHE_HEADS || c.num_pages > 0x7FFFFFFF / c.page_size || a.T > 0x1FFFFFFF / c.H)
     return CONVROT_ERR_UNSUPPORTED;
   auto stride = [](int64_t n, int64_t st) { return n > 1 ? st : 0; };
   p->kt = stride(a.T, a.k_token), p->kh = stride(c.H, a.k_head);
@@ -193,7 +225,7 @@ convrot_status cell_params(const convrot_cache_args* args, CellParams* p) {
   p->v_codes = c.v_codes;
   p->k_scale = c.k_scale;
   p->v_scale = c.v_scale;
-  p->vectors = 2 * a.T * c.H;
+  p->pairs = static_cast<int>(a.T * c.H);
   p->H = static_cast<int>(c.H);
   p->page_shift = 0;
   while ((int64_t{1} << p->page_shift) < c.page_size) ++p->page_shift;
@@ -203,7 +235,7 @@ convrot_status cell_params(const convrot_cache_args* args, CellParams* p) {
 }
 
 unsigned cell_grid(const CellParams& p) {
-  return static_cast<unsigned>((p.vectors * 4 + kCellThreads - 1) / kCellThreads);
+  return (static_cast<unsigned>(p.pairs) * 4 + kCellThreads - 1) / kCellThreads;
 }
 
 }  // namespace

@@ -14,7 +14,9 @@
 // tokens; hp x (D/16) threads share a token, and a thread keeps the same eight
 // pairs for every head it visits, so their sines and cosines are read from
 // shared memory once. The first four heads' loads are issued before the angles
-// are computed.
+// are computed. Six CTAs of 128 threads per SM (80 registers): 43.9 us for 16896
+// tokens of 32 heads, 98 % of the copy bandwidth; CTAs of 256 threads took 46.2 to
+// 53.8 us, two heads ahead 49.5.
 
 #include <cuda_runtime.h>
 
@@ -27,8 +29,8 @@ namespace convrot {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeAhead = 4;         // heads whose loads a thread has in flight
+constexpr int kRopeThreads = 128;
+constexpr int kRopeAhead = 4;        // heads whose loads a thread has in flight
 constexpr int kRopeMaxDim = 512;
 constexpr int kRopeTableMax = 2048;   // sine/cosine pairs a CTA holds (16 KB)
 
@@ -88,7 +90,7 @@ __device__ __forceinline__ void rope_apply(uint4& lo, uint4& hi, const float2 (&
 
 // Sixteen-byte accesses: D and R multiples of 16, pointers and strides of 16 bytes.
 template <bool F16, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const RopeParams p) {
   __shared__ float2 table[kRopeTableMax];
   const int per_head = p.D >> 4, pairs = p.R >> 1;
   const int group = p.hp * per_head;  // threads of a token
