@@ -45,6 +45,7 @@
 #include <cstdint>
 #include <initializer_list>
 
+#include "cache_attention.cuh"
 #include "convrot.h"
 #include "fwht128.cuh"
 #include "fwht_dev.cuh"
@@ -54,7 +55,6 @@ namespace convrot {
 
 namespace {
 
-constexpr int CA_D = 128;
 constexpr int CA_WARPS = 4;
 constexpr int CA_THREADS = 32 * CA_WARPS;
 constexpr int CA_SUB = 16;                 // keys of a warp's stage
@@ -62,8 +62,6 @@ constexpr int CA_KT = CA_SUB * CA_WARPS;   // keys of a tile
 constexpr int CA_CODES = CA_SUB * CA_D;    // key (or value) codes of a stage
 constexpr int CA_STAGE = 2 * CA_CODES;
 constexpr int CA_QPITCH = CA_D + 16;       // bytes between query rows in shared memory
-constexpr int CA_BAD = CONVROT_ERR_INVALID_ARG;
-constexpr int CA_MAX_WORKERS = 640;        // pieces the workspace has room for
 // What a run costs beside its tiles, and the least a piece takes, in tiles: with 6 and 6 the trees of 8 sequences took
 // 74 us against 83 with 4 and 102 with none, and one sequence of 4224 keys 12.6 us against 14.1 with a least of 8.
 constexpr int CA_SETUP = 6;
@@ -89,39 +87,6 @@ struct CaShape {
 // as long as two of 16 rows on a tree of 64 drafts.
 using Shape8 = CaShape<1, 2, 4>;
 using Shape16 = CaShape<2, 3, 3>;
-
-// What a piece leaves for the join: its last item, if that goes on in the next pieces.
-struct CaCut {
-  int pieces;       // pieces that hold a part of the item (0: nothing to join)
-  int rows;         // rows of the tile
-  int row0;         // first row of the tile in the sequence's rows
-  int head;         // key head
-  int token0;       // first query token of the sequence
-  int pad[3];
-};
-
-struct CaParams {
-  const uint16_t* q;
-  uint16_t* o;
-  int64_t qt, qh, ot, oh;
-  const int8_t* k_codes;
-  const int8_t* v_codes;
-  const float* k_scale;
-  const float* v_scale;
-  const int32_t* pages;
-  const int32_t* lengths;
-  const int32_t* starts;      // null: token b belongs to sequence b
-  const unsigned long long* tree;  // null: causal
-  int64_t table_stride;
-  int T, B, Hkv, G, table_pages, num_pages, page_shift;
-  float c_scale;              // softmax_scale log2(e)
-  int* piece_status;          // [workers]
-  CaCut* cuts;                // [workers]
-  float* part;                // [2 workers][rows][128]
-  float2* part_ml;            // [2 workers][rows] maximum, sum
-  int* status;                // the call's status word, written by the join
-  int workers;
-};
 
 __device__ __forceinline__ void mma_s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -179,9 +144,6 @@ __device__ __forceinline__ void copy_wait() {  // all but the last N groups have
 
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// The maximum of a row that has seen no key: below every logit, and finite, so that exponents of
-// differences need no special case.
-constexpr float CA_NONE = -1e30f;
 // The reference of a row moves when a logit passes it by 24 (exponentials of up to 2^24 cost float32 no
 // precision), and the factor when a weight passes 2^15 of fp16's 65504: with 8 and 2^12 a tile of 32 rows moved one of
 // them at every other step of a short run.
@@ -206,80 +168,10 @@ __device__ __forceinline__ float weight_factor(float weight) {
   return __uint_as_float((254u - e) << 23);
 }
 
-// A sequence: its keys, its query tokens, and its share of the line of work. An item is CA_SETUP
-// units for what every run costs (queries, first loads, the warps' join) and one for each key tile; without keys one
-// unit, in which its rows are zeroed.
-struct CaSeq {
-  int keys, first, news;
-  int tiles, span;  // key tiles and units of an item
-  int64_t count;    // units of all its items
-};
-
-template <int ROWS>
-__device__ __forceinline__ CaSeq ca_seq(const CaParams& p, int b, int& bad) {
-  CaSeq s;
-  const int64_t room = static_cast<int64_t>(p.table_pages) << p.page_shift;
-  int keys = __ldg(p.lengths + b), lo = b, hi = b + 1;
-  if (p.starts != nullptr) lo = __ldg(p.starts + b), hi = __ldg(p.starts + b + 1);
-  if (keys < 0 || keys > room || lo < 0 || hi < lo || hi > p.T) bad |= CA_BAD;
-  keys = keys < 0 ? 0 : keys > room ? static_cast<int>(room) : keys;
-  lo = lo < 0 ? 0 : lo > p.T ? p.T : lo;
-  hi = hi < lo ? lo : hi > p.T ? p.T : hi;
-  s.keys = keys;
-  s.first = lo;
-  s.news = hi - lo;
-  s.tiles = static_cast<int>((static_cast<uint32_t>(keys) + CA_KT - 1) / CA_KT);
-  s.span = s.tiles > 0 ? s.tiles + CA_SETUP : 1;
-  const uint32_t tall = (static_cast<uint32_t>(s.news) * static_cast<uint32_t>(p.G) + ROWS - 1) / ROWS;  // < 2^30
-  s.count = static_cast<int64_t>(tall * static_cast<uint32_t>(p.Hkv)) * s.span;
-  return s;
-}
-
-// A run of one item's tiles within a piece.
-struct CaRun {
-  int head, row0, rows, t0, t1;
-  int left;  // units of the item behind the run
-};
-
-// Walks a piece: the runs from `pos` to `end`, the same for every warp.
-template <int ROWS>
-struct CaWalk {
-  int64_t pos, end, base;
-  int b;
-  CaSeq s;
-  __device__ __forceinline__ bool next(const CaParams& p, CaRun* r, int& bad) {
-    while (pos < end) {
-      while (pos >= base + s.count) {
-        base += s.count;
-        ++b;
-        s = ca_seq<ROWS>(p, b, bad);  // pos < total, so a sequence with work follows
-      }
-      const int64_t rel = pos - base;
-      int64_t item;
-      if (rel < (int64_t{1} << 32)) item = static_cast<uint32_t>(rel) / static_cast<uint32_t>(s.span);
-      else item = rel / s.span;
-      const int u0 = static_cast<int>(rel - item * s.span);
-      const int take = end - pos < s.span - u0 ? static_cast<int>(end - pos) : s.span - u0;
-      pos += take;
-      const int setup = s.tiles > 0 ? CA_SETUP : 0;
-      r->t0 = u0 > setup ? u0 - setup : 0;
-      r->t1 = u0 + take > setup ? u0 + take - setup : 0;
-      if (r->t1 <= r->t0) continue;  // the piece ends before the item's first tile
-      r->left = s.span - u0 - take;
-      const uint32_t tall = static_cast<uint32_t>(item) / static_cast<uint32_t>(p.Hkv);  // items of a sequence < 2^32
-      r->head = static_cast<int>(static_cast<uint32_t>(item) - tall * p.Hkv);
-      r->row0 = static_cast<int>(tall * ROWS);
-      const int rows = s.news * p.G - r->row0;
-      r->rows = rows < ROWS ? rows : ROWS;
-      return true;
-    }
-    return false;
-  }
-};
-
 template <class Shape, bool F16>
 __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
     cache_attention_kernel(const CaParams p) {
+  using Grain = CaGrain<Shape::kRows, CA_KT, CA_SETUP, CA_LEAST>;
   constexpr int NT = Shape::kNt, ST = Shape::kStages, ROWS = Shape::kRows;
   extern __shared__ __align__(128) uint8_t smem[];
   int64_t* scan = reinterpret_cast<int64_t*>(smem + Shape::kOffScan);  // a sum per warp; then found
@@ -305,59 +197,9 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
 
   griddep_launch_dependents();  // the join's CTAs may take their places; they wait for this grid
 
-  // The piece: all tiles summed over the sequences, then the sequence it starts in.
   int bad = 0;
-  CaWalk<ROWS> walk{};
-  int64_t per = 0;
-  {
-    int64_t mine = 0, sum = 0;
-    for (int b = tid; b < p.B; b += CA_THREADS) {
-      const int64_t count = ca_seq<ROWS>(p, b, bad).count;
-      if (b == tid) mine = count;
-      sum += count;
-    }
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
-    if (lane == 0) scan[warp] = sum;
-    __syncthreads();
-    const int64_t total = (scan[0] + scan[1]) + (scan[2] + scan[3]);
-    per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < CA_LEAST) per = CA_LEAST;
-    walk.pos = blockIdx.x * per;
-    walk.end = walk.pos + per < total ? walk.pos + per : total;
-    if (walk.pos < total) {
-      int64_t before = 0;
-      for (int b0 = 0; b0 < p.B; b0 += CA_THREADS) {
-        const int b = b0 + tid;
-        int64_t count = mine;
-        if (b0 > 0) count = b < p.B ? ca_seq<ROWS>(p, b, bad).count : 0;
-        int64_t incl = count;
-#pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-          const int64_t other = __shfl_up_sync(0xFFFFFFFFu, incl, m);
-          if (lane >= m) incl += other;
-        }
-        __syncthreads();  // the sums before have been read
-        if (lane == 31) scan[warp] = incl;
-        __syncthreads();
-        int64_t lo = before + incl - count;
-#pragma unroll
-        for (int w = 0; w < CA_WARPS; ++w) {
-          if (w < warp) lo += scan[w];
-          before += scan[w];
-        }
-        if (lo <= walk.pos && walk.pos < lo + count) {
-          scan[4] = b;
-          scan[5] = lo;
-        }
-        if (walk.pos < before) break;  // the same for every thread
-      }
-      __syncthreads();
-      walk.b = static_cast<int>(scan[4]);
-      walk.base = scan[5];
-      walk.s = ca_seq<ROWS>(p, walk.b, bad);
-    }
-  }
+  CaWalk<Grain> walk{};
+  const int64_t per = ca_piece<Grain, CA_THREADS>(p, scan, &walk, bad);
 
   CaRun r;
   CaCut cut{};
@@ -739,17 +581,17 @@ template <bool F16>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_attention_join_kernel(const CaParams p, int rows) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_wait();
-  if (blockIdx.x == 0) {
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
     int st = 0;
     for (int i = tid; i < p.workers; i += 32 * kJoinWarps) st |= p.piece_status[i];
-    st = __syncthreads_or(st);
-    if (tid == 0) *p.status = st ? CA_BAD : 0;
+    const int any_bad = __syncthreads_or(st & CA_BAD), late = __syncthreads_or(st & 4);  // a timeout is 5
+    if (tid == 0) *p.status = late ? CA_LATE : any_bad ? CA_BAD : 0;
   }
   const CaCut cut = p.cuts[blockIdx.x];
   if (cut.pieces < 1) return;
   // part 0 of the item is slot 2 c + 1, the k-th after it slot 2 (c + k)
   auto slot = [&](int k) { return 2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? 1 : 0); };
-  for (int row = warp; row < cut.rows; row += kJoinWarps) {
+  for (int row = blockIdx.y * kJoinWarps + warp; row < cut.rows; row += kJoinWarps * gridDim.y) {
     float top = CA_NONE;
     for (int k = lane; k < cut.pieces; k += 32) top = fmaxf(top, p.part_ml[slot(k) * rows + row].x);
 #pragma unroll
@@ -798,22 +640,27 @@ struct CaLayout {
   size_t status, cuts, ml, part, total;
 };
 
-template <class Shape>
-CaLayout ca_layout() {
+CaLayout ca_layout(int rows) {
+  const size_t workers = rows == CA_WIDE_ROWS ? CA_WIDE_WORKERS : CA_MAX_WORKERS;
   CaLayout w;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   w.status = 256;
-  w.cuts = up(w.status + CA_MAX_WORKERS * sizeof(int));
-  w.ml = up(w.cuts + CA_MAX_WORKERS * sizeof(CaCut));
-  w.part = up(w.ml + 2 * static_cast<size_t>(CA_MAX_WORKERS) * Shape::kRows * sizeof(float2));
-  w.total = up(w.part + 2 * static_cast<size_t>(CA_MAX_WORKERS) * Shape::kRows * CA_D * sizeof(float));
+  w.cuts = up(w.status + workers * sizeof(int));
+  w.ml = up(w.cuts + workers * sizeof(CaCut));
+  w.part = up(w.ml + 2 * workers * rows * sizeof(float2));
+  w.total = up(w.part + 2 * workers * rows * CA_D * sizeof(float));
   return w;
 }
 
-// The tile of rows by the mean number of rows a sequence has: a wider tile
+#ifndef CA_WIDE_FROM
+#define CA_WIDE_FROM 32
+#endif
+// The tile of rows by the mean number of rows a sequence has for a key head: a wider tile
 // re-reads the keys for fewer tiles, a narrower one wastes fewer rows of the
 // matrix instructions and leaves more CTAs per SM to hide the loads.
-int ca_rows(int64_t T, int64_t B, int64_t G) { return T * G <= 8 * B ? 8 : 16; }
+int ca_rows(int64_t T, int64_t B, int64_t G) {
+  return T * G <= 8 * B ? 8 : T * G <= 16 * B ? 16 : T * G <= CA_WIDE_FROM * B ? 16 : CA_WIDE_ROWS;
+}
 
 bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   return D == CA_D && T >= 0 && B >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hkv <= CONVROT_MAX_CACHE_HEADS &&
@@ -821,34 +668,39 @@ bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
 }
 
 template <class Shape, bool F16>
-cudaError_t ca_launch(CaParams p, uint8_t* ws,
-                      cudaStream_t s) {
-  static std::atomic<int> ready[64];  // SMs of a device whose attribute is set
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
+cudaError_t ca_launch(const CaParams& p, int dev, cudaStream_t s) {
+  static std::atomic<int> ready[64];  // devices whose attribute is set
   const bool known = dev >= 0 && dev < 64;
-  int sms = known ? ready[dev].load(std::memory_order_acquire) : 0;
-  if (sms == 0) {
-    e = cudaFuncSetAttribute(cache_attention_kernel<Shape, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shape::kBytes);
+  if (!known || ready[dev].load(std::memory_order_acquire) == 0) {
+    const cudaError_t e = cudaFuncSetAttribute(cache_attention_kernel<Shape, F16>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes);
     if (e != cudaSuccess) return e;
-    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    if (known) ready[dev].store(sms, std::memory_order_release);
+    if (known) ready[dev].store(1, std::memory_order_release);
   }
-  const CaLayout lay = ca_layout<Shape>();
-  p.workers = sms * Shape::kOcc < CA_MAX_WORKERS ? sms * Shape::kOcc : CA_MAX_WORKERS;
+  cache_attention_kernel<Shape, F16><<<p.workers, CA_THREADS, Shape::kBytes, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t ca_run(CaParams p, int rows, bool f16, int64_t cells, uint8_t* ws, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int most = rows == CA_WIDE_ROWS ? CA_WIDE_WORKERS : CA_MAX_WORKERS;
+  const int want = sms * (rows == 8 ? Shape8::kOcc : rows == 16 ? Shape16::kOcc : 1);
+  const CaLayout lay = ca_layout(rows);
+  p.workers = want < most ? want : most;
   p.status = reinterpret_cast<int*>(ws);
   p.piece_status = reinterpret_cast<int*>(ws + lay.status);
   p.cuts = reinterpret_cast<CaCut*>(ws + lay.cuts);
   p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
   p.part = reinterpret_cast<float*>(ws + lay.part);
-  cache_attention_kernel<Shape, F16><<<p.workers, CA_THREADS, Shape::kBytes, s>>>(p);
-  e = cudaGetLastError();
+  if (rows == 8) e = f16 ? ca_launch<Shape8, true>(p, dev, s) : ca_launch<Shape8, false>(p, dev, s);
+  else if (rows == 16) e = f16 ? ca_launch<Shape16, true>(p, dev, s) : ca_launch<Shape16, false>(p, dev, s);
+  else e = launch_cache_attention_wide(p, f16, cells, s);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.workers);
+  cfg.gridDim = dim3(p.workers, (rows + kJoinWarps - 1) / kJoinWarps);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
@@ -856,7 +708,8 @@ cudaError_t ca_launch(CaParams p, uint8_t* ws,
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<F16>, p, static_cast<int>(Shape::kRows));
+  return f16 ? cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<true>, p, rows)
+             : cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<false>, p, rows);
 }
 
 }  // namespace
@@ -869,7 +722,7 @@ size_t convrot_cache_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq,
   using namespace convrot;
   if (!ca_sizes_ok(T, B, Hq, Hkv, D)) return 0;
   if (T == 0 || B == 0) return 256;
-  return ca_rows(T, B, Hq / Hkv) == 8 ? ca_layout<Shape8>().total : ca_layout<Shape16>().total;
+  return ca_layout(ca_rows(T, B, Hq / Hkv)).total;
 }
 
 convrot_status convrot_cache_attention(const convrot_cache_attention_args* args, convrot_stream_t stream) {
@@ -925,14 +778,8 @@ convrot_status convrot_cache_attention(const convrot_cache_attention_args* args,
   p.num_pages = static_cast<int>(c.num_pages);
   while ((int64_t{1} << p.page_shift) < c.page_size) ++p.page_shift;
   p.c_scale = a.softmax_scale * 1.4426950408889634f;
-  uint8_t* w = static_cast<uint8_t*>(a.ws);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool f16 = a.dtype == CONVROT_DTYPE_F16;
-  cudaError_t e;
-  if (ca_rows(a.T, a.B, p.G) == 8)
-    e = f16 ? ca_launch<Shape8, true>(p, w, s) : ca_launch<Shape8, false>(p, w, s);
-  else
-    e = f16 ? ca_launch<Shape16, true>(p, w, s) : ca_launch<Shape16, false>(p, w, s);
+  const cudaError_t e = ca_run(p, ca_rows(a.T, a.B, p.G), a.dtype == CONVROT_DTYPE_F16, c.num_pages * c.H * c.page_size,
+                               static_cast<uint8_t*>(a.ws), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;
 }
 
