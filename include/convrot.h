@@ -511,10 +511,13 @@ CONVROT_API convrot_status convrot_cache_read(const convrot_cache_args* args, co
  *             page_size] (the nearest bound is used), a page outside
  *             [0, num_pages) (its keys are not seen), or the starts did not rise
  *             within [0, T] (they are clamped).
- * Keys are read once per 16, 32 or 64 query rows (n * Hq / Hkv rows per key
- * head), so this is the form for single tokens, drafts and short chunks; long
- * prompts belong to convrot_attention_int8. Two kernels; how the work is cut
- * follows from the lengths, and the result does not depend on timing.
+ * Keys are read once per tile of 8, 16 or 128 query rows (n * Hq / Hkv rows per
+ * key head; the tile follows from T, B and the heads), so this is the form for
+ * single tokens, drafts and chunks; long prompts belong to
+ * convrot_attention_int8. Two kernels; how the work is cut follows from the
+ * lengths, and the result does not depend on timing. A timed-out wait (the tile
+ * of 128 rows waits on its own copies and products) sets the status word to
+ * CONVROT_ERR_DEVICE_TIMEOUT.
  */
 CONVROT_API size_t convrot_cache_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
 typedef struct {

@@ -137,6 +137,33 @@ template <class Grain, int THREADS>
 __device__ __forceinline__ int64_t ca_piece(const CaParams& p, int64_t* scan, CaWalk<Grain>* walk, int& bad) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (THREADS <= 128 && p.B <= 32) {  // every warp finds it by itself (not worth its registers in the wide kernel)
+    const CaSeq s = ca_seq<Grain>(p, lane < p.B ? lane : p.B - 1, bad);
+    const int64_t count = lane < p.B ? s.count : 0;
+    int64_t incl = count;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int64_t other = __shfl_up_sync(0xFFFFFFFFu, incl, m);
+      if (lane >= m) incl += other;
+    }
+    const int64_t total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < Grain::kLeast) per = Grain::kLeast;
+    walk->pos = blockIdx.x * per;
+    walk->end = walk->pos + per < total ? walk->pos + per : total;
+    if (walk->pos < total) {
+      const uint32_t past = __ballot_sync(0xFFFFFFFFu, incl > walk->pos);
+      walk->b = __ffs(past) - 1;
+      walk->base = __shfl_sync(0xFFFFFFFFu, incl - count, walk->b);
+      walk->s.keys = __shfl_sync(0xFFFFFFFFu, s.keys, walk->b);
+      walk->s.first = __shfl_sync(0xFFFFFFFFu, s.first, walk->b);
+      walk->s.news = __shfl_sync(0xFFFFFFFFu, s.news, walk->b);
+      walk->s.tiles = __shfl_sync(0xFFFFFFFFu, s.tiles, walk->b);
+      walk->s.span = __shfl_sync(0xFFFFFFFFu, s.span, walk->b);
+      walk->s.count = __shfl_sync(0xFFFFFFFFu, s.count, walk->b);
+    }
+    return per;
+  }
   int64_t mine = 0, sum = 0;
   for (int b = tid; b < p.B; b += THREADS) {
     const int64_t count = ca_seq<Grain>(p, b, bad).count;

@@ -6,21 +6,27 @@
 // attention: one exponential per row and key and five or six instructions beside it.
 // One CTA per SM, two pipelines in it that take turns over the key tiles, so that
 // one's softmax runs while the other's products do; each has its own sums (O in
-// TMEM, maximum and row sum in registers), joined at the end of a run:
+// TMEM, reference and row sum in registers), joined at the end of a run:
 //   warps 0-3, 4-7 : softmax of pipeline 0 and 1, a query row per thread: S from
 //                    TMEM, logits, weights p s_v in fp16 into swizzled shared memory;
 //   warps 8-11     : the tile's values, widened exactly from int8 to fp16 into the
-//                    (MN-major) operand of P V, and its scales;
+//                    (MN-major) operand of P V, and its scales; the loads run a
+//                    tile and two tiles ahead;
 //   warp 12        : key codes by TMA (boxes of 16 keys: pages are no smaller);
 //   warp 13        : issues S = Q K^T (kind::i8, 128 x 128 x 128) and O += P V
 //                    (kind::f16, fp16 operands);
-//   warps 14, 15   : idle (they complete a register group).
-// The softmax holds 128 logits a thread: its warps take 192 registers and leave
-// 64 to the others.
-// The reference of a row's exponentials is chosen so that the weights, not the
-// exponentials, fit fp16: the largest weight so far lies between 1 and 2^15, whatever
-// the range of the value scales. It moves only where a tile's largest logit and
-// largest value scale together could pass that, and then by the weights themselves.
+//   warps 14, 15   : idle; they complete a register group.
+// A tile is one pass over its logits at the row's reference, 64 keys at a time: with
+// a row's 128 logits held in registers, and their maximum taken first, the code of a
+// tile no longer fits the instruction cache and a tile took 3.8 us where it takes 2.2.
+// The reference is chosen so that the weights, not the exponentials, fit fp16: the
+// largest weight so far lies between 1 and 2^15, whatever the range of the value
+// scales. A row whose weights have grown takes it up at the next tile (that alone:
+// 67 to 60 us for a tree of 64 drafts behind 32768 keys); only where a weight passes
+// 2^15 within one tile is the tile taken again, at a reference from its largest logit
+// and scale, and from the weights that gives. What bounds a tile now: the two passes
+// of 3400 cycles that share a scheduler (2048 of them the exponentials), and between
+// them the turn of the products, which need the logits read before the next are made.
 // Every wait is bounded.
 
 #include <cuda.h>
@@ -44,13 +50,17 @@ namespace {
 constexpr int CW_KT = 128;           // keys of a tile
 constexpr int CW_THREADS = 512;
 constexpr int CW_HALF = 128 * 128;   // 128 rows of 128 bytes
+// Registers a thread: the kernel is launched with 128 for each of the four groups of four warps.
+constexpr int CW_REGS_SOFTMAX = 184, CW_REGS_VALUES = 96, CW_REGS_ISSUE = 48;
+static_assert(2 * CW_REGS_SOFTMAX + CW_REGS_VALUES + CW_REGS_ISSUE == 4 * 128, "the groups' shares are what was launched");
 constexpr uint64_t CW_TIMEOUT_NS = 2000000000ull;
 // a run costs about as much as three tiles beside its tiles
 using CwGrain = CaGrain<CA_WIDE_ROWS, CW_KT, 3, 2>;
 constexpr uint32_t CW_IDESC_S = idesc_i8(128, CW_KT);
 // fp16 operands, float32 sums, 128 x 128, B MN-major
 constexpr uint32_t CW_IDESC_O = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-constexpr float CW_FIT = 15.0f;      // weights stay below 2^15
+constexpr float CW_MOST = 32768.0f;  // weights stay below 2^15
+constexpr float CW_GROWN = 16.0f;    // past it a row's reference goes up at the next tile
 constexpr float CW_SPAN = 100.0f;    // exponentials below 2^100
 
 struct CwSmem {
@@ -63,14 +73,15 @@ struct CwSmem {
   static constexpr int kOffRow = kOffTile + 2 * 2 * 8 * 4;   // query factors
   static constexpr int kOffStat = kOffRow + 128 * 4;         // [pipeline][row] maximum, sum
   static constexpr int kOffScan = kOffStat + 2 * 128 * 8;
-  // per pipeline: k_full, k_empty, s_full, s_empty, p_full, o_done, v_full, sc_full; then drain
+  // per pipeline: keys there, keys read, S there, S read, weights there, P V done, values there, scales there (of each
+  // buffer); then drain
   static constexpr int kOffBar = kOffScan + 18 * 8;
-  static constexpr int kOffMisc = kOffBar + 17 * 8;
+  static constexpr int kOffMisc = kOffBar + 19 * 8 + 8;
   static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
 
-enum CwBar { kKFull, kKEmpty, kSFull, kSEmpty, kPFull, kODone, kVFull, kScFull, kBars };
+enum CwBar { kKFull, kKEmpty, kSFull, kSEmpty, kPFull, kODone, kVFull, kSc0, kSc1, kBars };
 
 __device__ __forceinline__ void cw_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -98,37 +109,89 @@ __device__ __forceinline__ uint32_t placed(unsigned long long bits, int at, int 
   return static_cast<uint32_t>(shift >= 0 ? bits >> shift : bits << -shift);
 }
 
-// Weights of 64 keys (half h) of a row, in fp16 in its line of the operand; the sum of their exponentials.
-template <bool MASKED>
-__device__ __forceinline__ float2 cw_weights(const float (&u)[128], int h, float c, float ref, const uint32_t (&vis)[4],
-                                             const float* sv, uint8_t* line, int sw) {
-  const float2 c2 = make_float2(c, c), nref = make_float2(-ref, -ref);
-  float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+// Two sums of 128 products of codes (|acc| < 2^22) as floats times the keys' scales, without a conversion
+// instruction: the integer added to the bits of 1.5 * 2^23 is exact, and so is subtracting 1.5 * 2^23.
+__device__ __forceinline__ float2 cw_logits(uint32_t a, uint32_t b, float2 scale) {
+  const float2 x = make_float2(__uint_as_float(a + 0x4B400000u), __uint_as_float(b + 0x4B400000u));
+  return __fmul2_rn(__fadd2_rn(x, make_float2(-12582912.0f, -12582912.0f)), scale);
+}
+
+// The largest logit of a row among the keys it sees, without the row's factor. Rolled, 32 keys at a time, here
+// and below: unrolled over the tile the code no longer fits the instruction cache.
+__device__ __forceinline__ float cw_top(uint32_t tS, const uint32_t (&vis)[4], const float* sk) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int w = 0; w < 4; ++w) {
+    uint32_t a[32];
+    tmem_ld_32x32b_x32(tS + w * 32, a);
+    const uint32_t on = w == 0 ? vis[0] : w == 1 ? vis[1] : w == 2 ? vis[2] : vis[3];
+    tmem_ld_wait_regs(a);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    uint32_t w[4];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const float4 f = *reinterpret_cast<const float4*>(sv + h * 64 + i * 8 + 4 * q);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int k = h * 64 + i * 8 + 4 * q + 2 * e;
-        const float2 t = __ffma2_rn(c2, make_float2(u[k], u[k + 1]), nref);
-        float2 pr = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-        float2 x = __fmul2_rn(pr, e == 0 ? make_float2(f.x, f.y) : make_float2(f.z, f.w));
-        if (MASKED) {
-          const bool a = vis[k >> 5] >> (k & 31) & 1u, b = vis[k >> 5] >> ((k & 31) + 1) & 1u;
-          pr = make_float2(a ? pr.x : 0.0f, b ? pr.y : 0.0f);
-          x = make_float2(a ? x.x : 0.0f, b ? x.y : 0.0f);
-        }
-        sum[e] = __fadd2_rn(sum[e], pr);
-        const __half2 hx = __floats2half2_rn(x.x, x.y);
-        w[2 * q + e] = *reinterpret_cast<const uint32_t*>(&hx);
-      }
+    for (int k = 0; k < 32; k += 2) {
+      const float2 u = cw_logits(a[k], a[k + 1], *reinterpret_cast<const float2*>(sk + w * 32 + k));
+      top = fwht::fmax3f(top, on >> k & 1u ? u.x : -INFINITY, on >> (k + 1) & 1u ? u.y : -INFINITY);
     }
-    *reinterpret_cast<uint4*>(line + ((i ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  return __fadd2_rn(sum[0], sum[1]);
+  return top;
+}
+
+// One pass over a tile's logits: the weights of the row in fp16 into its line of the operand, the sum of the
+// exponentials, and the largest weight.
+template <bool MASKED>
+__device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, const uint32_t (&vis)[4], const float* sk,
+                                        uint8_t* line, int sw, float* sum, float* most) {
+  const float* sv = sk + 128;
+  const float2 c2 = make_float2(c, c), nref = make_float2(-ref, -ref);
+  float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  float big[2] = {0.0f, 0.0f};
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {
+    uint32_t a[2][32];
+    tmem_ld_32x32b_x32(tS + h * 64, a[0]);
+    tmem_ld_32x32b_x32(tS + h * 64 + 32, a[1]);
+    const uint32_t on[2] = {h == 0 ? vis[0] : vis[2], h == 0 ? vis[1] : vis[3]};
+    const float* skh = sk + h * 64;
+    const float* svh = sv + h * 64;
+    uint8_t* to = line + h * CW_HALF;
+    tmem_ld_wait_regs(a[0]);
+    tmem_ld_wait_regs(a[1]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 fk = *reinterpret_cast<const float4*>(skh + i * 8 + 4 * q);
+        const float4 fv = *reinterpret_cast<const float4*>(svh + i * 8 + 4 * q);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int k = i * 8 + 4 * q + 2 * e;
+          const float2 u = cw_logits(a[k >> 5][k & 31], a[k >> 5][(k & 31) + 1],
+                                     e == 0 ? make_float2(fk.x, fk.y) : make_float2(fk.z, fk.w));
+          const float2 t = __ffma2_rn(c2, u, nref);
+          float2 pr = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+          float2 x = __fmul2_rn(pr, e == 0 ? make_float2(fv.x, fv.y) : make_float2(fv.z, fv.w));
+          if (MASKED) {
+            const bool y = on[k >> 5] >> (k & 31) & 1u, z = on[k >> 5] >> ((k & 31) + 1) & 1u;
+            pr = make_float2(y ? pr.x : 0.0f, z ? pr.y : 0.0f);
+            x = make_float2(y ? x.x : 0.0f, z ? x.y : 0.0f);
+          }
+          part[e] = __fadd2_rn(part[e], pr);
+          big[e] = fwht::fmax3f(big[e], x.x, x.y);
+          const __half2 hx = __floats2half2_rn(x.x, x.y);
+          w[2 * q + e] = *reinterpret_cast<const uint32_t*>(&hx);
+        }
+      }
+      *reinterpret_cast<uint4*>(to + ((i ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  const float2 all = __fadd2_rn(part[0], part[1]);
+  *sum = all.x + all.y;
+  *most = fmaxf(big[0], big[1]);
+}
+
+// Exponent of a positive float: 2^e <= x < 2^(e + 1).
+__device__ __forceinline__ float exponent_of(float x) {
+  return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127);
 }
 
 template <bool F16>
@@ -139,7 +202,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
   // aligned by an offset, not through an integer, so that the compiler still knows it is shared memory
   uint8_t* smem = smem_raw + ((0u - smem_addr(smem_raw)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
-  uint64_t* drain = bars + 16;
+  uint64_t* drain = bars + 2 * kBars;
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kOffMisc);
   uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -156,7 +219,8 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       mbar_init(bar(pipe, kPFull), 4);
       mbar_init(bar(pipe, kODone), 1);
       mbar_init(bar(pipe, kVFull), 4);
-      mbar_init(bar(pipe, kScFull), 4);
+      mbar_init(bar(pipe, kSc0), 4);
+      mbar_init(bar(pipe, kSc1), 4);
     }
     mbar_init(drain, 1);
     *abort = 0;
@@ -176,12 +240,17 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
 
   // A wait of the role; false once one has run out anywhere in the CTA.
   auto wait = [&](uint64_t* b, int use) {
-    const bool ok = mbar_wait_bounded(b, static_cast<uint32_t>(use & 1), abort, CW_TIMEOUT_NS);
-    if (!ok) {
-      *abort = 1;
-      bad |= CA_LATE;
+    const uint32_t parity = static_cast<uint32_t>(use & 1);
+    if (mbar_try_wait(b, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait_suspend(b, parity, 2000)) {
+      if (*abort || global_timer_ns() - t0 > CW_TIMEOUT_NS) {
+        *abort = 1;
+        bad |= CA_LATE;
+        return false;
+      }
     }
-    return ok;
+    return true;
   };
   // Tiles that a pipeline has taken in earlier runs: the parity of its barriers. Every role counts alike, and
   // meets the others twice a run (barrier 0): the queries are in place; the sums have been read.
@@ -191,7 +260,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    regs_more<192>();
+    regs_more<CW_REGS_SOFTMAX>();
     const int pipe = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -211,36 +280,53 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         continue;
       }
       if (p.tree != nullptr && walk.s.news > 64) bad |= CA_BAD;
-      // the tile's queries, rotated and quantised: 16 rows a warp, four at a time
-#pragma unroll 1
-      for (int k0 = 0; k0 < 16; k0 += 4) {
-        float v[4][4];
+      // the tile's queries, rotated and quantised: four lanes a row, 16 rows a warp
+      {
+        const int l4 = lane & 3;
+        uint4 w[2][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int at = warp + 8 * (k0 + k);
-          v[k][0] = v[k][1] = v[k][2] = v[k][3] = 0.0f;
-          if (at < r.rows) {
-            const int of = r.row0 + at, i = of / p.G;
-            const uint16_t* src = p.q + (walk.s.first + i) * p.qt + (r.head * p.G + (of - i * p.G)) * p.qh;
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(src + 4 * lane));
-            const float2 a = fwht::widen_pair<F16>(w.x), b = fwht::widen_pair<F16>(w.y);
-            v[k][0] = a.x, v[k][1] = a.y, v[k][2] = b.x, v[k][3] = b.y;
-          }
+        for (int k = 0; k < 2; ++k) {
+          const int at = warp * 16 + k * 8 + (lane >> 2);
+          const int of = r.row0 + at, i = of / p.G;
+          const uint16_t* src = p.q + (walk.s.first + i) * p.qt + (r.head * p.G + (of - i * p.G)) * p.qh + 8 * l4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[k][j] = at < r.rows ? __ldg(reinterpret_cast<const uint4*>(src + 32 * j)) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int at = warp + 8 * (k0 + k);
-          fwht::fwht128_warp(v[k], lane);
-          float amax = fmaxf(fmaxf(fabsf(v[k][0]), fabsf(v[k][1])), fmaxf(fabsf(v[k][2]), fabsf(v[k][3])));
+        for (int k = 0; k < 2; ++k) {
+          const int at = warp * 16 + k * 8 + (lane >> 2);
+          float2 v[16];
 #pragma unroll
-          for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, m));
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t a[4] = {w[k][j].x, w[k][j].y, w[k][j].z, w[k][j].w};
+            const uint32_t b[4] = {w[k][2 + j].x, w[k][2 + j].y, w[k][2 + j].z, w[k][2 + j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              fwht::fwht_first_pair<F16>(a[e], fwht::widen_pair<F16>(b[e]), v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+          }
+          fwht::fwht128_quad(v, l4);
+          float amax = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) amax = fwht::fmax3f(amax, fabsf(v[i].x), fabsf(v[i].y));
+          amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
           const fwht::CodeFactor f = fwht::code_factor(amax);
-          float c[4];
+          const float2 ci = make_float2(f.ci, f.ci), pre = make_float2(f.pre, f.pre);
+          const float2 magic = make_float2(fwht::kRoundMagic, fwht::kRoundMagic);
+          uint8_t* line_q = smem + L::kOffQ + at * 128 + (l4 & 1) * 8;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) c[e] = fmaf(v[k][e] * f.pre, f.ci, fwht::kRoundMagic);
-          *reinterpret_cast<uint32_t*>(smem + L::kOffQ + at * 128 + (((lane >> 2) ^ (at & 7)) << 4) + (lane & 3) * 4) =
-              fwht::pack4(c[0], c[1], c[2], c[3]);
-          if (lane == 0) row_c[at] = fwht::scale_of<128>(amax) * p.c_scale;
+          for (int j = 0; j < 2; ++j) {
+            float2 x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = __ffma2_rn(__fmul2_rn(v[8 * j + e], pre), ci, magic);
+            // channels 32 j + 8 l4 .. + 7 and 64 more: half of a 16-byte chunk each
+            *reinterpret_cast<uint2*>(line_q + (((2 * j + (l4 >> 1)) ^ (at & 7)) << 4)) =
+                make_uint2(fwht::pack4(x[0].x, x[1].x, x[2].x, x[3].x), fwht::pack4(x[4].x, x[5].x, x[6].x, x[7].x));
+            *reinterpret_cast<uint2*>(line_q + (((4 + 2 * j + (l4 >> 1)) ^ (at & 7)) << 4)) =
+                make_uint2(fwht::pack4(x[0].y, x[1].y, x[2].y, x[3].y), fwht::pack4(x[4].y, x[5].y, x[6].y, x[7].y));
+          }
+          if (l4 == 0) row_c[at] = fwht::scale_of<128>(amax) * p.c_scale;
         }
       }
       fence_proxy_async_smem();
@@ -255,7 +341,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         if (p.tree != nullptr && row < r.rows) bits = __ldg(p.tree + walk.s.first + i);
       }
       const int clear = p.tree != nullptr ? context : context + 1;  // keys below it are seen by every row
-      float ref = CA_NONE, l = 0.0f;
+      float ref = CA_NONE, l = 0.0f, largest = 0.0f;
       bool weighed = false;  // the row has had a weight
       bool ok = true;
       int use = used[pipe];
@@ -263,110 +349,58 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         const int key0 = t * CW_KT;
         const int buffer = pipe * 2 + (use & 1);
         const float* sk = reinterpret_cast<const float*>(smem + L::kOffScale) + buffer * 256;
-        const float* sv = sk + 128;
         const uint32_t* there = reinterpret_cast<const uint32_t*>(smem + L::kOffTile) + buffer * 8;
         const float* most = reinterpret_cast<const float*>(there + 4);
-        ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kScFull), use) && wait(bar(pipe, kSFull), use));
+        ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kSc0 + (use & 1)), use >> 1) && wait(bar(pipe, kSFull), use));
         if (!ok) break;
-        tc_fence_after();
-        float u[128];  // s_k[key] S[row, key]: the logit without the row's factor
-        {
-          uint32_t a0[32], a1[32];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            tmem_ld_32x32b_x32(tS + half * 64, a0);
-            tmem_ld_32x32b_x32(tS + half * 64 + 32, a1);
-            tmem_ld_wait_regs(a0);
-            tmem_ld_wait_regs(a1);
-            if (half == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar(pipe, kSEmpty));
-            }
-            const float2 mg = make_float2(-12582912.0f, -12582912.0f);
-#pragma unroll
-            for (int k4 = 0; k4 < 16; ++k4) {
-              const float4 s4 = *reinterpret_cast<const float4*>(sk + half * 64 + 4 * k4);
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int k = 4 * k4 + 2 * e;
-                const uint32_t x0 = (k < 32) ? a0[k] : a1[k - 32], x1 = (k + 1 < 32) ? a0[k + 1] : a1[k - 31];
-                // float(acc) for |acc| < 2^22: the integer added to the bits of 1.5 * 2^23, minus 1.5 * 2^23
-                const float2 x = make_float2(__uint_as_float(x0 + 0x4B400000u), __uint_as_float(x1 + 0x4B400000u));
-                const float2 v =
-                    __fmul2_rn(__fadd2_rn(x, mg), e == 0 ? make_float2(s4.x, s4.y) : make_float2(s4.z, s4.w));
-                u[half * 64 + k] = v.x;
-                u[half * 64 + k + 1] = v.y;
-              }
-            }
-          }
-        }
-        uint32_t vis[4] = {there[0], there[1], there[2], there[3]};
-        const bool masked = key0 + CW_KT > clear || (vis[0] & vis[1] & vis[2] & vis[3]) != 0xFFFFFFFFu;
-        float top;
-        if (!masked) {
-          float a[43], b[15], c5[5];
-#pragma unroll
-          for (int i = 0; i < 42; ++i) a[i] = fwht::fmax3f(u[3 * i], u[3 * i + 1], u[3 * i + 2]);
-          a[42] = fmaxf(u[126], u[127]);
-#pragma unroll
-          for (int i = 0; i < 14; ++i) b[i] = fwht::fmax3f(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
-          b[14] = a[42];
-#pragma unroll
-          for (int i = 0; i < 5; ++i) c5[i] = fwht::fmax3f(b[3 * i], b[3 * i + 1], b[3 * i + 2]);
-          top = fmaxf(fwht::fmax3f(c5[0], c5[1], c5[2]), fmaxf(c5[3], c5[4]));
-        } else {
-          top = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            vis[w] &= below(lim - key0, w) | placed(bits, context - key0, w);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) top = (vis[w] >> k & 1u) ? fmaxf(top, u[32 * w + k]) : top;
-          }
-        }
-        const bool some = (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
-        const float tm = some ? c * top : CA_NONE;
-        // log2 of the tile's largest value scale, rounded up
-        const float high = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-        const float e_high = static_cast<float>(static_cast<int>(__float_as_uint(high) >> 23) - 126);
-        float alpha = 1.0f;
-        if (__any_sync(0xFFFFFFFFu, some && (!weighed || tm + e_high > ref + CW_FIT || tm > ref + CW_SPAN))) {
-          // the row's largest weight, as a power of two over its largest logit
-          float big = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 128; ++k) {
-            const float x = ex2_approx(fmaf(c, u[k], -tm)) * sv[k];
-            big = (vis[k >> 5] >> (k & 31) & 1u) ? fmaxf(big, x) : big;
-          }
-          const float at = tm + static_cast<float>(static_cast<int>(__float_as_uint(big) >> 23) - 127);
-          float now = ref;
-          if (some) {
-            if (!weighed) now = big > 0.0f ? at : tm;
-            else if (big > 0.0f && at > ref + (CW_FIT - 1.0f)) now = at;
-            if (tm > now + CW_SPAN) now = tm - CW_SPAN;
-            weighed |= big > 0.0f;
-          }
-          alpha = ref == CA_NONE ? 0.0f : ex2_approx(ref - now);
-          if (now == ref) alpha = 1.0f;
-          ref = now;
-        }
         // the pipeline's last P V has finished: O is stable and the operand's memory free
         if (use > 0) {
           ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kODone), use - 1));
           if (!ok) break;
         }
         tc_fence_after();
-        float2 sum;
-        if (!masked) {
-          sum = __fadd2_rn(cw_weights<false>(u, 0, c, ref, vis, sv, line, sw),
-                           cw_weights<false>(u, 1, c, ref, vis, sv, line + CW_HALF, sw));
-        } else {
-          sum = __fadd2_rn(cw_weights<true>(u, 0, c, ref, vis, sv, line, sw),
-                           cw_weights<true>(u, 1, c, ref, vis, sv, line + CW_HALF, sw));
-        }
-        l = l * alpha + (sum.x + sum.y);
-        if (t >= r.t0 + 2 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+        uint32_t vis[4] = {there[0], there[1], there[2], there[3]};
+        const bool masked = key0 + CW_KT > clear || (vis[0] & vis[1] & vis[2] & vis[3]) != 0xFFFFFFFFu;
+        if (masked) {
 #pragma unroll
+          for (int w = 0; w < 4; ++w) vis[w] &= below(lim - key0, w) | placed(bits, context - key0, w);
+        }
+        // A reference at which every weight of the tile is below 2^8, from its largest logit and largest scale.
+        const float high = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+        const bool some = (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
+        auto bound = [&]() {
+          const float tm = c * cw_top(tS, vis, sk);
+          return fmaxf(high > 0.0f ? tm + exponent_of(high) - 7.0f : tm, tm - CW_SPAN);
+        };
+        float now = ref, sum, big;
+        bool fresh = false;  // `now` is such a bound: the weights may be far below it
+        // A row whose weights have grown takes its reference up before they can pass fp16's range: one
+        // rescaling of O instead of a second pass.
+        if (largest > CW_GROWN) now += exponent_of(largest);
+        if (__any_sync(0xFFFFFFFFu, some && !weighed)) {
+          const float at = bound();
+          if (some && !weighed) now = at, fresh = true;
+        }
+#pragma unroll 1
+        for (int attempt = 0;; ++attempt) {
+          if (masked) cw_pass<true>(tS, c, now, vis, sk, line, sw, &sum, &big);
+          else cw_pass<false>(tS, c, now, vis, sk, line, sw, &sum, &big);
+          const bool over = !(big <= CW_MOST) || !(sum <= 0x1p110f);
+          const bool under = fresh && big > 0.0f && big < 1.0f;
+          if (attempt == 3 || !__any_sync(0xFFFFFFFFu, over || under)) break;
+          const float at = bound();
+          if (over) now = at, fresh = true;
+          else if (under) now += exponent_of(big), fresh = false;
+        }
+        weighed |= big > 0.0f;
+        const float scale = now == ref ? 1.0f : ex2_approx(ref - now);
+        largest = fmaxf(largest * scale, big);
+        const float alpha = ref == CA_NONE ? (now == ref ? 1.0f : 0.0f) : scale;
+        ref = now;
+        l = l * alpha + sum;
+        // the logits have been read, the operand is in place, and O has the new reference
+        if (t >= r.t0 + 2 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+#pragma unroll 1
           for (int ch = 0; ch < 4; ++ch) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(tO + ch * 32, o);
@@ -380,7 +414,10 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(pipe, kPFull));
+        if (lane == 0) {
+          mbar_arrive(bar(pipe, kSEmpty));
+          mbar_arrive(bar(pipe, kPFull));
+        }
       }
       const int mine = r.t1 - r.t0 > pipe ? (r.t1 - r.t0 - pipe + 1) / 2 : 0;
       if (ok && mine > 0) ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kODone), used[pipe] + mine - 1));
@@ -398,32 +435,33 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       const uint32_t tO0 = tmem + lanes + 256, tO1 = tO0 + 128;
       const bool alive = *abort == 0;  // else there may be no sums
       float v[64];
+      // whole: the last butterfly stage, between channels 64 apart, comes first; part: this half's channels
+      const int from = whole ? 0 : pipe * 64;
+      const float sign = whole ? (pipe == 0 ? 1.0f : -1.0f) : 0.0f;
+      const float g0 = sign * f0, g1 = sign * f1;
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {
-        uint32_t a[32], b[32];
-        // whole: the last butterfly stage, between channels 64 apart, comes first; part: this half's channels
-        const int from = whole ? ch * 32 : pipe * 64 + ch * 32;
-        tmem_ld_32x32b_x32(tO0 + from, a);
-        tmem_ld_wait_regs(a);
+      for (int ch = 0; ch < 4; ++ch) {
+        uint32_t a[16], b[16];
+        tmem_ld_32x32b_x16(tO0 + from + ch * 16, a);
+        if (whole) tmem_ld_32x32b_x16(tO0 + 64 + ch * 16, b);
+        tmem_ld_wait_regs16(a);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[ch * 32 + i] = __uint_as_float(a[i]) * f0;
-        if (second) {
-          tmem_ld_32x32b_x32(tO1 + from, b);
-          tmem_ld_wait_regs(b);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[ch * 32 + i] = fmaf(__uint_as_float(b[i]), f1, v[ch * 32 + i]);
-        }
+        for (int i = 0; i < 16; ++i) v[ch * 16 + i] = __uint_as_float(a[i]) * f0;
         if (whole) {
-          const float sign = pipe == 0 ? 1.0f : -1.0f;
-          tmem_ld_32x32b_x32(tO0 + 64 + from, a);
-          tmem_ld_wait_regs(a);
+          tmem_ld_wait_regs16(b);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[ch * 32 + i] = fmaf(__uint_as_float(a[i]), sign * f0, v[ch * 32 + i]);
-          if (second) {
-            tmem_ld_32x32b_x32(tO1 + 64 + from, b);
-            tmem_ld_wait_regs(b);
+          for (int i = 0; i < 16; ++i) v[ch * 16 + i] = fmaf(__uint_as_float(b[i]), g0, v[ch * 16 + i]);
+        }
+        if (second) {
+          tmem_ld_32x32b_x16(tO1 + from + ch * 16, a);
+          if (whole) tmem_ld_32x32b_x16(tO1 + 64 + ch * 16, b);
+          tmem_ld_wait_regs16(a);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[ch * 32 + i] = fmaf(__uint_as_float(b[i]), sign * f1, v[ch * 32 + i]);
+          for (int i = 0; i < 16; ++i) v[ch * 16 + i] = fmaf(__uint_as_float(a[i]), f1, v[ch * 16 + i]);
+          if (whole) {
+            tmem_ld_wait_regs16(b);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[ch * 16 + i] = fmaf(__uint_as_float(b[i]), g1, v[ch * 16 + i]);
           }
         }
       }
@@ -469,7 +507,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     if (tid == 0) p.cuts[blockIdx.x] = cut;
   } else if (warp < 12) {
     // ----------------------------------------------------------------- values
-    regs_fewer<64>();
+    regs_fewer<CW_REGS_VALUES>();
     const int me = tid - 256;  // the thread's key of a tile, for the scales
     const int w4 = warp - 8;
     while (walk.next(p, &r, bad)) {
@@ -485,32 +523,25 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         }
         return ((page * p.Hkv + r.head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
       };
-      cw_sync(0, CW_THREADS);
-      bool ok = true;
-      for (int t = r.t0; t < r.t1 && ok; ++t) {
-        const int pipe = (t - r.t0) & 1, use = used[pipe] + ((t - r.t0) >> 1);
-        const int key0 = t * CW_KT;
-        // eight lanes a key, 16 codes each: keys w4 * 32 + 4 i + lane / 8
-        uint4 code[8];
-        const int my_cell = cell_of(key0 + me);
-        const float mk = my_cell >= 0 ? __ldg(p.k_scale + my_cell) : 0.0f;
-        const float mv = my_cell >= 0 ? __ldg(p.v_scale + my_cell) : 0.0f;
+      // Loads run ahead: codes one tile, scales two. Eight lanes a key, 16 codes each: keys w4 * 32 + 4 i + lane / 8.
+      auto load_codes = [&](int cell_mine, uint4 (&code)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int cell = __shfl_sync(0xFFFFFFFFu, my_cell, 4 * i + (lane >> 3));
+          const int cell = __shfl_sync(0xFFFFFFFFu, cell_mine, 4 * i + (lane >> 3));
           code[i] = cell >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.v_codes + static_cast<int64_t>(cell) * CA_D) +
                                       (lane & 7))
                               : make_uint4(0u, 0u, 0u, 0u);
         }
-        // the scale buffer was last used two tiles of this pipeline ago, whose softmax is done once the next began
-        if (use > 0) ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kSEmpty), use - 1));
-        if (!ok) break;
-        const int buffer = pipe * 2 + (use & 1);
+      };
+      auto load_scale = [&](const float* from, int cell) { return cell >= 0 ? __ldg(from + cell) : 0.0f; };
+      auto give_scales = [&](int n, int cell, float mk, float mv) {  // tile n of the run
+        // the buffer was last used two tiles of this pipeline ago, whose P V has been waited for
+        const int pipe = n & 1, use = used[pipe] + (n >> 1), buffer = pipe * 2 + (use & 1);
         float* sk = reinterpret_cast<float*>(smem + L::kOffScale) + buffer * 256;
         uint32_t* there = reinterpret_cast<uint32_t*>(smem + L::kOffTile) + buffer * 8;
         sk[me] = mk;
         sk[128 + me] = mv;
-        const uint32_t on = __ballot_sync(0xFFFFFFFFu, my_cell >= 0);
+        const uint32_t on = __ballot_sync(0xFFFFFFFFu, cell >= 0);
         float most = fabsf(mv);
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, m));
@@ -519,9 +550,20 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           reinterpret_cast<float*>(there + 4)[w4] = most;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(pipe, kScFull));
-        if (use > 0) ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kODone), use - 1));
-        if (!ok) break;
+        if (lane == 0) mbar_arrive(bar(pipe, kSc0 + (use & 1)));
+      };
+      const int tiles = r.t1 - r.t0;
+      // Tile n: the codes of the next into `other`, its scales, then this one's values; false once a wait has run out.
+      int cell1 = -1, cell2 = -1;  // of this thread's key in the next tile and the one after
+      float mk = 0.0f, mv = 0.0f;  // the next tile's scales
+      auto tile = [&](int n, const uint4 (&code)[8], uint4 (&other)[8]) {
+        const int pipe = n & 1, use = used[pipe] + (n >> 1);
+        if (n + 1 < tiles) {
+          load_codes(cell1, other);
+          give_scales(n + 1, cell1, mk, mv);
+          cell2 = n + 2 < tiles ? cell_of((r.t0 + n + 2) * CW_KT + me) : -1;
+        }
+        if (use > 0 && !__all_sync(0xFFFFFFFFu, wait(bar(pipe, kODone), use - 1))) return false;
         uint8_t* to = smem + L::kOffV + pipe * 2 * CW_HALF + ((lane >> 2) & 1) * CW_HALF;  // channels from 64 on: second half
         const __half2 offset = __floats2half2_rn(1152.0f, 1152.0f);
 #pragma unroll
@@ -545,13 +587,32 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(pipe, kVFull));
+        cell1 = cell2;
+        mk = load_scale(p.k_scale, cell1);
+        mv = load_scale(p.v_scale, cell1);
+        return true;
+      };
+      uint4 code_a[8], code_b[8];
+      {
+        const int cell0 = cell_of(r.t0 * CW_KT + me);
+        cell1 = tiles > 1 ? cell_of((r.t0 + 1) * CW_KT + me) : -1;
+        const float k0 = load_scale(p.k_scale, cell0), v0 = load_scale(p.v_scale, cell0);
+        load_codes(cell0, code_a);
+        mk = load_scale(p.k_scale, cell1);
+        mv = load_scale(p.v_scale, cell1);
+        give_scales(0, cell0, k0, v0);
+      }
+      cw_sync(0, CW_THREADS);
+      for (int n = 0; n < tiles; n += 2) {
+        if (!tile(n, code_a, code_b)) break;
+        if (n + 1 < tiles && !tile(n + 1, code_b, code_a)) break;
       }
       used[0] += (r.t1 - r.t0 + 1) / 2;
       used[1] += (r.t1 - r.t0) / 2;
       cw_sync(0, CW_THREADS);
     }
   } else {
-    regs_fewer<64>();
+    regs_fewer<CW_REGS_ISSUE>();
     if (warp == 12) {
       // ------------------------------------------------------------------ keys
       int issued[2] = {0, 0};
@@ -622,9 +683,9 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           if (ok && tiles > 1) ok = logits(1);
           for (int n = 0; n < tiles && ok; ++n) {
             const int pipe = n & 1, use = used[pipe] + (n >> 1);
-            // the pipeline's next S once its softmax has read this one
-            if (n + 2 < tiles) ok = wait(bar(pipe, kSEmpty), use) && logits(n + 2);
-            if (!ok || !wait(bar(pipe, kPFull), use) || !wait(bar(pipe, kVFull), use)) break;
+            // the pipeline's next S first: its softmax waits for it, and for this P V only after that
+            if (n + 2 < tiles && !(wait(bar(pipe, kSEmpty), use) && logits(n + 2))) break;
+            if (!wait(bar(pipe, kPFull), use) || !wait(bar(pipe, kVFull), use)) break;
             tc_fence_after();
             const uint32_t pa = smem_addr(smem + L::kOffP + pipe * 2 * CW_HALF);
             const uint32_t va = smem_addr(smem + L::kOffV + pipe * 2 * CW_HALF);
