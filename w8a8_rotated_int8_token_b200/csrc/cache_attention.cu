@@ -34,7 +34,9 @@
 //         brought to fp16's range by a factor per row, kept so that the largest
 //         weight so far lies between 1 and 2^15: rounding one to fp16 costs at
 //         most 2^-11 of it or 2^-25 of the largest, whatever the range of the
-//         value scales.
+//         value scales. That is far below bf16's own rounding of the output; for
+//         an fp16 output, whose rounding is no larger, a second product adds what
+//         the first rounding left.
 // The reference maximum and that factor move only when a key passes them by far;
 // a vote of the warp is all it costs otherwise.
 
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
             }
           }
         }
-        uint32_t pw[NT][2];
+        uint32_t pw[NT][2], rest[NT][2];  // weights in fp16, and for fp16 outputs what that rounding left
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float2 top = make_float2(fmaxf(s[n][0].x, s[n][1].x), fmaxf(s[n][0].y, s[n][1].y));
@@ -417,6 +419,11 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
             const float2 w = __fmul2_rn(x[e], inv[n]);
             const __half2 h = __floats2half2_rn(w.x, w.y);
             pw[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
+            if (F16) {
+              const float2 f = __half22float2(h);
+              const __half2 h2 = __floats2half2_rn(w.x - f.x, w.y - f.y);
+              rest[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h2));
+            }
           }
         }
         // values: channels 16 g .. 16 g + 15 of keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
@@ -446,7 +453,10 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
               a[e] = *reinterpret_cast<const uint32_t*>(&c);
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_f16(acc[n][2 * q4 + pair], a, pw[n][0], pw[n][1]);
+            for (int n = 0; n < NT; ++n) {
+              mma_f16(acc[n][2 * q4 + pair], a, pw[n][0], pw[n][1]);
+              if (F16) mma_f16(acc[n][2 * q4 + pair], a, rest[n][0], rest[n][1]);
+            }
           }
         }
       }
