@@ -404,6 +404,98 @@ def test_two_graphs_share_a_workspace_and_follow_the_lengths(cr):
     graphs.clear()
 
 
+# ---- more than 72 rows a sequence and key head on average: tiles of 128 rows
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("seqs,hq,hkv,page", [
+    ([(1, 1)], 80, 1, 16), ([(127, 1)], 128, 1, 16), ([(128, 1), (129, 1)], 200, 2, 32), ([(1000, 1)], 90, 1, 1024),
+    ([(0, 1), (300, 1), (0, 2)], 100, 1, 64), ([(256, 256)], 2, 2, 16), ([(300, 130), (90, 90), (5, 9)], 3, 3, 16),
+    ([(3000, 33)], 12, 3, 64), ([(20000, 1)], 96, 1, 256), ([(385, 2)] * 7, 130, 2, 128)])
+def test_tall_tiles(cr, kind, seqs, hq, hkv, page):
+    s = Setup(cr, seqs, hq, hkv, page, kind, seed=len(seqs) + hq)
+    s.check(s.run())
+
+
+@pytest.mark.parametrize("seqs,hq,hkv,page", [([(64, 64)], 8, 4, 16), ([(191, 64), (192, 64), (193, 64)], 6, 3, 32),
+                                              ([(1500, 50), (70, 64)], 4, 2, 128), ([(2600, 64)], 8, 2, 64),
+                                              ([(90, 64), (0, 40)], 4, 2, 16)])
+def test_tall_trees(cr, seqs, hq, hkv, page):
+    tree = _tree(np.random.default_rng(hq), [n for _, n in seqs])
+    s = Setup(cr, seqs, hq, hkv, page, "f16", seed=hq, tree=tree)
+    s.check(s.run())
+
+
+def test_tall_tiles_at_their_limits(cr):
+    """The cases above that strain the references, with 80 query heads to a key head."""
+    s = Setup(cr, [(900, 1)], 80, 1, 64, "f16", seed=6)
+    for j in range(900):
+        s.scales[0][s.pages[0, j // 64], :, j % 64] = 0.001 * 1.01 ** j
+    s.check(s.run())
+    for order in (1, -1):
+        s = Setup(cr, [(600, 1), (50, 1), (700, 1)], 80, 1, 16, "bf16", seed=7)
+        for j in range(600):
+            s.scales[1][s.pages[0, j // 16], :, j % 16] = 10.0 ** (order * (j - 300) / 25.0)
+        for j in range(50):
+            s.scales[1][s.pages[1, j // 16], :, j % 16] = 0.0
+        for j in range(700):  # nothing to weigh for four tiles
+            if j < 520:
+                s.scales[1][s.pages[2, j // 16], :, j % 16] = 0.0
+        o = s.check(s.run())
+        assert not o[1].any()
+    tree = np.array([1, 3, 1, 9, 17, 33], np.uint64)  # nothing sees draft 2
+    s = Setup(cr, [(130, 6)], 80, 2, 16, seed=8, tree=tree)
+    j = 130 - 6 + 2
+    s.scales[0][s.pages[0, j // 16], :, j % 16] = np.inf
+    s.scales[1][s.pages[0, j // 16], :, j % 16] = np.nan
+    s.check(s.run())
+    s = Setup(cr, [(500, 1)], 80, 1, 16, seed=9)
+    s.Q.zero_()
+    s.q[:] = 0.0
+    s.check(s.run())
+
+
+def test_tall_tiles_with_bad_pages_bounds_and_rows_left_alone(cr):
+    import torch
+
+    s = Setup(cr, [(400, 1), (40, 1)], 80, 1, 64, seed=13)
+    see = [np.ones((1, 400), bool), np.ones((1, 40), bool)]
+    good = s.pages.copy()
+    for column, bad in ((0, -1), (4, len(s.codes[0]))):
+        s.pages[0, column] = bad
+        see[0][0, column * 64:(column + 1) * 64] = False
+    O = s.run(status=1)
+    s.pages = good
+    s.check(O, see=see)
+    out = torch.full((4, 80, 128), 3.0, dtype=s.dtype, device="cuda")
+    cr.convrot_cache_attention(torch.cat([s.Q, s.Q]), *s.cells(), *s.args(), O=out)
+    s.check(out[:2])
+    assert bool((out[2:] == 3.0).all())
+
+
+def test_tall_tiles_the_same_every_time_and_in_a_graph(cr):
+    import torch
+
+    s = Setup(cr, [(5000, 2), (300, 1), (64, 5)], 64, 2, 64, "f16", seed=17)
+    cells, args = s.cells(), s.args()
+    want = cr.convrot_cache_attention(s.Q, *cells, *args)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [cr.convrot_cache_attention(s.Q, *cells, *args, stream=st) for _ in range(5) for st in (None, side)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    out = torch.empty_like(s.Q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cr.convrot_cache_attention(s.Q, *cells, *args, O=out)
+    for keys in (5000, 130, 0):
+        args[1][0] = keys
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, cr.convrot_cache_attention(s.Q, *cells, *args))
+    del graph
+
+
 def test_a_decoder_step_by_step(cr):
     """Projection, positions, cache and attention as a decoder runs them: a prompt, single tokens, then a tree of
     drafts, against the oracle on the cells the cache ends up with, and the cells against the tokens' own keys."""
