@@ -171,3 +171,24 @@ def test_cache_slots():
     pos = torch.tensor([0, 17, 15, 16, 32, 0, 0, -1])
     assert cache.slots(pages, seq, pos).tolist() == [48, 17, 47, -1, -1, -1, -1, -1]
     assert cache.slots(pages[:, :0], seq, pos).tolist() == [-1] * 8
+
+
+def test_native_binding_leaves_other_calls_to_python(L):
+    """Built, of this torch, bound to the library; what it does not take it hands back without a launch."""
+    import torch
+
+    from w8a8_rotated_int8_token_b200 import _lib
+
+    b = _lib.binding()
+    assert b is not None
+    x = torch.zeros((1, 4, 2, 128), dtype=torch.bfloat16)
+    i32, f64 = torch.zeros((3, 4), dtype=torch.int32), torch.zeros((4,), dtype=torch.float64)
+    c, s = torch.zeros((1, 2, 16, 128), dtype=torch.int8), torch.zeros((1, 2, 16))
+    assert b.rope(x, i32, f64, i32[0], False, False, None) is None
+    assert b.append(x[0], x[0], i32[0], c, c, s, s, None) is None
+    assert b.read(i32[0], c, c, s, s, 0, None, None, None) is None
+    assert b.attention(x[0], c, c, s, s, i32, i32[0], None, None, None, None, None) is None
+    for fn, n in ((b.rope, 7), (b.append, 8), (b.read, 9), (b.attention, 12)):
+        assert fn(*[None] * n) is None and fn(*[0] * n) is None and fn() is None
+    with pytest.raises(TypeError):
+        b.bind(1)

@@ -574,3 +574,79 @@ def test_a_prompt_through_the_dense_attention(cr):
     O = tight.attention(q[:, -1:].transpose(0, 1).contiguous(), flat, torch.tensor([S], dtype=torch.int32, device="cuda"))
     last = O[0].double().cpu().numpy()
     assert np.linalg.norm(last - ref[:, -1]) <= 1e-2 * np.linalg.norm(ref[:, -1])
+
+
+def test_native_and_python_binding_agree(cr, monkeypatch):
+    """The native form takes a decoding step's calls, strided views, outputs and fp16 too, and gives what
+    the Python form gives, bit for bit; both refuse the same."""
+    import torch
+
+    g = torch.Generator("cuda").manual_seed(5)
+
+    def rnd(*shape, dtype=torch.bfloat16):
+        return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+    def step(dtype, given):
+        rows = rnd(6, 16, 128, dtype=dtype)
+        q, k, v = rows[:, :8], rows[:, 8:12], rows[:, 12:]
+        cache = cr.ConvRotCache(8, 4, 16)
+        freq, axis = cr.convrot_rope_tables([16, 24, 24])
+        where = torch.arange(18, device="cuda", dtype=torch.int32).view(3, 6)
+        table = torch.arange(6, device="cuda", dtype=torch.int32).view(3, 2)
+        lengths = torch.tensor([20, 7, 0], device="cuda", dtype=torch.int32)
+        starts = torch.tensor([0, 2, 6, 6], device="cuda", dtype=torch.int32)
+        tree = torch.tensor([1, 3, 1, 3, 5, 9], device="cuda", dtype=torch.int64)
+        slots = torch.tensor([18, 19, 35, 36, 37, 38], device="cuda", dtype=torch.int32)
+        room = [torch.empty(6, 12, 128, dtype=dtype, device="cuda")[:, 1:9] if given else None for _ in range(4)]
+
+        def calls():
+            out = [cr.convrot_rope(q, where, freq, axis, interleaved=given, inverse=given, Y=room[0])]
+            out.append(cr.convrot_rope(q[None], where[:, None], freq, axis))
+            cache.append(k, v, slots)
+            out += cache.read(slots, dtype=dtype, K=room[1][:, :4] if given else None,
+                              V=room[2][:, :4] if given else None)
+            scale = 0.3 if given else None
+            room_ws = cr.convrot_cache_attention_workspace_bytes(6, 3, 8, 4)
+            ws = torch.empty(room_ws, dtype=torch.uint8, device="cuda") if given else None
+            out.append(cache.attention(q, table, lengths, starts, tree=tree, softmax_scale=scale, O=room[3], ws=ws))
+            out.append(cache.attention(q[:3], table, lengths))
+            return [t.clone() for t in out] + [t.clone() for t in cache.cells]
+
+        return calls, q, cache
+
+    T = cr._T
+    for dtype in (torch.bfloat16, torch.float16):
+        for given in (False, True):
+            calls, q, cache = step(dtype, given)
+            took = []
+
+            def count(fn):
+                def run(*a):
+                    done = fn(*a)
+                    took.append(done is not None)
+                    return done
+                return run
+
+            with monkeypatch.context() as m:
+                for name in ("rope", "append", "read", "attention"):
+                    m.setattr(T, name, count(getattr(T, name)))
+                native = calls()
+            assert took == [True] * 6
+            with monkeypatch.context() as m:
+                for name in ("rope", "append", "read", "attention"):
+                    m.setattr(T, name, lambda *a: None)
+                plain = calls()
+            assert all(torch.equal(a.view(torch.int8), b.view(torch.int8)) for a, b in zip(native, plain))
+
+    table = torch.zeros(6, 1, device="cuda", dtype=torch.int32)
+    lengths = torch.ones(6, device="cuda", dtype=torch.int32)
+    for bad in (dict(O=q.float()), dict(O=q[:, :1].expand(6, 8, 128)), dict(ws=lengths[::2]),
+                dict(tree=lengths), dict(starts=lengths), dict(softmax_scale=float("nan"))):
+        with pytest.raises((TypeError, ValueError, cr.ConvRotError)):
+            cache.attention(q, table, lengths, **bad)
+    with pytest.raises(cr.ConvRotError):
+        cache.attention(q, table, lengths, ws=lengths[:0])
+    with pytest.raises(TypeError):
+        cache.read(lengths, dtype=torch.float32)
+    with pytest.raises(ValueError):
+        cache.read(lengths, dtype=torch.bfloat16, K=torch.empty(6, 4, 128, dtype=torch.float16, device="cuda"))

@@ -425,6 +425,10 @@ class _Torch:
         self.empty_like, self.empty = torch.empty_like, torch.empty
         self.device = torch._C._cuda_getDevice
         self.stream = torch._C._cuda_getCurrentRawStream  # a Stream object costs ten times as much
+        # the native forms of the calls; they return None where the Python form has to see to a call
+        native = _lib.binding()
+        self.rope, self.append, self.read, self.attention = (
+            (native.rope, native.append, native.read, native.attention) if native else (lambda *a: None,) * 4)
         return object.__getattribute__(self, name)
 
 
@@ -512,6 +516,10 @@ def convrot_rope(X, positions, freq, axis, interleaved: bool = False, inverse: b
     freq float64 (radians), axis int32. `inverse` turns back, which is also the gradient.
     Y: an output of X's shape and any strides (X itself works in place); with
     Y = buf.transpose(-3, -2) the heads come out as convrot_attention_int8 takes them."""
+    if stream is None:
+        done = _T.rope(X, positions, freq, axis, interleaved, inverse, Y)
+        if done is not None:
+            return done
     code, index, shape, xs = _head_vectors(X, "X", (3, 4))
     if stream is not None or _T.device() != index:
         where = _elsewhere(index, stream)
@@ -576,6 +584,8 @@ def convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status
     rotated int8 cache: token t to slot slots[t] (int32; page * page size + place; negative: skipped;
     the others must differ). Cache: codes int8 [pages, H, page size, 128], scales float32 [pages, H,
     page size]. status: an int32 [1] tensor that a slot past the cache sets to 1, or None."""
+    if stream is None and _T.append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status):
+        return
     code, index, shape, ks = _head_vectors(K, "K")
     if stream is not None or _T.device() != index:
         where = _elsewhere(index, stream)
@@ -602,6 +612,12 @@ def convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype=None, K=
                        stream=None):
     """Read the keys and values of slots [T] back: (K, V) [T, H, 128] in `dtype` (bf16 by default, or
     fp16); a negative slot reads as zeros. K, V: outputs with strided tokens and heads, or None."""
+    if stream is None:
+        want = dtype if dtype is not None else K.dtype if K is not None else V.dtype if V is not None else None
+        code = DTYPE_BF16 if want is None else _T.code.get(want, -1)
+        done = _T.read(slots, k_codes, v_codes, k_scale, v_scale, code, K, V, status)
+        if done is not None:
+            return done
     index = slots.get_device()
     if index < 0:
         raise ValueError("slots must be on a CUDA device")
@@ -651,6 +667,10 @@ def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, length
     (None: token b belongs to sequence b). Among its new tokens a query sees the earlier ones and
     itself, or, with tree [T] int64, those whose bit is set in its mask (at most 64 a sequence).
     See include/convrot.h."""
+    if stream is None:
+        done = _T.attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree, softmax_scale, O, ws)
+        if done is not None:
+            return done
     code, index, shape, qs = _head_vectors(Q, "Q")
     if stream is not None or _T.device() != index:
         where = _elsewhere(index, stream)

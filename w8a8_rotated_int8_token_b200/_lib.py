@@ -87,3 +87,22 @@ def load() -> ctypes.CDLL:
         fn.argtypes = args
     _lib = lib
     return lib
+
+
+def binding():
+    """The native form of the binding's rope and cache calls (csrc/binding.cpp), bound to the loaded
+    library, or None if it was built for another torch or not at all: the Python form of the same
+    checks serves then."""
+    lib = load()
+    try:
+        import torch
+
+        from . import _binding
+    except ImportError:
+        return None
+    if _binding.torch_version != str(torch.__version__):
+        return None
+    _binding.bind(*(ctypes.cast(fn, _c_void_p).value for fn in (
+        lib.convrot_rope, lib.convrot_cache_append, lib.convrot_cache_read, lib.convrot_cache_attention,
+        lib.convrot_cache_attention_workspace_bytes)))
+    return _binding

@@ -4,6 +4,8 @@
 ``csrc/*.cu`` into ``w8a8_rotated_int8_token_b200/libconvrot.so``. No GPU is
 needed to build. The CUDA runtime is linked statically and its symbols are
 kept private, so the library does not clash with the runtime PyTorch loads.
+Beside it, g++ compiles ``csrc/binding.cpp`` against the installed PyTorch into
+``_binding.so``, the Python binding's short way to the calls of a decoding step.
 """
 
 from __future__ import annotations
@@ -17,6 +19,8 @@ import sys
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 LIB_PATH = os.path.join(PKG_DIR, "libconvrot.so")
+BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
+BINDING_SOURCE = os.path.join(PKG_DIR, "csrc", "binding.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -45,27 +49,59 @@ def _deps() -> list[str]:
         os.path.join(ROOT, "include", "convrot.h")]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _newer(path: str, deps: list[str]) -> bool:
+    if not os.path.exists(path):
         return False
-    t = os.path.getmtime(LIB_PATH)
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
+def up_to_date() -> bool:
+    return _newer(LIB_PATH, _deps())
+
+
+def _binding_up_to_date() -> bool:
+    import torch
+
+    installed = os.path.join(os.path.dirname(torch.__file__), "version.py")  # another torch may have come since
+    return _newer(BINDING_PATH, [BINDING_SOURCE, os.path.join(ROOT, "include", "convrot.h"), installed])
+
+
+def _binding_command(out: str) -> list[str]:
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    include = [os.path.join(ROOT, "include"), os.path.join(base, "include"), os.path.join(cuda, "include"),
+               sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            f'-DBUILT_FOR_TORCH="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{d}" for d in include),
+            BINDING_SOURCE, "-o", out, f"-L{os.path.join(base, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library if a source is newer than it; return its path."""
-    if not force and up_to_date():
-        return LIB_PATH
-    tmp = LIB_PATH + ".tmp"
-    cmd = [_nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources()]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({r.returncode}):\n{r.stdout}\n{r.stderr}")
-    if verbose and (r.stdout or r.stderr):
-        print(r.stdout + r.stderr, file=sys.stderr)
-    os.replace(tmp, LIB_PATH)
+    """Compile the library and the binding if a source is newer than them; return the library's path."""
+    jobs = []
+    if force or not up_to_date():
+        tmp = LIB_PATH + ".tmp"
+        jobs.append((LIB_PATH, [_nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources()]))
+    if force or not _binding_up_to_date():
+        jobs.append((BINDING_PATH, _binding_command(BINDING_PATH + ".tmp")))
+    running = []
+    for path, cmd in jobs:
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        running.append((path, cmd[0], subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
+    ended = [(path, tool, *p.communicate(), p.returncode) for path, tool, p in running]
+    for path, tool, out, err, code in ended:
+        if code != 0:
+            raise RuntimeError(f"{os.path.basename(tool)} failed ({code}):\n{out}\n{err}")
+        if verbose and (out or err):
+            print(out + err, file=sys.stderr)
+        os.replace(path + ".tmp", path)
     return LIB_PATH
 
 
