@@ -202,3 +202,29 @@ def test_captured_and_on_another_stream(cr):
     torch.cuda.synchronize()
     assert torch.equal(out[0], want[1]) and torch.equal(out[1], want[0])
     del graph
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_read_any_codes(cr, kind):
+    """Cells filled by hand: each sign pattern of the transform, the largest sums, -128 among the codes."""
+    import torch
+
+    cache = cr.ConvRotCache(20, 1, 16)
+    g = torch.Generator("cuda").manual_seed(11)
+    for codes, scale in (cache.cells[::2], cache.cells[1::2]):
+        codes.copy_(torch.randint(-128, 128, codes.shape, generator=g, device="cuda"))
+        scale.copy_(torch.rand(scale.shape, generator=g, device="cuda") * 0.01)
+    flat = cache.k_codes.view(320, 128)
+    i = torch.arange(128)
+    for c in range(128):  # row c: the signs of channel c, the sum 127 * 128 in one place
+        flat[c] = torch.tensor([127 if bin(c & int(j)).count("1") % 2 == 0 else -127 for j in i], dtype=torch.int8)
+    flat[128:256] = 0
+    flat[128 + i, i] = 1  # one code at each channel
+    flat[256] = -128
+    slots = torch.arange(320, dtype=torch.int32, device="cuda")
+    k, v = cache.read(slots, _dtype(kind))
+    for x, codes, scale in ((k, cache.k_codes, cache.k_scale), (v, cache.v_codes, cache.v_scale)):
+        codes, scale = codes.view(320, 1, 128).cpu().numpy(), scale.view(320, 1).cpu().numpy()
+        ref = oracle.cache_value(codes, scale)
+        own = 2 * 128 * 2.0**-53 * 128 * 128 / np.sqrt(128.0) * scale.astype(np.float64)[..., None]  # the oracle's, as above
+        assert np.all(np.abs(x.double().cpu().numpy() - ref) <= (OUT_REL[kind] + 2.0**-22) * np.abs(ref) + OUT_ABS[kind] + own)

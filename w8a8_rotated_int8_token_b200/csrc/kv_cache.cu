@@ -7,14 +7,18 @@
 // g = 128. Reading gives (c s) R, since R is its own inverse.
 //
 // Bound by memory: 256 bytes on the dense side and 132 in the cell per vector.
-// Four lanes share a key and its value, 32 channels each: five of the seven
-// butterfly stages stay in registers, packed two to an instruction, and two cross
-// lanes (64 shuffles a lane and vector; with 16 lanes it would be twice as many per
-// vector); every access on the dense side is 16 bytes a lane in runs of 64 per
-// vector. Both vectors' loads are issued before either is transformed: 32768
-// scattered tokens of 8 heads are read in 40.9 us against 47.3 with a thread per
-// vector (204 MB, 77 % of the copy bandwidth; the scales of scattered cells cost a
-// 32-byte sector each, 17 MB more).
+// Four lanes share a key and its value, 32 channels each; every access on the dense
+// side is 16 bytes a lane in runs of 64 per vector, and both vectors' loads are issued
+// before either is transformed. Writing, five of the seven butterfly stages stay in
+// registers, packed two to an instruction, and two cross lanes (64 shuffles a lane
+// and vector; with 16 lanes it would be twice as many per vector).
+// Reading transforms whole numbers, exact in any order, so there the tensor cores
+// take five stages at once (a product with the 32-point signs, eight instructions for
+// eight vectors) and nothing crosses lanes: 32768 scattered tokens of 8 heads in 37.3 us
+// (204 MB, 85 % of the copy bandwidth; the scales of scattered cells cost a 32-byte
+// sector each, 17 MB more) against 40.9 with the stages of writing, where shuffles and
+// narrow loads kept the first-level data path 85 % busy, 47.3 with a thread per vector
+// and 53.9 with the first four stages in pairs of fp16.
 
 #include <cuda_runtime.h>
 
@@ -130,42 +134,70 @@ __global__ void __launch_bounds__(kCellThreads) cache_append_kernel(const CellPa
   write_cell<F16>(v, l, c.cell, p.v_codes, p.v_scale);
 }
 
-// Byte e of a word of codes with the sign bits flipped, as a float plus 2^23 + 128.
-__device__ __forceinline__ float code_plus(uint32_t flipped, int e) {
-  return __uint_as_float(__byte_perm(flipped, 0x4B000000u, 0x7440 + e));
+// Sums of 32 codes of 16 rows with signs, added to the bits of a float: exact.
+__device__ __forceinline__ void mma_codes(uint32_t (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1, uint32_t c) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c));
 }
 
-// A lane's four 8-byte pieces of codes to its channels of the vector; zeros where there is no cell.
+// The signs of the 32-point transform as the operand of mma_codes: lane 4 g + t holds rows 8 t + 4 h + e (byte e of
+// word h) of column 8 (g / 2) + 2 n + g % 2 in sign[n][h], so that lane t of a vector brings channels 8 t .. + 7 of a
+// block of 32 and gets their sums back.
+__device__ __forceinline__ void block_signs(int lane, uint32_t (&sign)[4][2]) {
+  const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int n = 0; n < 4; ++n) {
+    const int col = 8 * (g >> 1) + 2 * n + (g & 1);
+    // bytes 0 .. 3 of columns 0 .. 3 (mod 4)
+    const uint32_t low = n & 1 ? ((g & 1) != 0 ? 0x01FFFF01u : 0xFFFF0101u) : ((g & 1) != 0 ? 0xFF01FF01u : 0x01010101u);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      sign[n][h] = (__popc((8 * t + 4 * h) & col) & 1) != 0 ? low ^ 0xFEFEFEFEu : low;  // 1 and -1 change places
+  }
+}
+
+// A vector's four 8-byte pieces of codes (channels 32 j + 8 l .. + 7) to the same channels of the vector; zeros where
+// there is no cell. The sums of 128 codes are whole numbers and every step is exact: the stages on index bits
+// 0 to 4 are the matrix product, those on 5 and 6 in registers.
 template <bool F16>
-__device__ __forceinline__ void read_cell(const uint2 (&w)[4], int l, float scale, bool there, bool any, uint16_t* dst) {
-  // sums of 128 codes: every stage is exact in float32
-  float2 v[16];
+__device__ __forceinline__ void read_cell(const uint2 (&w)[4], const uint32_t (&sign)[4][2], float scale, bool there,
+                                          bool any, uint16_t* dst) {
+  constexpr uint32_t kBits = 0x4B400000u;  // 1.5 * 2^23: plus a sum as an integer it is that plus the sum as a float
+  const float2 bias = make_float2(-12582912.0f, -12582912.0f);
+  float2 v[4][4];  // channels 32 j + 8 l + 2 n, + 1 in v[j][n]
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int n = 0; n < 4; ++n) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float a = code_plus((e < 4 ? w[j].x : w[j].y) ^ 0x80808080u, e & 3);
-      const float b = code_plus((e < 4 ? w[2 + j].x : w[2 + j].y) ^ 0x80808080u, e & 3);
-      const float2 ab = __fadd2_rn(make_float2(a, b), make_float2(-8388736.0f, -8388736.0f));
-      v[8 * j + e] = make_float2(ab.x + ab.y, ab.x - ab.y);
+    for (int j = 0; j < 4; j += 2) {
+      uint32_t d[4];
+      mma_codes(d, w[j].x, w[j + 1].x, w[j].y, w[j + 1].y, sign[n][0], sign[n][1], kBits);
+      v[j][n] = __fadd2_rn(make_float2(__uint_as_float(d[0]), __uint_as_float(d[1])), bias);
+      v[j + 1][n] = __fadd2_rn(make_float2(__uint_as_float(d[2]), __uint_as_float(d[3])), bias);
     }
   }
-  fwht::fwht128_quad(v, l);
   if (!there) return;
   const float by1 = scale * fwht::kInvSqrt128;
   const float2 by = make_float2(by1, by1);
+  uint32_t out[4][4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    uint32_t lo[4], hi[4];
+  for (int n = 0; n < 4; ++n) {
+    const float2 s0 = fwht::bfly_sum(v[0][n], v[1][n]), d0 = fwht::bfly_diff(v[0][n], v[1][n]);
+    const float2 s1 = fwht::bfly_sum(v[2][n], v[3][n]), d1 = fwht::bfly_diff(v[2][n], v[3][n]);
+    const float2 y[4] = {fwht::bfly_sum(s0, s1), fwht::bfly_sum(d0, d1), fwht::bfly_diff(s0, s1),
+                         fwht::bfly_diff(d0, d1)};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 a = __fmul2_rn(v[8 * j + 2 * e], by), b = __fmul2_rn(v[8 * j + 2 * e + 1], by);
-      lo[e] = any ? fwht::narrow_pair<F16>(a.x, b.x) : 0u;
-      hi[e] = any ? fwht::narrow_pair<F16>(a.y, b.y) : 0u;
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = __fmul2_rn(y[j], by);
+      out[j][n] = any ? fwht::narrow_pair<F16>(x.x, x.y) : 0u;
     }
-    *reinterpret_cast<uint4*>(dst + 32 * j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    *reinterpret_cast<uint4*>(dst + 64 + 32 * j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(dst + 32 * j) = make_uint4(out[j][0], out[j][1], out[j][2], out[j][3]);
 }
 
 template <bool F16>
@@ -190,8 +222,10 @@ __global__ void __launch_bounds__(kCellThreads) cache_read_kernel(const CellPara
     ks = __ldg(p.k_scale + c.cell);
     vs = __ldg(p.v_scale + c.cell);
   }
-  read_cell<F16>(k, l, ks, there, c.cell >= 0, p.k + c.t * p.kt + c.h * p.kh + 8 * l);
-  read_cell<F16>(v, l, vs, there, c.cell >= 0, p.v + c.t * p.vt + c.h * p.vh + 8 * l);
+  uint32_t sign[4][2];
+  block_signs(threadIdx.x & 31, sign);
+  read_cell<F16>(k, sign, ks, there, c.cell >= 0, p.k + c.t * p.kt + c.h * p.kh + 8 * l);
+  read_cell<F16>(v, sign, vs, there, c.cell >= 0, p.v + c.t * p.vt + c.h * p.vh + 8 * l);
 }
 
 bool aligned_to(const void* ptr, uintptr_t a) { return (reinterpret_cast<uintptr_t>(ptr) % a) == 0; }
