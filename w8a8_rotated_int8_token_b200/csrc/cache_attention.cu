@@ -586,49 +586,70 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
 // per lane.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinAhead = 8;  // parts whose loads a lane has in flight
+constexpr int kWideAhead = 4;
+
+// The call's status from the pieces' (by the first CTA).
+__device__ __forceinline__ void join_status(const CaParams& p) {
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    int st = 0;
+    for (int i = threadIdx.x; i < p.workers; i += 32 * kJoinWarps) st |= p.piece_status[i];
+    const int any_bad = __syncthreads_or(st & CA_BAD), late = __syncthreads_or(st & 4);  // a timeout is 5
+    if (threadIdx.x == 0) *p.status = late ? CA_LATE : any_bad ? CA_BAD : 0;
+  }
+}
+
+// The rotation of a row's mean and its rounding, four channels a lane.
+template <bool F16>
+__device__ __forceinline__ void join_out(const CaParams& p, const CaCut& cut, int row, float (&v)[4], int lane) {
+  fwht::fwht128_warp(v, lane);
+  const int of = cut.row0 + row, i = of / p.G;
+  uint16_t* dst = p.o + (cut.token0 + i) * p.ot + (cut.head * p.G + (of - i * p.G)) * p.oh + 4 * lane;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(fwht::narrow_pair<F16>(v[0], v[1]), fwht::narrow_pair<F16>(v[2], v[3]));
+}
 
 template <bool F16>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_attention_join_kernel(const CaParams p, int rows) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   griddep_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    int st = 0;
-    for (int i = tid; i < p.workers; i += 32 * kJoinWarps) st |= p.piece_status[i];
-    const int any_bad = __syncthreads_or(st & CA_BAD), late = __syncthreads_or(st & 4);  // a timeout is 5
-    if (tid == 0) *p.status = late ? CA_LATE : any_bad ? CA_BAD : 0;
-  }
+  join_status(p);
   const CaCut cut = p.cuts[blockIdx.x];
   if (cut.pieces < 1) return;
   // part 0 of the item is slot 2 c + 1, the k-th after it slot 2 (c + k)
   auto slot = [&](int k) { return 2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? 1 : 0); };
   for (int row = blockIdx.y * kJoinWarps + warp; row < cut.rows; row += kJoinWarps * gridDim.y) {
-    float top = CA_NONE;
-    for (int k = lane; k < cut.pieces; k += 32) top = fmaxf(top, p.part_ml[slot(k) * rows + row].x);
+    auto load = [&](int k) {
+      return k < cut.pieces ? *reinterpret_cast<const float4*>(
+                                  p.part + (static_cast<int64_t>(slot(k)) * rows + row) * CA_D + 4 * lane)
+                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+    auto statistic = [&](int k) {
+      return k < cut.pieces ? p.part_ml[slot(k) * rows + row] : make_float2(CA_NONE, 0.0f);
+    };
+    // the first parts are under way before their weights are known
+    const float2 first = statistic(lane);
+    float4 o[kJoinAhead];
+#pragma unroll
+    for (int j = 0; j < kJoinAhead; ++j) o[j] = load(j);
+    float top = first.x;
+    for (int k = lane + 32; k < cut.pieces; k += 32) top = fmaxf(top, statistic(k).x);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
     float sum = 0.0f;
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int k0 = 0; k0 < cut.pieces; k0 += 32) {
       const int here = cut.pieces - k0 < 32 ? cut.pieces - k0 : 32;
-      float weight = 0.0f;
-      if (lane < here) {
-        const float2 ml = p.part_ml[slot(k0 + lane) * rows + row];
-        weight = ex2_approx(ml.x - top);
-        sum += weight * ml.y;
-      }
+      const float2 ml = k0 == 0 ? first : statistic(k0 + lane);
+      const float weight = ex2_approx(ml.x - top);
+      sum += weight * ml.y;  // a statistic of no part: 0
       for (int j0 = 0; j0 < here; j0 += kJoinAhead) {
-        float4 o[kJoinAhead];
-#pragma unroll
-        for (int j = 0; j < kJoinAhead; ++j)
-          o[j] = j0 + j < here ? *reinterpret_cast<const float4*>(
-                                     p.part + (static_cast<int64_t>(slot(k0 + j0 + j)) * rows + row) * CA_D + 4 * lane)
-                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int j = 0; j < kJoinAhead; ++j) {
           const float w = __shfl_sync(0xFFFFFFFFu, weight, (j0 + j) & 31);
           v[0] = fmaf(w, o[j].x, v[0]), v[1] = fmaf(w, o[j].y, v[1]);
           v[2] = fmaf(w, o[j].z, v[2]), v[3] = fmaf(w, o[j].w, v[3]);
         }
+#pragma unroll
+        for (int j = 0; j < kJoinAhead; ++j) o[j] = load(k0 + j0 + kJoinAhead + j);
       }
     }
 #pragma unroll
@@ -636,12 +657,74 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_attention_join_kernel(c
     const float norm = sum == 0.0f ? 0.0f : fwht::kInvSqrt128 / sum;
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] *= norm;
-    fwht::fwht128_warp(v, lane);
-    const int of = cut.row0 + row, i = of / p.G;
-    uint16_t* dst = p.o + (cut.token0 + i) * p.ot + (cut.head * p.G + (of - i * p.G)) * p.oh + 4 * lane;
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(fwht::narrow_pair<F16>(v[0], v[1]), fwht::narrow_pair<F16>(v[2], v[3]));
+    join_out<F16>(p, cut, row, v, lane);
   }
+}
+
+// The same for tiles of 128 rows, whose parts lie four channels of all rows after one
+// another: eight rows a CTA, a row and four channels a thread, so that eight lanes
+// read a line; then a warp per row as above.
+template <bool F16>
+__global__ void __launch_bounds__(32 * kJoinWarps) cache_attention_join_wide_kernel(const CaParams p) {
+  __shared__ float sums[kJoinWarps][CA_D + 4];
+  __shared__ float norms[kJoinWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  griddep_wait();
+  join_status(p);
+  const CaCut cut = p.cuts[blockIdx.x];
+  const int row0 = blockIdx.y * kJoinWarps;
+  if (row0 >= (cut.pieces < 1 ? 0 : cut.rows)) return;
+  {
+    const int r = tid & (kJoinWarps - 1), c = tid / kJoinWarps;  // c of 32
+    const int row = row0 + r < cut.rows ? row0 + r : cut.rows - 1;
+    auto slot = [&](int k) { return 2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? 1 : 0); };
+    // parts in fours, the next four under way while these are added
+    float4 o[kWideAhead];
+    float2 ml[kWideAhead];
+    auto load = [&](int k0) {
+#pragma unroll
+      for (int i = 0; i < kWideAhead; ++i) {
+        const int k = k0 + i;
+        o[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        ml[i] = make_float2(CA_NONE, 0.0f);
+        if (k < cut.pieces) {
+          o[i] = reinterpret_cast<const float4*>(p.part)[(static_cast<int64_t>(slot(k)) * (CA_D / 4) + c) * CA_WIDE_ROWS + row];
+          ml[i] = p.part_ml[slot(k) * CA_WIDE_ROWS + row];
+        }
+      }
+    };
+    load(0);
+    float top = CA_NONE, sum = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k0 = 0; k0 < cut.pieces; k0 += kWideAhead) {
+      float4 x[kWideAhead];
+      float2 st[kWideAhead];
+#pragma unroll
+      for (int i = 0; i < kWideAhead; ++i) x[i] = o[i], st[i] = ml[i];
+      load(k0 + kWideAhead);
+      float most = top;
+#pragma unroll
+      for (int i = 0; i < kWideAhead; ++i) most = fmaxf(most, st[i].x);
+      const float f = ex2_approx(top - most);
+      top = most;
+      sum *= f, v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+#pragma unroll
+      for (int i = 0; i < kWideAhead; ++i) {
+        const float w = ex2_approx(st[i].x - top);  // of no part: no sum, no values
+        sum = fmaf(w, st[i].y, sum);
+        v.x = fmaf(w, x[i].x, v.x), v.y = fmaf(w, x[i].y, v.y), v.z = fmaf(w, x[i].z, v.z), v.w = fmaf(w, x[i].w, v.w);
+      }
+    }
+    *reinterpret_cast<float4*>(&sums[r][4 * c]) = v;
+    if (c == 0) norms[r] = sum == 0.0f ? 0.0f : fwht::kInvSqrt128 / sum;
+  }
+  __syncthreads();
+  const int row = row0 + warp;
+  if (row >= cut.rows) return;
+  const float4 s = *reinterpret_cast<const float4*>(&sums[warp][4 * lane]);
+  const float norm = norms[warp];
+  float v[4] = {s.x * norm, s.y * norm, s.z * norm, s.w * norm};
+  join_out<F16>(p, cut, row, v, lane);
 }
 
 // ------------------------------------------------------------------------ host
@@ -664,9 +747,9 @@ CaLayout ca_layout(int rows) {
 
 // The tile of rows by the mean number of rows a sequence has for a key head. A taller tile reads the keys for
 // fewer tiles, a lower one wastes fewer of its rows. 16 rows against 128, 8 sequences of 4096 keys and 8 key heads:
-// 64 rows each 53 against 66 us, 96 rows 70 against 69, 128 rows 87 against 72; with 48 to 128 rows (mean 80) and 1600
-// to 4096 keys 74 against 61.
-int ca_rows(int64_t T, int64_t B, int64_t G) { return T * G <= 8 * B ? 8 : T * G <= 72 * B ? 16 : CA_WIDE_ROWS; }
+// 48 rows each 45 against 53 us, 56 rows 52 against 53, 64 rows 54 against 53, 72 rows 60 against 54, 96 rows 72
+// against 55.
+int ca_rows(int64_t T, int64_t B, int64_t G) { return T * G <= 8 * B ? 8 : T * G <= 60 * B ? 16 : CA_WIDE_ROWS; }
 
 bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   return D == CA_D && T >= 0 && B >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hkv <= CONVROT_MAX_CACHE_HEADS &&
@@ -714,6 +797,9 @@ cudaError_t ca_run(CaParams p, int rows, bool f16, int64_t cells, uint8_t* ws, c
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if (rows == CA_WIDE_ROWS)
+    return f16 ? cudaLaunchKernelEx(&cfg, cache_attention_join_wide_kernel<true>, p)
+               : cudaLaunchKernelEx(&cfg, cache_attention_join_wide_kernel<false>, p);
   return f16 ? cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<true>, p, rows)
              : cudaLaunchKernelEx(&cfg, cache_attention_join_kernel<false>, p, rows);
 }

@@ -16,17 +16,26 @@
 //   warp 13        : issues S = Q K^T (kind::i8, 128 x 128 x 128) and O += P V
 //                    (kind::f16, fp16 operands);
 //   warps 14, 15   : idle; they complete a register group.
-// A tile is one pass over its logits at the row's reference, 64 keys at a time: with
-// a row's 128 logits held in registers, and their maximum taken first, the code of a
-// tile no longer fits the instruction cache and a tile took 3.8 us where it takes 2.2.
+// A tile is one pass over its logits at the row's reference, 16 keys at a time. The
+// roles of a CTA run different code at once, and what they share is the instruction
+// cache: with a row's 128 logits in registers, and their maximum taken first, a tile
+// took 3.8 us; rolled over 64 keys the trees of 8 sequences took 61 us, over 32 57.6, over
+// 16 54.6, with the values' loop rolled too 54.3. Splitting a tile into halves with barriers
+// of their own, so that one half's products run during the other's softmax, cost more in
+// code than it hid (58.7).
 // The reference is chosen so that the weights, not the exponentials, fit fp16: the
 // largest weight so far lies between 1 and 2^15, whatever the range of the value
 // scales. A row whose weights have grown takes it up at the next tile (that alone:
 // 67 to 60 us for a tree of 64 drafts behind 32768 keys); only where a weight passes
 // 2^15 within one tile is the tile taken again, at a reference from its largest logit
-// and scale, and from the weights that gives. What bounds a tile now: the two passes
-// of 3400 cycles that share a scheduler (2048 of them the exponentials), and between
-// them the turn of the products, which need the logits read before the next are made.
+// and scale, and from the weights that gives.
+// A run costs about as much as three tiles beside its tiles. Its first two tiles' keys
+// are fetched before its queries are in place, their pages looked up by eight lanes at
+// once, and the parts it leaves for the join lie four channels of all rows after one
+// another, so that both sides move whole lines: 54.3 to 43.9 us for the trees of 8
+// sequences. What bounds a tile now (2 us per SM): the latencies of a pass, 1024 cycles of
+// which are the exponentials, and between passes the turn of the products, which need the
+// logits read before the next are made.
 // Every wait is bounded.
 
 #include <cuda.h>
@@ -116,8 +125,7 @@ __device__ __forceinline__ float2 cw_logits(uint32_t a, uint32_t b, float2 scale
   return __fmul2_rn(__fadd2_rn(x, make_float2(-12582912.0f, -12582912.0f)), scale);
 }
 
-// The largest logit of a row among the keys it sees, without the row's factor. Rolled, 32 keys at a time, here
-// and below: unrolled over the tile the code no longer fits the instruction cache.
+// The largest logit of a row among the keys it sees, without the row's factor.
 __device__ __forceinline__ float cw_top(uint32_t tS, const uint32_t (&vis)[4], const float* sk) {
   float top = -INFINITY;
 #pragma unroll 1
@@ -145,43 +153,44 @@ __device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, const u
   float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   float big[2] = {0.0f, 0.0f};
 #pragma unroll 1
-  for (int h = 0; h < 2; ++h) {
-    uint32_t a[2][32];
-    tmem_ld_32x32b_x32(tS + h * 64, a[0]);
-    tmem_ld_32x32b_x32(tS + h * 64 + 32, a[1]);
-    const uint32_t on[2] = {h == 0 ? vis[0] : vis[2], h == 0 ? vis[1] : vis[3]};
-    const float* skh = sk + h * 64;
-    const float* svh = sv + h * 64;
-    uint8_t* to = line + h * CW_HALF;
-    tmem_ld_wait_regs(a[0]);
-    tmem_ld_wait_regs(a[1]);
+  for (int w = 0; w < 8; ++w) {
+    uint32_t a[16];
+    tmem_ld_32x32b_x16(tS + w * 16, a);
+    float4 fks[4], fvs[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t w[4];
+    for (int i = 0; i < 4; ++i) {
+      fks[i] = *reinterpret_cast<const float4*>(sk + w * 16 + 4 * i);
+      fvs[i] = *reinterpret_cast<const float4*>(sv + w * 16 + 4 * i);
+    }
+    tmem_ld_wait_regs16(a);
+    const uint32_t on = (w < 4 ? (w < 2 ? vis[0] : vis[1]) : (w < 6 ? vis[2] : vis[3])) >> (16 * (w & 1));
+    uint8_t* to = line + (w >= 4 ? CW_HALF : 0);
+    const int c0 = 2 * (w & 3);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t out[4];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        const float4 fk = *reinterpret_cast<const float4*>(skh + i * 8 + 4 * q);
-        const float4 fv = *reinterpret_cast<const float4*>(svh + i * 8 + 4 * q);
+        const float4 fk = fks[2 * i + q], fv = fvs[2 * i + q];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int k = i * 8 + 4 * q + 2 * e;
-          const float2 u = cw_logits(a[k >> 5][k & 31], a[k >> 5][(k & 31) + 1],
-                                     e == 0 ? make_float2(fk.x, fk.y) : make_float2(fk.z, fk.w));
+          const float2 u = cw_logits(a[k], a[k + 1], e == 0 ? make_float2(fk.x, fk.y) : make_float2(fk.z, fk.w));
           const float2 t = __ffma2_rn(c2, u, nref);
           float2 pr = make_float2(ex2_approx(t.x), ex2_approx(t.y));
           float2 x = __fmul2_rn(pr, e == 0 ? make_float2(fv.x, fv.y) : make_float2(fv.z, fv.w));
           if (MASKED) {
-            const bool y = on[k >> 5] >> (k & 31) & 1u, z = on[k >> 5] >> ((k & 31) + 1) & 1u;
+            const bool y = on >> k & 1u, z = on >> (k + 1) & 1u;
             pr = make_float2(y ? pr.x : 0.0f, z ? pr.y : 0.0f);
             x = make_float2(y ? x.x : 0.0f, z ? x.y : 0.0f);
           }
           part[e] = __fadd2_rn(part[e], pr);
           big[e] = fwht::fmax3f(big[e], x.x, x.y);
           const __half2 hx = __floats2half2_rn(x.x, x.y);
-          w[2 * q + e] = *reinterpret_cast<const uint32_t*>(&hx);
+          out[2 * q + e] = *reinterpret_cast<const uint32_t*>(&hx);
         }
       }
-      *reinterpret_cast<uint4*>(to + ((i ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(to + (((c0 + i) ^ sw) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
   const float2 all = __fadd2_rn(part[0], part[1]);
@@ -388,9 +397,11 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           const bool over = !(big <= CW_MOST) || !(sum <= 0x1p110f);
           const bool under = fresh && big > 0.0f && big < 1.0f;
           if (attempt == 3 || !__any_sync(0xFFFFFFFFu, over || under)) break;
-          const float at = bound();
-          if (over) now = at, fresh = true;
-          else if (under) now += exponent_of(big), fresh = false;
+          if (__any_sync(0xFFFFFFFFu, over)) {
+            const float at = bound();
+            if (over) now = at, fresh = true;
+          }
+          if (!over && under) now += exponent_of(big), fresh = false;
         }
         weighed |= big > 0.0f;
         const float scale = now == ref ? 1.0f : ex2_approx(ref - now);
@@ -434,38 +445,56 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       const bool whole = r.t0 == 0 && r.t1 == walk.s.tiles;
       const uint32_t tO0 = tmem + lanes + 256, tO1 = tO0 + 128;
       const bool alive = *abort == 0;  // else there may be no sums
-      float v[64];
-      // whole: the last butterfly stage, between channels 64 apart, comes first; part: this half's channels
-      const int from = whole ? 0 : pipe * 64;
-      const float sign = whole ? (pipe == 0 ? 1.0f : -1.0f) : 0.0f;
-      const float g0 = sign * f0, g1 = sign * f1;
-#pragma unroll
-      for (int ch = 0; ch < 4; ++ch) {
-        uint32_t a[16], b[16];
-        tmem_ld_32x32b_x16(tO0 + from + ch * 16, a);
-        if (whole) tmem_ld_32x32b_x16(tO0 + 64 + ch * 16, b);
-        tmem_ld_wait_regs16(a);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[ch * 16 + i] = __uint_as_float(a[i]) * f0;
-        if (whole) {
-          tmem_ld_wait_regs16(b);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[ch * 16 + i] = fmaf(__uint_as_float(b[i]), g0, v[ch * 16 + i]);
-        }
-        if (second) {
-          tmem_ld_32x32b_x16(tO1 + from + ch * 16, a);
-          if (whole) tmem_ld_32x32b_x16(tO1 + 64 + ch * 16, b);
+      if (!whole) {
+        // this half's channels, unnormalised; rolled, for the instruction cache
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (r.t0 == 0 ? 1 : 0);
+        // four channels of all rows after one another, so that a warp's stores are contiguous
+        float4* dst = reinterpret_cast<float4*>(p.part) + (slot * (CA_D / 4) + 16 * pipe) * CA_WIDE_ROWS + row;
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ++ch, dst += 4 * CA_WIDE_ROWS) {
+          uint32_t a[16], b[16];
+          tmem_ld_32x32b_x16(tO0 + 64 * pipe + ch * 16, a);
+          if (second) tmem_ld_32x32b_x16(tO1 + 64 * pipe + ch * 16, b);
           tmem_ld_wait_regs16(a);
+          float v[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[ch * 16 + i] = fmaf(__uint_as_float(a[i]), f1, v[ch * 16 + i]);
-          if (whole) {
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(a[i]) * f0;
+          if (second) {
             tmem_ld_wait_regs16(b);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[ch * 16 + i] = fmaf(__uint_as_float(b[i]), g1, v[ch * 16 + i]);
+            for (int i = 0; i < 16; ++i) v[i] = fmaf(__uint_as_float(b[i]), f1, v[i]);
+          }
+          if (row < r.rows && alive) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              dst[k * CA_WIDE_ROWS] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
           }
         }
-      }
-      if (whole) {
+        if (pipe == 0 && row < r.rows && alive) p.part_ml[slot * CA_WIDE_ROWS + row] = make_float2(top, total);
+      } else {
+        // the last butterfly stage, between channels 64 apart, comes first
+        float v[64];
+        const float sign = pipe == 0 ? 1.0f : -1.0f;
+        const float g0 = sign * f0, g1 = sign * f1;
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t a[16], b[16];
+          tmem_ld_32x32b_x16(tO0 + ch * 16, a);
+          tmem_ld_32x32b_x16(tO0 + 64 + ch * 16, b);
+          tmem_ld_wait_regs16(a);
+          tmem_ld_wait_regs16(b);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[ch * 16 + i] = fmaf(__uint_as_float(b[i]), g0, __uint_as_float(a[i]) * f0);
+          if (second) {
+            tmem_ld_32x32b_x16(tO1 + ch * 16, a);
+            tmem_ld_32x32b_x16(tO1 + 64 + ch * 16, b);
+            tmem_ld_wait_regs16(a);
+            tmem_ld_wait_regs16(b);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              v[ch * 16 + i] = fmaf(__uint_as_float(b[i]), g1, fmaf(__uint_as_float(a[i]), f1, v[ch * 16 + i]));
+          }
+        }
         const float norm = total == 0.0f ? 0.0f : fwht::kInvSqrt128 / total;
 #pragma unroll
         for (int i = 0; i < 64; ++i) v[i] = total == 0.0f ? 0.0f : v[i] * norm;
@@ -484,12 +513,6 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
                 fwht::narrow_pair<F16>(v[8 * k], v[8 * k + 1]), fwht::narrow_pair<F16>(v[8 * k + 2], v[8 * k + 3]),
                 fwht::narrow_pair<F16>(v[8 * k + 4], v[8 * k + 5]), fwht::narrow_pair<F16>(v[8 * k + 6], v[8 * k + 7]));
         }
-      } else if (row < r.rows && alive) {
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (r.t0 == 0 ? 1 : 0);
-        float4* dst = reinterpret_cast<float4*>(p.part + (slot * CA_WIDE_ROWS + row) * CA_D + 64 * pipe);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        if (pipe == 0) p.part_ml[slot * CA_WIDE_ROWS + row] = make_float2(top, total);
       }
       if (r.t0 == 0 && !whole) {
         // the piece ends inside an item that begins in it: it describes the item to the join
@@ -603,9 +626,11 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         give_scales(0, cell0, k0, v0);
       }
       cw_sync(0, CW_THREADS);
-      for (int n = 0; n < tiles; n += 2) {
+#pragma unroll 1
+      for (int n = 0; n < tiles; ++n) {
         if (!tile(n, code_a, code_b)) break;
-        if (n + 1 < tiles && !tile(n + 1, code_b, code_a)) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) code_a[i] = code_b[i];
       }
       used[0] += (r.t1 - r.t0 + 1) / 2;
       used[1] += (r.t1 - r.t0) / 2;
@@ -618,35 +643,32 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       int issued[2] = {0, 0};
       while (walk.next(p, &r, bad)) {
         if (walk.s.keys == 0) continue;
-        cw_sync(0, CW_THREADS);
-        if (lane == 0) {
-          const int32_t* table = p.pages + walk.b * p.table_stride;
-          bool ok = true;
-          for (int t = r.t0; t < r.t1; ++t) {
-            const int pipe = (t - r.t0) & 1, use = used[pipe] + ((t - r.t0) >> 1);
-            if (use > 0) ok = wait(bar(pipe, kKEmpty), use - 1);
-            if (!ok) break;
-            int cell[8], boxes = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int key = t * CW_KT + 16 * i;
-              cell[i] = -1;
-              if (key < walk.s.keys) {
-                const int page = __ldg(table + (key >> p.page_shift));
-                if (static_cast<uint32_t>(page) < static_cast<uint32_t>(p.num_pages)) {
-                  cell[i] = ((page * p.Hkv + r.head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
-                  ++boxes;
-                }
-              }
-            }
-            mbar_arrive_expect_tx(bar(pipe, kKFull), boxes * 16 * CA_D);
-            uint8_t* to = smem + L::kOffK + pipe * CW_HALF;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (cell[i] >= 0) tma_load_2d(to + i * 16 * CA_D, &tmK, bar(pipe, kKFull), 0, cell[i]);
-            issued[pipe] = use + 1;
-          }
+        const int32_t* table = p.pages + walk.b * p.table_stride;
+        // a lane per box of 16 keys; the pages of a tile are looked up a tile ahead
+        auto cell_of = [&](int t) {
+          const int key = t * CW_KT + 16 * lane;
+          if (lane >= CW_KT / 16 || key >= walk.s.keys) return -1;
+          const int page = __ldg(table + (key >> p.page_shift));
+          if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) return -1;
+          return ((page * p.Hkv + r.head) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+        };
+        int ahead = cell_of(r.t0);
+        // the first two tiles need no query: they are on their way before the queries are in place
+        bool ok = true;
+        for (int t = r.t0; t < r.t1; ++t) {
+          const int pipe = (t - r.t0) & 1, use = used[pipe] + ((t - r.t0) >> 1);
+          const int cell = ahead;
+          if (t + 1 < r.t1) ahead = cell_of(t + 1);
+          if (t == r.t0 + 2) cw_sync(0, CW_THREADS);
+          if (ok && use > 0) ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kKEmpty), use - 1));
+          if (!ok) continue;
+          const int boxes = __popc(__ballot_sync(0xFFFFFFFFu, cell >= 0));
+          if (lane == 0) mbar_arrive_expect_tx(bar(pipe, kKFull), boxes * 16 * CA_D);
+          __syncwarp();
+          if (cell >= 0) tma_load_2d(smem + L::kOffK + pipe * CW_HALF + lane * 16 * CA_D, &tmK, bar(pipe, kKFull), 0, cell);
+          issued[pipe] = use + 1;
         }
+        if (r.t1 - r.t0 <= 2) cw_sync(0, CW_THREADS);
         used[0] += (r.t1 - r.t0 + 1) / 2;
         used[1] += (r.t1 - r.t0) / 2;
         __syncwarp();
