@@ -65,19 +65,23 @@ __device__ __forceinline__ float2 rope_turn(const RopeParams& p, int64_t n, int 
   return make_float2(c, p.inverse ? -s : s);
 }
 
-// Sixteen channels of a head: the two runs of eight that hold pairs 8c .. 8c + 7.
+// Sixteen channels of a head, two runs of eight: the first and the second channels of eight pairs, or,
+// interleaved, four pairs each.
 template <bool F16, bool INTER>
-__device__ __forceinline__ void rope_apply(uint4& lo, uint4& hi, const float2 (&cs)[8]) {
+__device__ __forceinline__ void rope_apply(uint4& lo, uint4& hi, const float2 (&cs)[8], bool turn_lo, bool turn_hi) {
   uint32_t* a = reinterpret_cast<uint32_t*>(&lo);
   uint32_t* b = reinterpret_cast<uint32_t*>(&hi);
   if (INTER) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 u = fwht::widen_pair<F16>(a[i]), v = fwht::widen_pair<F16>(b[i]);
-      a[i] = fwht::narrow_pair<F16>(fmaf(u.x, cs[i].x, -u.y * cs[i].y), fmaf(u.y, cs[i].x, u.x * cs[i].y));
-      b[i] = fwht::narrow_pair<F16>(fmaf(v.x, cs[4 + i].x, -v.y * cs[4 + i].y), fmaf(v.y, cs[4 + i].x, v.x * cs[4 + i].y));
+      const uint32_t x = fwht::narrow_pair<F16>(fmaf(u.x, cs[i].x, -u.y * cs[i].y), fmaf(u.y, cs[i].x, u.x * cs[i].y));
+      const uint32_t y =
+          fwht::narrow_pair<F16>(fmaf(v.x, cs[4 + i].x, -v.y * cs[4 + i].y), fmaf(v.y, cs[4 + i].x, v.x * cs[4 + i].y));
+      a[i] = turn_lo ? x : a[i];
+      b[i] = turn_hi ? y : b[i];
     }
-  } else {
+  } else if (turn_lo) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 u = fwht::widen_pair<F16>(a[i]), v = fwht::widen_pair<F16>(b[i]);
@@ -99,10 +103,14 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const RopeParams 
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.tok;
   const int64_t n = first + slot;
   const bool mine = slot < p.tok && n < p.tokens;
-  const bool turned = 8 * c < pairs;
-  // channels of the thread's two runs of eight
-  const int d_lo = !turned ? 16 * c : INTER ? 16 * c : 8 * c;
-  const int d_hi = !turned || INTER ? d_lo + 8 : pairs + 8 * c;
+  // Channels of the thread's two runs of eight. Neighbouring threads take neighbouring runs, also of interleaved
+  // pairs: with sixteen channels in a row per thread 4224 tokens of 32 heads took
+  // 16.8 us for 14.1.
+  const bool split = !INTER && 8 * c < pairs;
+  const int d_lo = INTER || split ? 8 * c : 16 * c;
+  const int d_hi = INTER ? (p.D >> 1) + 8 * c : split ? pairs + 8 * c : d_lo + 8;
+  const bool turn_lo = INTER ? d_lo < p.R : split, turn_hi = INTER ? d_hi < p.R : split;
+  const int pair_lo = INTER ? d_lo >> 1 : 8 * c, pair_hi = INTER ? d_hi >> 1 : 8 * c + 4;  // of four each
   const int64_t b = mine ? static_cast<uint32_t>(n) / static_cast<uint32_t>(p.S) : 0, s = mine ? n - b * p.S : 0;
   const uint16_t* x = p.x + b * p.xb + s * p.xs;
   uint16_t* y = p.y + b * p.yb + s * p.ys;
@@ -124,13 +132,16 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const RopeParams 
   if (!mine) return;
   float2 cs[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) cs[i] = turned ? table[slot * pairs + 8 * c + i] : make_float2(1.0f, 0.0f);
+  for (int i = 0; i < 4; ++i) {
+    cs[i] = turn_lo ? table[slot * pairs + pair_lo + i] : make_float2(1.0f, 0.0f);
+    cs[4 + i] = turn_hi ? table[slot * pairs + pair_hi + i] : make_float2(1.0f, 0.0f);
+  }
   for (int hb = h0; hb < p.H; hb += kRopeAhead * p.hp) {
 #pragma unroll
     for (int k = 0; k < kRopeAhead; ++k) {
       const int h = hb + k * p.hp;
       if (h < p.H) {
-        if (turned) rope_apply<F16, INTER>(lo[k], hi[k], cs);
+        rope_apply<F16, INTER>(lo[k], hi[k], cs, turn_lo, turn_hi);
         *reinterpret_cast<uint4*>(y + h * p.yh + d_lo) = lo[k];
         *reinterpret_cast<uint4*>(y + h * p.yh + d_hi) = hi[k];
       }
