@@ -650,3 +650,57 @@ def test_native_and_python_binding_agree(cr, monkeypatch):
         cache.read(lengths, dtype=torch.float32)
     with pytest.raises(ValueError):
         cache.read(lengths, dtype=torch.bfloat16, K=torch.empty(6, 4, 128, dtype=torch.float16, device="cuda"))
+
+
+def test_first_calls_may_be_captured():
+    """In a fresh process nothing has been launched or looked up before the capture."""
+    import subprocess
+    import sys
+
+    code = """
+import torch
+import w8a8_rotated_int8_token_b200 as cr
+g = torch.Generator("cuda").manual_seed(3)
+rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+cache = cr.ConvRotCache(16, 2, 16)
+freq, axis = cr.convrot_rope_tables([32, 32])
+q, k, v = rnd(100, 8, 128), rnd(100, 2, 128), rnd(100, 2, 128)
+pos = torch.arange(200, device="cuda", dtype=torch.int32).view(2, 100)
+slots = torch.arange(100, device="cuda", dtype=torch.int32)
+pages = torch.arange(16, device="cuda", dtype=torch.int32)[None]
+lengths = torch.tensor([100], device="cuda", dtype=torch.int32)
+starts = torch.tensor([0, 100], device="cuda", dtype=torch.int32)
+def step():
+    y = cr.convrot_rope(q, pos, freq, axis)
+    cache.append(cr.convrot_rope(k, pos, freq, axis), v, slots)
+    wide = cache.attention(y, pages, lengths, starts)            # many rows
+    few = cache.attention(y[99:], pages, lengths)                # one token
+    return wide, few, *cache.read(slots)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+for t in cache.cells:
+    t.zero_()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+assert all(bool(t.isfinite().all()) and bool(t.any()) for t in got)
+torch.cuda.synchronize()
+del graph
+print("captured")
+"""
+    import os
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_sixty_rows_decide_the_tile(cr):
+    """Either side of the rule that picks 16 or 128 rows, and sequences far from the mean."""
+    for news in (7, 8, 15, 16):  # 4 heads a key head: 28, 32, 60, 64 rows each
+        s = Setup(cr, [(40 + news, news), (333, news), (news, news)], 8, 2, 32, seed=news)
+        s.check(s.run())
+    s = Setup(cr, [(200, 40), (77, 1), (50, 0), (129, 4)], 8, 2, 16, "f16", seed=9)
+    s.check(s.run())

@@ -14,8 +14,8 @@
 // and vector; with 16 lanes it would be twice as many per vector).
 // Reading transforms whole numbers, exact in any order, so there the tensor cores
 // take five stages at once (a product with the 32-point signs, eight instructions for
-// eight vectors) and nothing crosses lanes: 32768 scattered tokens of 8 heads in 37.3 us
-// (204 MB, 85 % of the copy bandwidth; the scales of scattered cells cost a 32-byte
+// eight vectors) and nothing crosses lanes: 32768 scattered tokens of 8 heads in 36.3 us
+// (204 MB, 87 % of the copy bandwidth; the scales of scattered cells cost a 32-byte
 // sector each, 17 MB more) against 40.9 with the stages of writing, where shuffles and
 // narrow loads kept the first-level data path 85 % busy, 47.3 with a thread per vector
 // and 53.9 with the first four stages in pairs of fp16.
@@ -144,27 +144,25 @@ __device__ __forceinline__ void mma_codes(uint32_t (&d)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c));
 }
 
-// The signs of the 32-point transform as the operand of mma_codes: lane 4 g + t holds rows 8 t + 4 h + e (byte e of
-// word h) of column 8 (g / 2) + 2 n + g % 2 in sign[n][h], so that lane t of a vector brings channels 8 t .. + 7 of a
-// block of 32 and gets their sums back.
-__device__ __forceinline__ void block_signs(int lane, uint32_t (&sign)[4][2]) {
+// The signs of the 32-point transform as the operand of mma_codes: lane 4 g + t needs rows 8 t + 4 h + e (byte e of
+// word h) of column 8 (g / 2) + 2 n + g % 2, so that lane t of a vector brings channels 8 t .. + 7 of a block of 32
+// and gets their sums back. Of n that leaves its low bit to the word, sign[n % 2], and its high bit to an inversion
+// of the second half's rows (h = 1), sign[2 + n % 2].
+__device__ __forceinline__ void block_signs(int lane, uint32_t (&sign)[4]) {
   const int g = lane >> 2, t = lane & 3;
-#pragma unroll
-  for (int n = 0; n < 4; ++n) {
-    const int col = 8 * (g >> 1) + 2 * n + (g & 1);
-    // bytes 0 .. 3 of columns 0 .. 3 (mod 4)
-    const uint32_t low = n & 1 ? ((g & 1) != 0 ? 0x01FFFF01u : 0xFFFF0101u) : ((g & 1) != 0 ? 0xFF01FF01u : 0x01010101u);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      sign[n][h] = (__popc((8 * t + 4 * h) & col) & 1) != 0 ? low ^ 0xFEFEFEFEu : low;  // 1 and -1 change places
-  }
+  const uint32_t flip = (__popc(t & (g >> 1)) & 1) != 0 ? 0xFEFEFEFEu : 0u;  // 1 and -1 change places
+  // bytes 0 .. 3 of columns 0 .. 3 (mod 4)
+  sign[0] = ((g & 1) != 0 ? 0xFF01FF01u : 0x01010101u) ^ flip;
+  sign[1] = ((g & 1) != 0 ? 0x01FFFF01u : 0xFFFF0101u) ^ flip;
+  sign[2] = sign[0] ^ 0xFEFEFEFEu;
+  sign[3] = sign[1] ^ 0xFEFEFEFEu;
 }
 
 // A vector's four 8-byte pieces of codes (channels 32 j + 8 l .. + 7) to the same channels of the vector; zeros where
 // there is no cell. The sums of 128 codes are whole numbers and every step is exact: the stages on index bits
 // 0 to 4 are the matrix product, those on 5 and 6 in registers.
 template <bool F16>
-__device__ __forceinline__ void read_cell(const uint2 (&w)[4], const uint32_t (&sign)[4][2], float scale, bool there,
+__device__ __forceinline__ void read_cell(const uint2 (&w)[4], const uint32_t (&sign)[4], float scale, bool there,
                                           bool any, uint16_t* dst) {
   constexpr uint32_t kBits = 0x4B400000u;  // 1.5 * 2^23: plus a sum as an integer it is that plus the sum as a float
   const float2 bias = make_float2(-12582912.0f, -12582912.0f);
@@ -174,7 +172,7 @@ __device__ __forceinline__ void read_cell(const uint2 (&w)[4], const uint32_t (&
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
       uint32_t d[4];
-      mma_codes(d, w[j].x, w[j + 1].x, w[j].y, w[j + 1].y, sign[n][0], sign[n][1], kBits);
+      mma_codes(d, w[j].x, w[j + 1].x, w[j].y, w[j + 1].y, sign[n & 1], sign[n], kBits);
       v[j][n] = __fadd2_rn(make_float2(__uint_as_float(d[0]), __uint_as_float(d[1])), bias);
       v[j + 1][n] = __fadd2_rn(make_float2(__uint_as_float(d[2]), __uint_as_float(d[3])), bias);
     }
@@ -201,7 +199,7 @@ __device__ __forceinline__ void read_cell(const uint2 (&w)[4], const uint32_t (&
 }
 
 template <bool F16>
-__global__ void __launch_bounds__(kCellThreads) cache_read_kernel(const CellParams p) {
+__global__ void __launch_bounds__(kCellThreads, 16) cache_read_kernel(const CellParams p) {
   const int pair = (blockIdx.x * kCellThreads + threadIdx.x) >> 2;
   const int l = threadIdx.x & 3;
   const bool there = pair < p.pairs;
@@ -222,7 +220,7 @@ __global__ void __launch_bounds__(kCellThreads) cache_read_kernel(const CellPara
     ks = __ldg(p.k_scale + c.cell);
     vs = __ldg(p.v_scale + c.cell);
   }
-  uint32_t sign[4][2];
+  uint32_t sign[4];
   block_signs(threadIdx.x & 31, sign);
   read_cell<F16>(k, sign, ks, there, c.cell >= 0, p.k + c.t * p.kt + c.h * p.kh + 8 * l);
   read_cell<F16>(v, sign, vs, there, c.cell >= 0, p.v + c.t * p.vt + c.h * p.vh + 8 * l);
