@@ -64,10 +64,11 @@ constexpr int CA_KT = CA_SUB * CA_WARPS;   // keys of a tile
 constexpr int CA_CODES = CA_SUB * CA_D;    // key (or value) codes of a stage
 constexpr int CA_STAGE = 2 * CA_CODES;
 constexpr int CA_QPITCH = CA_D + 16;       // bytes between query rows in shared memory
-// What a run costs beside its tiles, and the least a piece takes, in tiles: with 6 and 6 the trees of 8 sequences took
-// 74 us against 83 with 4 and 102 with none, and one sequence of 4224 keys 12.6 us against 14.1 with a least of 8.
+// What a run costs beside its tiles, and the least a piece takes, in tiles: with a cost of 6 the trees of 8 sequences
+// took 74 us against 83 with 4 and 102 with none (64 long sequences 218 us, 226 with 4, 223 with 8), and one sequence of
+// 4224 keys takes 10.9 us with a least of 3, 12.4 with 2, 11.4 with 4, 11.7 with 6.
 constexpr int CA_SETUP = 6;
-constexpr int CA_LEAST = 6;
+constexpr int CA_LEAST = 3;
 
 // A shape of CTA: 8 NT rows, stages of a warp's ring, CTAs per SM.
 template <int NT, int ST, int OCC>
