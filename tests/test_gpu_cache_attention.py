@@ -697,9 +697,9 @@ print("captured")
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
-def test_sixty_rows_decide_the_tile(cr):
+def test_mean_rows_decide_the_tile(cr):
     """Either side of the rule that picks 16 or 128 rows, and sequences far from the mean."""
-    for news in (7, 8, 15, 16):  # 4 heads a key head: 28, 32, 60, 64 rows each
+    for news in (2, 3, 7, 8, 9, 16):  # 4 heads a key head: 8, 12, 28, 32, 36, 64 rows each
         s = Setup(cr, [(40 + news, news), (333, news), (news, news)], 8, 2, 32, seed=news)
         s.check(s.run())
     s = Setup(cr, [(200, 40), (77, 1), (50, 0), (129, 4)], 8, 2, 16, "f16", seed=9)

@@ -747,10 +747,11 @@ CaLayout ca_layout(int rows) {
 }
 
 // The tile of rows by the mean number of rows a sequence has for a key head. A taller tile reads the keys for
-// fewer tiles, a lower one wastes fewer of its rows. 16 rows against 128, 8 sequences of 4096 keys and 8 key heads:
-// 48 rows each 45 against 53 us, 56 rows 52 against 53, 64 rows 54 against 53, 72 rows 60 against 54, 96 rows 72
-// against 55.
-int ca_rows(int64_t T, int64_t B, int64_t G) { return T * G <= 8 * B ? 8 : T * G <= 60 * B ? 16 : CA_WIDE_ROWS; }
+// fewer tiles, a lower one wastes fewer of its rows. 16 rows against 128, 8 sequences and 8 key heads: behind 4096 keys
+// 32 rows each 38 against 46 us, 40 rows 50 against 46, 64 rows 63 against 47, 128 rows 112 against 50; behind 512 keys
+// 32 rows 19 against 23, 40 rows 22 against 23, 56 rows 25 against 23; behind 16384 32 rows 106 against 136, 40 rows
+// 149 against 136; 4 to 96 rows (mean 48) behind 4096 keys 57 against 47.
+int ca_rows(int64_t T, int64_t B, int64_t G) { return T * G <= 8 * B ? 8 : T * G <= 32 * B ? 16 : CA_WIDE_ROWS; }
 
 bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
   return D == CA_D && T >= 0 && B >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && Hkv <= CONVROT_MAX_CACHE_HEADS &&

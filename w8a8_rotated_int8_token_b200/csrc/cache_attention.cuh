@@ -137,7 +137,7 @@ template <class Grain, int THREADS>
 __device__ __forceinline__ int64_t ca_piece(const CaParams& p, int64_t* scan, CaWalk<Grain>* walk, int& bad) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (THREADS <= 128 && p.B <= 32) {  // every warp finds it by itself (not worth its registers in the wide kernel)
+  if (p.B <= 32) {  // every warp finds it by itself
     const CaSeq s = ca_seq<Grain>(p, lane < p.B ? lane : p.B - 1, bad);
     const int64_t count = lane < p.B ? s.count : 0;
     int64_t incl = count;

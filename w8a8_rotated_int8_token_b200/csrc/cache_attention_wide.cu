@@ -14,8 +14,7 @@
 //                    tile and two tiles ahead;
 //   warp 12        : key codes by TMA (boxes of 16 keys: pages are no smaller);
 //   warp 13        : issues S = Q K^T (kind::i8, 128 x 128 x 128) and O += P V
-//                    (kind::f16, fp16 operands);
-//   warps 14, 15   : idle; they complete a register group.
+//                    (kind::f16, fp16 operands).
 // A tile is one pass over its logits at the row's reference, 16 keys at a time. The
 // roles of a CTA run different code at once, and what they share is the instruction
 // cache: with a row's 128 logits in registers, and their maximum taken first, a tile
@@ -33,7 +32,9 @@
 // are fetched before its queries are in place, their pages looked up by eight lanes at
 // once, and the parts it leaves for the join lie four channels of all rows after one
 // another, so that both sides move whole lines: 54.3 to 43.9 us for the trees of 8
-// sequences. What bounds a tile now (2 us per SM): the latencies of a pass, 1024 cycles of
+// sequences (42.5 since the warps keep the registers they are launched with: handing
+// some of the others' to the softmax warps gained nothing and cost spills).
+// What bounds a tile now (2 us per SM): the latencies of a pass, 1024 cycles of
 // which are the exponentials, and between passes the turn of the products, which need the
 // logits read before the next are made.
 // Every wait is bounded.
@@ -57,11 +58,8 @@ namespace convrot {
 namespace {
 
 constexpr int CW_KT = 128;           // keys of a tile
-constexpr int CW_THREADS = 512;
+constexpr int CW_THREADS = 448;
 constexpr int CW_HALF = 128 * 128;   // 128 rows of 128 bytes
-// Registers a thread: the kernel is launched with 128 for each of the four groups of four warps.
-constexpr int CW_REGS_SOFTMAX = 184, CW_REGS_VALUES = 96, CW_REGS_ISSUE = 48;
-static_assert(2 * CW_REGS_SOFTMAX + CW_REGS_VALUES + CW_REGS_ISSUE == 4 * 128, "the groups' shares are what was launched");
 constexpr uint64_t CW_TIMEOUT_NS = 2000000000ull;
 // a run costs about as much as three tiles beside its tiles
 using CwGrain = CaGrain<CA_WIDE_ROWS, CW_KT, 3, 2>;
@@ -94,15 +92,6 @@ enum CwBar { kKFull, kKEmpty, kSFull, kSEmpty, kPFull, kODone, kVFull, kSc0, kSc
 
 __device__ __forceinline__ void cw_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-template <int N>
-__device__ __forceinline__ void regs_more() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_fewer() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // A word of the keys below `n` among keys 32 w .. 32 w + 31 of a tile.
@@ -269,7 +258,6 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    regs_more<CW_REGS_SOFTMAX>();
     const int pipe = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
@@ -530,7 +518,6 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     if (tid == 0) p.cuts[blockIdx.x] = cut;
   } else if (warp < 12) {
     // ----------------------------------------------------------------- values
-    regs_fewer<CW_REGS_VALUES>();
     const int me = tid - 256;  // the thread's key of a tile, for the scales
     const int w4 = warp - 8;
     while (walk.next(p, &r, bad)) {
@@ -637,7 +624,6 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       cw_sync(0, CW_THREADS);
     }
   } else {
-    regs_fewer<CW_REGS_ISSUE>();
     if (warp == 12) {
       // ------------------------------------------------------------------ keys
       int issued[2] = {0, 0};
@@ -679,7 +665,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         for (int pipe = 0; pipe < 2; ++pipe)
           if (issued[pipe] > 0)
             mbar_wait_bounded(bar(pipe, kKFull), static_cast<uint32_t>((issued[pipe] - 1) & 1), nullptr, CW_TIMEOUT_NS);
-    } else if (warp == 13) {
+    } else {
       // -------------------------------------------------------------- products
       const uint32_t qa = smem_addr(smem + L::kOffQ);
       while (walk.next(p, &r, bad)) {
@@ -734,12 +720,6 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         mbar_wait_bounded(drain, 0u, nullptr, CW_TIMEOUT_NS);
       }
       __syncwarp();
-    } else {
-      while (walk.next(p, &r, bad)) {
-        if (walk.s.keys == 0) continue;
-        cw_sync(0, CW_THREADS);
-        cw_sync(0, CW_THREADS);
-      }
     }
   }
   tc_fence_before();
