@@ -704,3 +704,23 @@ def test_mean_rows_decide_the_tile(cr):
         s.check(s.run())
     s = Setup(cr, [(200, 40), (77, 1), (50, 0), (129, 4)], 8, 2, 16, "f16", seed=9)
     s.check(s.run())
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (80, 2)])
+@pytest.mark.parametrize("value", [np.inf, 3e38, 1e30])
+def test_unseen_values_of_any_size(cr, hq, hkv, value):
+    """A draft that no mask names, with a value scale that would dwarf the others, beside them in one tile and
+    in a tile of its own kind behind them; seen by some rows only, it counts for those alone."""
+    tree = np.array([1, 3, 1, 9, 17, 33], np.uint64)  # nothing sees draft 2
+    for keys in (100, 131):
+        s = Setup(cr, [(keys, 6)], hq, hkv, 16, seed=8, tree=tree)
+        j = keys - 6 + 2
+        s.scales[0][s.pages[0, j // 16], :, j % 16] = np.nan
+        s.scales[1][s.pages[0, j // 16], :, j % 16] = value
+        s.check(s.run())
+    if value == 1e30:
+        tree[2] = 4 | 1
+        s = Setup(cr, [(100, 6)], hq, hkv, 16, seed=8, tree=tree)
+        j = 100 - 6 + 2
+        s.scales[1][s.pages[0, j // 16], :, j % 16] = value
+        s.check(s.run())

@@ -26,8 +26,8 @@
 // largest weight so far lies between 1 and 2^15, whatever the range of the value
 // scales. A row whose weights have grown takes it up at the next tile (that alone:
 // 67 to 60 us for a tree of 64 drafts behind 32768 keys); only where a weight passes
-// 2^15 within one tile is the tile taken again, at a reference from its largest logit
-// and scale, and from the weights that gives.
+// 2^15 within one tile, or a row's first ones are far below their bound, is the tile taken
+// again, at a reference from the logit and scale of each key.
 // A run costs about as much as three tiles beside its tiles. Its first two tiles' keys
 // are fetched before its queries are in place, their pages looked up by eight lanes at
 // once, and the parts it leaves for the join lie four channels of all rows after one
@@ -130,6 +130,30 @@ __device__ __forceinline__ float cw_top(uint32_t tS, const uint32_t (&vis)[4], c
     }
   }
   return top;
+}
+
+// The reference at which a row's largest weight among the keys it sees lies near 2, unless exponentials would pass
+// 2^CW_SPAN: from the logit and the scale of each key.
+__device__ __forceinline__ float cw_exact(uint32_t tS, float c, const uint32_t (&vis)[4], const float* sk) {
+  float top = -INFINITY, heavy = -INFINITY;
+#pragma unroll 1
+  for (int w = 0; w < 8; ++w) {
+    uint32_t a[16];
+    tmem_ld_32x32b_x16(tS + w * 16, a);
+    const uint32_t on = (w < 4 ? (w < 2 ? vis[0] : vis[1]) : (w < 6 ? vis[2] : vis[3])) >> (16 * (w & 1));
+    tmem_ld_wait_regs16(a);
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      const float2 u = cw_logits(a[k], a[k + 1], *reinterpret_cast<const float2*>(sk + w * 16 + k));
+      const float2 v = *reinterpret_cast<const float2*>(sk + 128 + w * 16 + k);
+      const float x = on >> k & 1u ? c * u.x : -INFINITY, y = on >> (k + 1) & 1u ? c * u.y : -INFINITY;
+      top = fwht::fmax3f(top, x, y);
+      // the exponent's bits as the last ones of 2^23: the sum is rounded to a whole number
+      heavy = fwht::fmax3f(heavy, x + __uint_as_float(0x4B000000u | (__float_as_uint(v.x) >> 23 & 255u)),
+                           y + __uint_as_float(0x4B000000u | (__float_as_uint(v.y) >> 23 & 255u)));
+    }
+  }
+  return fmaxf(heavy - (8388608.0f + 127.0f + 1.0f), top - CW_SPAN);
 }
 
 // One pass over a tile's logits: the weights of the row in fp16 into its line of the operand, the sum of the
@@ -362,34 +386,25 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
 #pragma unroll
           for (int w = 0; w < 4; ++w) vis[w] &= below(lim - key0, w) | placed(bits, context - key0, w);
         }
-        // A reference at which every weight of the tile is below 2^8, from its largest logit and largest scale.
         const float high = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-        const bool some = (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
-        auto bound = [&]() {
-          const float tm = c * cw_top(tS, vis, sk);
-          return fmaxf(high > 0.0f ? tm + exponent_of(high) - 7.0f : tm, tm - CW_SPAN);
-        };
+        const bool first = !weighed && (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
         float now = ref, sum, big;
-        bool fresh = false;  // `now` is such a bound: the weights may be far below it
         // A row whose weights have grown takes its reference up before they can pass fp16's range: one
         // rescaling of O instead of a second pass.
         if (largest > CW_GROWN) now += exponent_of(largest);
-        if (__any_sync(0xFFFFFFFFu, some && !weighed)) {
-          const float at = bound();
-          if (some && !weighed) now = at, fresh = true;
+        if (__any_sync(0xFFFFFFFFu, first)) {
+          // at this every weight of the tile is below 2^8, the largest usually little below
+          const float tm = c * cw_top(tS, vis, sk);
+          if (first) now = fmaxf(high > 0.0f ? tm + exponent_of(high) - 7.0f : tm, tm - CW_SPAN);
         }
 #pragma unroll 1
         for (int attempt = 0;; ++attempt) {
           if (masked) cw_pass<true>(tS, c, now, vis, sk, line, sw, &sum, &big);
           else cw_pass<false>(tS, c, now, vis, sk, line, sw, &sum, &big);
-          const bool over = !(big <= CW_MOST) || !(sum <= 0x1p110f);
-          const bool under = fresh && big > 0.0f && big < 1.0f;
-          if (attempt == 3 || !__any_sync(0xFFFFFFFFu, over || under)) break;
-          if (__any_sync(0xFFFFFFFFu, over)) {
-            const float at = bound();
-            if (over) now = at, fresh = true;
-          }
-          if (!over && under) now += exponent_of(big), fresh = false;
+          const bool lost = !(big <= CW_MOST) || !(sum <= 0x1p110f) || (first && high > 0.0f && big < 1.0f);
+          if (attempt == 1 || !__any_sync(0xFFFFFFFFu, lost)) break;
+          const float at = cw_exact(tS, c, vis, sk);
+          if (lost) now = at;
         }
         weighed |= big > 0.0f;
         const float scale = now == ref ? 1.0f : ex2_approx(ref - now);
