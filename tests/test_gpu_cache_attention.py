@@ -137,7 +137,11 @@ class Setup:
                         f = float((kk[on[i]] * tie[i, h]).sum(1).max()) * float(sq[i, h]) * scale
                         e += f * math.exp(f)
                     eps = 2.0**-11 + 2 * e + (keys / 16 + 64) * 2.0**-22
+                    # Keys without a value may hold all of a row's sum, and the others' weights be far below it: an
+                    # exponential below float32's 2^-126 may be lost, and where a row's sum is held below 2^101 a
+                    # weight rounded to fp16's 2^-25 is off by 2^-125 of the sum and less.
                     off = eps * (ws @ c) + 2.0**-24 * ws.max() * c[on[i]].sum(0)
+                    off = off + (2.0**-126 * s[on[i]] + 2.0**-125) @ c[on[i]]
                     u = OUT_REL[self.kind]
                     slack = np.linalg.norm(off) * (1 + u) + 8 * 2.0**-24 * np.linalg.norm(ws @ c)
                     bound = u * np.linalg.norm(want) + slack + OUT_ABS[self.kind] * math.sqrt(128)
@@ -724,3 +728,17 @@ def test_unseen_values_of_any_size(cr, hq, hkv, value):
         j = 100 - 6 + 2
         s.scales[1][s.pages[0, j // 16], :, j % 16] = value
         s.check(s.run())
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (80, 1)])
+def test_values_of_zero_before_others(cr, hq, hkv):
+    """Keys with large logits and values of zero, then small logits far below them, then large ones again: a
+    row's sum is kept through all of it. Many sequences, so that a CTA meets the whole of one."""
+    s = Setup(cr, [(768, 1)] * 160, hq, hkv, 64, seed=10)
+    for b in range(160):
+        for j in range(0, 768, 64):
+            page = s.pages[b, j // 64]
+            s.scales[0][page] *= 1e-6 if 256 <= j < 512 else 30.0
+            if j < 256:
+                s.scales[1][page] = 0.0
+    s.check(s.run(), sequences=range(0, 160, 16))

@@ -388,6 +388,8 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         }
         const float high = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
         const bool first = !weighed && (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
+        // the sum so far may be of keys without a value, and must stay in range where the reference comes down
+        const float least = l > 0.0f ? ref + exponent_of(l) - CW_SPAN : CA_NONE;
         float now = ref, sum, big;
         // A row whose weights have grown takes its reference up before they can pass fp16's range: one
         // rescaling of O instead of a second pass.
@@ -395,7 +397,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         if (__any_sync(0xFFFFFFFFu, first)) {
           // at this every weight of the tile is below 2^8, the largest usually little below
           const float tm = c * cw_top(tS, vis, sk);
-          if (first) now = fmaxf(high > 0.0f ? tm + exponent_of(high) - 7.0f : tm, tm - CW_SPAN);
+          if (first) now = fmaxf(high > 0.0f ? tm + exponent_of(high) - 7.0f : tm, fmaxf(tm - CW_SPAN, least));
         }
 #pragma unroll 1
         for (int attempt = 0;; ++attempt) {
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           const bool lost = !(big <= CW_MOST) || !(sum <= 0x1p110f) || (first && high > 0.0f && big < 1.0f);
           if (attempt == 1 || !__any_sync(0xFFFFFFFFu, lost)) break;
           const float at = cw_exact(tS, c, vis, sk);
-          if (lost) now = at;
+          if (lost) now = fmaxf(at, least);
         }
         weighed |= big > 0.0f;
         const float scale = now == ref ? 1.0f : ex2_approx(ref - now);
