@@ -228,3 +228,25 @@ def test_read_any_codes(cr, kind):
         ref = oracle.cache_value(codes, scale)
         own = 2 * 128 * 2.0**-53 * 128 * 128 / np.sqrt(128.0) * scale.astype(np.float64)[..., None]  # the oracle's, as above
         assert np.all(np.abs(x.double().cpu().numpy() - ref) <= (OUT_REL[kind] + 2.0**-22) * np.abs(ref) + OUT_ABS[kind] + own)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_read_with_a_last_warp_partly_without_tokens(cr, kind):
+    """Every count of vectors in the last warp (eight fill it), some of them without a cell: the bits of a read in
+    which each warp is full, and nothing behind the last token written."""
+    import torch
+
+    K, V = _heads(32, 1, kind, 5)
+    cache = cr.ConvRotCache(2, 1, 16)
+    slots = torch.randperm(32, device="cuda").to(torch.int32)
+    cache.append(K, V, slots)
+    full = cache.read(slots, _dtype(kind))
+    for T in range(1, 18):
+        some = slots[:T].clone()
+        some[T // 2] = -1
+        room = torch.full((2, 32, 1, 128), 3.0, dtype=_dtype(kind), device="cuda")
+        got = cache.read(some, K=room[0, :T], V=room[1, :T])
+        for x, want, rest in zip(got, full, room):
+            want = want[:T].clone()
+            want[T // 2] = 0.0
+            assert torch.equal(x, want) and bool((rest[T:] == 3.0).all())

@@ -167,6 +167,7 @@ __device__ __forceinline__ void read_cell(const uint2 (&w)[4], const uint32_t (&
   constexpr uint32_t kBits = 0x4B400000u;  // 1.5 * 2^23: plus a sum as an integer it is that plus the sum as a float
   const float2 bias = make_float2(-12582912.0f, -12582912.0f);
   float2 v[4][4];  // channels 32 j + 8 l + 2 n, + 1 in v[j][n]
+  __syncwarp();    // the products are the whole warp's, the loads and stores around them each lane's own
 #pragma unroll
   for (int n = 0; n < 4; ++n) {
 #pragma unroll
@@ -177,7 +178,6 @@ __device__ __forceinline__ void read_cell(const uint2 (&w)[4], const uint32_t (&
       v[j + 1][n] = __fadd2_rn(make_float2(__uint_as_float(d[2]), __uint_as_float(d[3])), bias);
     }
   }
-  if (!there) return;
   const float by1 = scale * fwht::kInvSqrt128;
   const float2 by = make_float2(by1, by1);
   uint32_t out[4][4];
@@ -193,9 +193,11 @@ __device__ __forceinline__ void read_cell(const uint2 (&w)[4], const uint32_t (&
       out[j][n] = any ? fwht::narrow_pair<F16>(x.x, x.y) : 0u;
     }
   }
+  if (there) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    *reinterpret_cast<uint4*>(dst + 32 * j) = make_uint4(out[j][0], out[j][1], out[j][2], out[j][3]);
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<uint4*>(dst + 32 * j) = make_uint4(out[j][0], out[j][1], out[j][2], out[j][3]);
+  }
 }
 
 template <bool F16>
