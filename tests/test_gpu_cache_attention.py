@@ -742,3 +742,18 @@ def test_values_of_zero_before_others(cr, hq, hkv):
             if j < 256:
                 s.scales[1][page] = 0.0
     s.check(s.run(), sequences=range(0, 160, 16))
+
+
+def test_tall_tiles_with_pages_missing_here_and_there(cr):
+    """Tiles of 128 keys in which some of the eight boxes of 16 keys have no page, others no key."""
+    rng = np.random.default_rng(3)
+    s = Setup(cr, [(2900, 1), (75, 1)], 80, 1, 16, seed=19)
+    see = [np.ones((1, n), bool) for n, _ in s.seqs]
+    good = s.pages.copy()
+    for b, (keys, _) in enumerate(s.seqs):
+        for column in np.flatnonzero(rng.random(-(-keys // 16)) < 0.4):
+            s.pages[b, column] = -1
+            see[b][0, column * 16:(column + 1) * 16] = False
+    O = s.run(status=1)
+    s.pages = good
+    s.check(O, see=see)

@@ -90,7 +90,9 @@ struct CwSmem {
 
 enum CwBar { kKFull, kKEmpty, kSFull, kSEmpty, kPFull, kODone, kVFull, kSc0, kSc1, kBars };
 
+// A barrier of whole warps: what stands before it may have been single lanes' work.
 __device__ __forceinline__ void cw_sync(int id, int threads) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
@@ -401,6 +403,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         }
 #pragma unroll 1
         for (int attempt = 0;; ++attempt) {
+          __syncwarp();  // a pass is the whole warp's; what led here differs by row
           if (masked) cw_pass<true>(tS, c, now, vis, sk, line, sw, &sum, &big);
           else cw_pass<false>(tS, c, now, vis, sk, line, sw, &sum, &big);
           const bool lost = !(big <= CW_MOST) || !(sum <= 0x1p110f) || (first && high > 0.0f && big < 1.0f);
@@ -474,6 +477,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             for (int k = 0; k < 4; ++k)
               dst[k * CA_WIDE_ROWS] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
           }
+          __syncwarp();
         }
         if (pipe == 0 && row < r.rows && alive) p.part_ml[slot * CA_WIDE_ROWS + row] = make_float2(top, total);
       } else {
@@ -740,6 +744,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     }
   }
   tc_fence_before();
+  __syncwarp();
   const int any_bad = __syncthreads_or(bad & CA_BAD), late = __syncthreads_or(bad & 4);  // a timeout is 5
   if (tid == 0) p.piece_status[blockIdx.x] = late ? CA_LATE : any_bad ? CA_BAD : 0;
   if (warp == 13) {
