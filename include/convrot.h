@@ -517,7 +517,7 @@ CONVROT_API convrot_status convrot_cache_read(const convrot_cache_args* args, co
  * convrot_attention_int8. Two kernels; how the work is cut follows from the
  * lengths, and the result does not depend on timing. A timed-out wait (the tile
  * of 128 rows waits on its own copies and products) sets the status word to
- * CONVROT_ERR_DEVICE_TIMEOUT.
+ * CONVROT_ERR_DEVICE_TIMEOUT, and every row it cost is NaN.
  */
 CONVROT_API size_t convrot_cache_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
 typedef struct {
@@ -538,6 +538,14 @@ typedef struct {
 } convrot_cache_attention_args;
 CONVROT_API convrot_status convrot_cache_attention(const convrot_cache_attention_args* args,
                                                    convrot_stream_t stream);
+/*
+ * The same with
+ *   status    one int, device, or NULL: what the status word of the workspace becomes is
+ *             ORed in. Never cleared, so that one word can stand for many calls.
+ *   wait_ns   longest that a wait may last, in nanoseconds; 0: two seconds.
+ */
+CONVROT_API convrot_status convrot_cache_attention_ex(const convrot_cache_attention_args* args, int* status,
+                                                      int64_t wait_ns, convrot_stream_t stream);
 
 /*
  * convrot_probe_i8_peak -- measurement aid for the GEMM's roofline (not part

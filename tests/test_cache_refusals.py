@@ -192,3 +192,22 @@ def test_native_binding_leaves_other_calls_to_python(L):
         assert fn(*[None] * n) is None and fn(*[0] * n) is None and fn() is None
     with pytest.raises(TypeError):
         b.bind(1)
+
+
+def test_attention_with_a_status_and_a_limit(L):
+    from w8a8_rotated_int8_token_b200 import _lib
+
+    args = _lib.CACHE_ATTENTION_ARGS.pack(*CELLS_OK, FAKE, FAKE, FAKE, FAKE, 0, 0, FAKE, 1 << 30, 0, 8, 0, 3, 3, 1024, 128,
+                                          1024, 128, 0.1, 0)  # no tokens: nothing is launched
+    assert L.convrot_cache_attention_ex(args, None, 0, None) == 0
+    assert L.convrot_cache_attention_ex(args, FAKE, 1000, None) == 0
+    assert L.convrot_cache_attention_ex(args, FAKE + 2, 0, None) == 1
+    assert L.convrot_cache_attention_ex(args, None, -1, None) == 1
+    assert L.convrot_cache_attention_ex(None, None, 0, None) == 1
+
+
+def test_binding_without_its_status_argument_is_left_to_python(L):
+    from w8a8_rotated_int8_token_b200 import _lib
+
+    b = _lib.binding()
+    assert b.attention(*[None] * 12) is None and b.attention(*[None] * 13) is None

@@ -757,3 +757,61 @@ def test_tall_tiles_with_pages_missing_here_and_there(cr):
     O = s.run(status=1)
     s.pages = good
     s.check(O, see=see)
+
+
+@pytest.mark.parametrize("native", [True, False])
+@pytest.mark.parametrize("hq", [4, 160])
+def test_a_cache_learns_what_its_attention_met(cr, monkeypatch, native, hq):
+    """Without a workspace of the caller's the status is not lost: it is kept in the cache's own word."""
+    import torch
+
+    if not native:
+        monkeypatch.setattr(cr._T, "attention", lambda *a: None)
+    s = Setup(cr, [(40, 1), (20, 1)], hq, 2, 16, seed=20)
+    cache = cr.ConvRotCache(len(s.codes[0]), 2, 16)
+    for t, x in zip(cache.cells, s.cells()):
+        t.copy_(x)
+    pages, lengths, starts = s.args()
+    O = cache.attention(s.Q, pages, lengths, starts)
+    cache.check()
+    s.check(O)
+    for bad in (dict(lengths=torch.tensor([40, -1], dtype=torch.int32, device="cuda")),
+                dict(pages=torch.full_like(pages, -1)), dict(starts=starts + 1)):
+        cache.attention(s.Q, **({"pages": pages, "lengths": lengths, "starts": starts} | bad))
+        cache.attention(s.Q, pages, lengths, starts)  # a good call does not clear it
+        with pytest.raises(cr.ConvRotError) as e:
+            cache.check()
+        assert e.value.status == 1
+        cache.status.zero_()
+    own = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cr.convrot_cache_attention(s.Q, *cache.cells, pages, -lengths, starts, status=own)
+    assert own.item() == 1 and cache.status.item() == 0
+    with pytest.raises(TypeError):
+        cr.convrot_cache_attention(s.Q, *cache.cells, pages, lengths, starts, status=own.float())
+
+
+def test_a_wait_that_runs_out_makes_rows_nan_and_is_reported(cr):
+    """A limit of a nanosecond on the waits of the 128-row kernel, some of which take longer: each row is what it is
+    with time, or NaN, and the status says so; the next call is as if nothing had been."""
+    import torch
+
+    s = Setup(cr, [(20000, 1), (0, 1)] + [(300, 1)] * 198, 40, 1, 64, "bf16", seed=21)
+    cells, (pages, lengths, starts) = s.cells(), s.args()
+    need = cr.convrot_cache_attention_workspace_bytes(200, 200, 40, 1)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = cr.convrot_cache_attention(s.Q, *cells, pages, lengths, starts, ws=ws)
+    told = torch.zeros(1, dtype=torch.int32, device="cuda")
+    O = torch.full_like(want, 7.0)
+    args = cr._lib.CACHE_ATTENTION_ARGS.pack(
+        *(t.data_ptr() for t in cells), *cells[0].shape, s.Q.data_ptr(), O.data_ptr(), pages.data_ptr(),
+        lengths.data_ptr(), starts.data_ptr(), 0, ws.data_ptr(), need, 200, 40, 200, pages.shape[1], pages.stride(0),
+        *s.Q.stride()[:2], *O.stride()[:2], SCALE, 0)
+    stream = torch.cuda.current_stream().cuda_stream
+    assert cr.lib().convrot_cache_attention_ex(args, told.data_ptr(), 1, stream) == 0
+    assert cr.convrot_read_device_status(ws) == 5 and told.item() == 5
+    lost = O.isnan().all(-1)
+    assert bool(lost.any()) and not bool(lost[1].any())
+    assert torch.equal(O[~lost], want[~lost])
+    told.zero_()
+    assert cr.lib().convrot_cache_attention_ex(args, told.data_ptr(), 0, stream) == 0
+    assert cr.convrot_read_device_status(ws) == 0 and told.item() == 0 and torch.equal(O, want)

@@ -660,15 +660,17 @@ def convrot_cache_attention_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D
 
 
 def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts=None, tree=None,
-                            softmax_scale=None, O=None, ws=None, stream=None):
+                            softmax_scale=None, O=None, ws=None, stream=None, status=None):
     """Attention of the newest tokens over the rotated int8 cache: Q [T, Hq, 128] (bf16 or fp16,
     strided tokens and heads) -> O [T, Hq, 128]. pages [B, n] int32: the cache pages of each sequence;
     lengths [B] int32: its keys, the new tokens' included; starts [B + 1] int32: its tokens in Q
     (None: token b belongs to sequence b). Among its new tokens a query sees the earlier ones and
     itself, or, with tree [T] int64, those whose bit is set in its mask (at most 64 a sequence).
-    See include/convrot.h."""
+    status: an int32 [1] tensor into which the call's status is ORed (1: a length, page or start was
+    out of range; 5: a wait ran out and the rows it cost are NaN), or None. See include/convrot.h."""
     if stream is None:
-        done = _T.attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree, softmax_scale, O, ws)
+        done = _T.attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree, softmax_scale, O, ws,
+                            status)
         if done is not None:
             return done
     code, index, shape, qs = _head_vectors(Q, "Q")
@@ -677,7 +679,7 @@ def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, length
         if where is not None:
             with where:
                 return convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree,
-                                               softmax_scale, O, ws)
+                                               softmax_scale, O, ws, status=status)
     T, Hq, D = shape
     cells = _cells(index, k_codes, v_codes, k_scale, v_scale)
     Hkv = cells[5]
@@ -711,10 +713,11 @@ def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, length
         if ws.get_device() != index or not ws.is_contiguous():
             raise ValueError("ws must be contiguous on the device of the other tensors")
         room = ws.numel() * ws.element_size()
+    status_ptr = 0 if status is None else _beside(status, "status", index, _T.int32, (1,))
     args = _lib.CACHE_ATTENTION_ARGS.pack(
         *cells, Q.data_ptr(), O.data_ptr(), pages.data_ptr(), lengths_ptr, starts_ptr, tree_ptr, ws.data_ptr(), room,
         T, Hq, B, pshape[1], ps[0], qs[0], qs[1], ot, oh, softmax_scale, code)
-    status = (_lib._lib or lib()).convrot_cache_attention(args, _T.stream(index))
+    status = (_lib._lib or lib()).convrot_cache_attention_ex(args, status_ptr, 0, _T.stream(index))
     if status != 0:
         raise ConvRotError(status, "convrot_cache_attention")
     return O
@@ -725,7 +728,8 @@ class ConvRotCache:
 
     ``cache.append(K, V, slots)``, ``cache.read(slots)`` and ``cache.attention(Q, pages, lengths)`` are
     the entry points of the same names on its tensors; ``cache.slots(pages, sequence, position)`` finds
-    the slots of tokens. ``check()`` synchronises and raises if a slot was past the cache.
+    the slots of tokens. ``check()`` synchronises and raises if a slot was past the cache, or an attention
+    met a length, page or start out of range or a wait that ran out (``status.zero_()`` forgets it).
     """
 
     def __init__(self, num_pages: int, heads: int, page_size: int = 64, device="cuda"):
@@ -764,7 +768,8 @@ class ConvRotCache:
         return convrot_cache_read(slots, *self.cells, dtype=dtype, K=K, V=V, status=self.status, stream=stream)
 
     def attention(self, Q, pages, lengths, starts=None, tree=None, softmax_scale=None, O=None, ws=None, stream=None):
-        return convrot_cache_attention(Q, *self.cells, pages, lengths, starts, tree, softmax_scale, O, ws, stream)
+        return convrot_cache_attention(Q, *self.cells, pages, lengths, starts, tree, softmax_scale, O, ws, stream,
+                                       self.status)
 
     def check(self):
         if int(self.status.item()) != 0:

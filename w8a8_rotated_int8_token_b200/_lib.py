@@ -63,6 +63,7 @@ SIGNATURES = {
     "convrot_cache_read": (_int, [_args, _c_void_p]),
     "convrot_cache_attention_workspace_bytes": (_size, [_i64, _i64, _i64, _i64, _i64]),
     "convrot_cache_attention": (_int, [_args, _c_void_p]),
+    "convrot_cache_attention_ex": (_int, [_args, _c_void_p, _i64, _c_void_p]),
     "convrot_probe_i8_peak_ctas": (_int, []),
     "convrot_probe_ex2_peak": (_int, [_i64, _c_void_p, _size, _c_void_p]),
     "convrot_probe_ex2_per_iter": (_i64, []),
@@ -103,6 +104,6 @@ def binding():
     if _binding.torch_version != str(torch.__version__):
         return None
     _binding.bind(*(ctypes.cast(fn, _c_void_p).value for fn in (
-        lib.convrot_rope, lib.convrot_cache_append, lib.convrot_cache_read, lib.convrot_cache_attention,
+        lib.convrot_rope, lib.convrot_cache_append, lib.convrot_cache_read, lib.convrot_cache_attention_ex,
         lib.convrot_cache_attention_workspace_bytes)))
     return _binding

@@ -27,7 +27,7 @@ using Status = convrot_status;
 Status (*rope_fn)(const convrot_rope_args*, convrot_stream_t) = nullptr;
 Status (*append_fn)(const convrot_cache_args*, convrot_stream_t) = nullptr;
 Status (*read_fn)(const convrot_cache_args*, convrot_stream_t) = nullptr;
-Status (*attention_fn)(const convrot_cache_attention_args*, convrot_stream_t) = nullptr;
+Status (*attention_fn)(const convrot_cache_attention_args*, int*, int64_t, convrot_stream_t) = nullptr;
 size_t (*attention_bytes_fn)(int64_t, int64_t, int64_t, int64_t, int64_t) = nullptr;
 
 constexpr float kScale = 0.08838834764831845f;  // 1 / sqrt(128)
@@ -94,12 +94,12 @@ bool status_word(PyObject* o, int device, int** to) {
   return true;
 }
 
-template <class Args>
-bool call(Status (*fn)(const Args*, convrot_stream_t), const Args& args, int device) {
+template <class Args, class... More, class... Same>
+bool call(Status (*fn)(const Args*, More...), const Args& args, int device, Same... more) {
   if (fn == nullptr) return false;
   const convrot_stream_t s = stream_of(device);
   Status st;
-  Py_BEGIN_ALLOW_THREADS st = fn(&args, s);
+  Py_BEGIN_ALLOW_THREADS st = fn(&args, more..., s);
   Py_END_ALLOW_THREADS return st == CONVROT_OK;
 }
 
@@ -228,16 +228,17 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree, softmax_scale, O, ws); the last
-// five may be None
+// attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree, softmax_scale, O, ws, status); the
+// last six may be None
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  if (n != 12) Py_RETURN_NONE;
+  if (n != 13) Py_RETURN_NONE;
   const at::Tensor *q = tensor(a[0]), *pages = tensor(a[5]), *lengths = tensor(a[6]);
   const int device = device_of(q);
   if (!here(device) || pages == nullptr || lengths == nullptr) Py_RETURN_NONE;
   const int code = code_of(q->scalar_type());
   convrot_cache_attention_args r{};
+  int* status = nullptr;
   if (code < 0 || !heads(q, device, 3, q->scalar_type()) || q->size(2) != 128 || !cells(a + 1, device, &r.cells))
     Py_RETURN_NONE;
   r.T = q->size(0), r.Hq = q->size(1), r.B = lengths->numel();
@@ -257,6 +258,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!plain(tree, device, at::kLong, {r.T})) Py_RETURN_NONE;
     r.tree = static_cast<const int64_t*>(tree->data_ptr());
   }
+  if (!status_word(a[12], device, &status)) Py_RETURN_NONE;
   r.softmax_scale = kScale;
   if (a[9] != Py_None) {
     const double scale = PyFloat_AsDouble(a[9]);
@@ -290,14 +292,14 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r.table_pages = pages->size(1), r.table_stride = pages->stride(0);
   r.q_token = q->stride(0), r.q_head = q->stride(1), r.o_token = o->stride(0), r.o_head = o->stride(1);
   r.dtype = code;
-  if (!call(attention_fn, r, device)) Py_RETURN_NONE;
+  if (!call(attention_fn, r, device, status, int64_t{0})) Py_RETURN_NONE;
   if (a[10] == Py_None) return THPVariable_Wrap(std::move(made));
   Py_INCREF(a[10]);
   return a[10];
   END_HANDLE_TH_ERRORS
 }
 
-// bind(rope, append, read, attention, attention_workspace_bytes): the addresses of the library's entry points
+// bind(rope, append, read, attention_ex, attention_workspace_bytes): the addresses of the library's entry points
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 5) {
     PyErr_SetString(PyExc_TypeError, "bind takes five addresses");

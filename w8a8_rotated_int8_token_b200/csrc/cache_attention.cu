@@ -595,7 +595,11 @@ __device__ __forceinline__ void join_status(const CaParams& p) {
     int st = 0;
     for (int i = threadIdx.x; i < p.workers; i += 32 * kJoinWarps) st |= p.piece_status[i];
     const int any_bad = __syncthreads_or(st & CA_BAD), late = __syncthreads_or(st & 4);  // a timeout is 5
-    if (threadIdx.x == 0) *p.status = late ? CA_LATE : any_bad ? CA_BAD : 0;
+    if (threadIdx.x == 0) {
+      const int all = late ? CA_LATE : any_bad ? CA_BAD : 0;
+      *p.status = all;
+      if (all != 0 && p.told != nullptr) atomicOr(p.told, all);
+    }
   }
 }
 
@@ -820,8 +824,14 @@ size_t convrot_cache_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq,
 }
 
 convrot_status convrot_cache_attention(const convrot_cache_attention_args* args, convrot_stream_t stream) {
+  return convrot_cache_attention_ex(args, nullptr, 0, stream);
+}
+
+convrot_status convrot_cache_attention_ex(const convrot_cache_attention_args* args, int* status, int64_t wait_ns,
+                                          convrot_stream_t stream) {
   using namespace convrot;
-  if (args == nullptr) return CONVROT_ERR_INVALID_ARG;
+  if (args == nullptr || wait_ns < 0 || reinterpret_cast<uintptr_t>(status) % alignof(int) != 0)
+    return CONVROT_ERR_INVALID_ARG;
   const convrot_cache_attention_args& a = *args;
   const convrot_cells& c = a.cells;
   if (a.dtype != CONVROT_DTYPE_BF16 && a.dtype != CONVROT_DTYPE_F16) return CONVROT_ERR_UNSUPPORTED;
@@ -872,6 +882,9 @@ convrot_status convrot_cache_attention(const convrot_cache_attention_args* args,
   p.num_pages = static_cast<int>(c.num_pages);
   while ((int64_t{1} << p.page_shift) < c.page_size) ++p.page_shift;
   p.c_scale = a.softmax_scale * 1.4426950408889634f;
+  p.told = status;
+  p.wait_ns = wait_ns > 0 ? static_cast<uint64_t>(wait_ns) : CA_WAIT_NS;
+  p.wait_step = p.wait_ns < 2000 ? static_cast<uint32_t>(p.wait_ns) : 2000;
   const cudaError_t e = ca_run(p, ca_rows(a.T, a.B, p.G), a.dtype == CONVROT_DTYPE_F16, c.num_pages * c.H * c.page_size,
                                static_cast<uint8_t*>(a.ws), reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CONVROT_OK : CONVROT_ERR_CUDA;

@@ -14,6 +14,7 @@ namespace convrot {
 constexpr int CA_D = 128;
 constexpr int CA_BAD = CONVROT_ERR_INVALID_ARG;
 constexpr int CA_LATE = CONVROT_ERR_DEVICE_TIMEOUT;
+constexpr uint64_t CA_WAIT_NS = 2000000000ull;  // limit of a wait, unless the caller sets one
 constexpr int CA_MAX_WORKERS = 640;  // pieces the workspace has room for
 // The maximum of a row that has seen no key: below every logit, and finite, so that exponents of
 // differences need no special case.
@@ -49,6 +50,9 @@ struct CaParams {
   float* part;                // [2 workers][rows][128]
   float2* part_ml;            // [2 workers][rows] maximum, sum
   int* status;                // the call's status word, written by the join
+  int* told;                  // null, or a word that it is ORed into as well
+  uint64_t wait_ns;           // limit of a wait
+  uint32_t wait_step;         // nanoseconds between two looks at it
   int workers;
 };
 

@@ -37,7 +37,9 @@
 // What bounds a tile now (2 us per SM): the latencies of a pass, 1024 cycles of
 // which are the exponentials, and between passes the turn of the products, which need the
 // logits read before the next are made.
-// Every wait is bounded.
+// Every wait is bounded. Once one has run out, the CTA's roles leave the walk together at
+// the end of the run, with the barriers' phases still agreed, and the softmax warps go on alone: the rows
+// of that run and of the piece's later ones become NaN, also where the join sums them.
 
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -60,7 +62,6 @@ namespace {
 constexpr int CW_KT = 128;           // keys of a tile
 constexpr int CW_THREADS = 448;
 constexpr int CW_HALF = 128 * 128;   // 128 rows of 128 bytes
-constexpr uint64_t CW_TIMEOUT_NS = 2000000000ull;
 // a run costs about as much as three tiles beside its tiles
 using CwGrain = CaGrain<CA_WIDE_ROWS, CW_KT, 3, 2>;
 constexpr uint32_t CW_IDESC_S = idesc_i8(128, CW_KT);
@@ -94,6 +95,21 @@ enum CwBar { kKFull, kKEmpty, kSFull, kSEmpty, kPFull, kODone, kVFull, kSc0, kSc
 __device__ __forceinline__ void cw_sync(int id, int threads) {
   __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The same barrier, and whether any of its threads brought a true.
+__device__ __forceinline__ bool cw_vote(int id, int threads, bool mine) {
+  uint32_t any;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(mine ? 1u : 0u), "r"(id), "r"(threads)
+      : "memory");
+  return any != 0;
 }
 
 // A word of the keys below `n` among keys 32 w .. 32 w + 31 of a tile.
@@ -267,8 +283,8 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     const uint32_t parity = static_cast<uint32_t>(use & 1);
     if (mbar_try_wait(b, parity)) return true;
     const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait_suspend(b, parity, 2000)) {
-      if (*abort || global_timer_ns() - t0 > CW_TIMEOUT_NS) {
+    while (!mbar_try_wait_suspend(b, parity, p.wait_step)) {
+      if (*abort || global_timer_ns() - t0 > p.wait_ns) {
         *abort = 1;
         bad |= CA_LATE;
         return false;
@@ -277,7 +293,8 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     return true;
   };
   // Tiles that a pipeline has taken in earlier runs: the parity of its barriers. Every role counts alike, and
-  // meets the others twice a run (barrier 0): the queries are in place; the sums have been read.
+  // meets the others twice a run (barrier 0): the queries are in place; the sums have been read, and whether a
+  // wait has run out is known to all.
   int used[2] = {0, 0};
   CaRun r;
   CaCut cut{};
@@ -292,16 +309,9 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
     const int sw = row & 7;
     float* row_c = reinterpret_cast<float*>(smem + L::kOffRow);
     float2* stat = reinterpret_cast<float2*>(smem + L::kOffStat);
-    while (walk.next(p, &r, bad)) {
+    // A run up to its sums, in stat and TMEM; false once a wait has run out in the CTA.
+    auto sums = [&]() {
       const int keys = walk.s.keys, context = keys - walk.s.news;
-      if (keys == 0) {  // nothing to see: zeros
-        for (int i = tid; i < r.rows * (CA_D / 8); i += 256) {
-          const int of = r.row0 + i / (CA_D / 8), token = of / p.G;
-          *reinterpret_cast<uint4*>(p.o + (walk.s.first + token) * p.ot + (r.head * p.G + (of - token * p.G)) * p.oh +
-                                    8 * (i % (CA_D / 8))) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        continue;
-      }
       if (p.tree != nullptr && walk.s.news > 64) bad |= CA_BAD;
       // the tile's queries, rotated and quantised: four lanes a row, 16 rows a warp
       {
@@ -442,8 +452,21 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       if (ok && mine > 0) ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kODone), used[pipe] + mine - 1));
       stat[pipe * 128 + row] = make_float2(ref, l);
       tc_fence_before();
-      cw_sync(1, 256);
+      const bool lost = cw_vote(1, 256, !ok);
       tc_fence_after();
+      return !lost;
+    };
+    bool dead = false;
+    while (walk.next(p, &r, bad)) {
+      if (walk.s.keys == 0) {  // nothing to see: zeros
+        for (int i = tid; i < r.rows * (CA_D / 8); i += 256) {
+          const int of = r.row0 + i / (CA_D / 8), token = of / p.G;
+          *reinterpret_cast<uint4*>(p.o + (walk.s.first + token) * p.ot + (r.head * p.G + (of - token * p.G)) * p.oh +
+                                    8 * (i % (CA_D / 8))) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        continue;
+      }
+      const bool there = !dead && sums();
       // ---- the pipelines joined; channels 0 .. 63 here, 64 .. 127 in the other pipeline's warps
       const bool second = r.t1 - r.t0 > 1;
       const float2 s0 = stat[row], s1 = second ? stat[128 + row] : make_float2(CA_NONE, 0.0f);
@@ -452,8 +475,20 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       const float total = s0.y * f0 + s1.y * f1;
       const bool whole = r.t0 == 0 && r.t1 == walk.s.tiles;
       const uint32_t tO0 = tmem + lanes + 256, tO1 = tO0 + 128;
-      const bool alive = *abort == 0;  // else there may be no sums
-      if (!whole) {
+      if (!there) {
+        if (pipe == 0 && row < r.rows) {
+          if (whole) {
+            const int of = r.row0 + row, i = of / p.G;
+            uint16_t* dst = p.o + (walk.s.first + i) * p.ot + (r.head * p.G + (of - i * p.G)) * p.oh;
+            for (int k = 0; k < CA_D / 8; ++k)  // NaN in either type
+              *reinterpret_cast<uint4*>(dst + 8 * k) = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+          } else {
+            // a sum that is no number makes the row none, whatever its channels hold
+            p.part_ml[(2 * static_cast<int64_t>(blockIdx.x) + (r.t0 == 0 ? 1 : 0)) * CA_WIDE_ROWS + row] =
+                make_float2(0.0f, __uint_as_float(0x7FFFFFFFu));
+          }
+        }
+      } else if (!whole) {
         // this half's channels, unnormalised; rolled, for the instruction cache
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (r.t0 == 0 ? 1 : 0);
         // four channels of all rows after one another, so that a warp's stores are contiguous
@@ -472,14 +507,14 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) v[i] = fmaf(__uint_as_float(b[i]), f1, v[i]);
           }
-          if (row < r.rows && alive) {
+          if (row < r.rows) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               dst[k * CA_WIDE_ROWS] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
           }
           __syncwarp();
         }
-        if (pipe == 0 && row < r.rows && alive) p.part_ml[slot * CA_WIDE_ROWS + row] = make_float2(top, total);
+        if (pipe == 0 && row < r.rows) p.part_ml[slot * CA_WIDE_ROWS + row] = make_float2(top, total);
       } else {
         // the last butterfly stage, between channels 64 apart, comes first
         float v[64];
@@ -513,7 +548,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         fwht::reg_stage<64, 8>(v);
         fwht::reg_stage<64, 16>(v);
         fwht::reg_stage<64, 32>(v);
-        if (row < r.rows && alive) {
+        if (row < r.rows) {
           const int of = r.row0 + row, i = of / p.G;
           uint16_t* dst = p.o + (walk.s.first + i) * p.ot + (r.head * p.G + (of - i * p.G)) * p.oh + 64 * pipe;
 #pragma unroll
@@ -531,10 +566,11 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         cut.head = r.head;
         cut.token0 = walk.s.first;
       }
+      if (dead) continue;
       used[0] += (r.t1 - r.t0 + 1) / 2;
       used[1] += (r.t1 - r.t0) / 2;
       tc_fence_before();
-      cw_sync(0, CW_THREADS);
+      dead = cw_vote(0, CW_THREADS, !there);
     }
     if (tid == 0) p.cuts[blockIdx.x] = cut;
   } else if (warp < 12) {
@@ -642,7 +678,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       }
       used[0] += (r.t1 - r.t0 + 1) / 2;
       used[1] += (r.t1 - r.t0) / 2;
-      cw_sync(0, CW_THREADS);
+      if (cw_vote(0, CW_THREADS, (bad & 4) != 0)) break;  // a timeout is 5
     }
   } else {
     if (warp == 12) {
@@ -678,14 +714,13 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         if (r.t1 - r.t0 <= 2) cw_sync(0, CW_THREADS);
         used[0] += (r.t1 - r.t0 + 1) / 2;
         used[1] += (r.t1 - r.t0) / 2;
-        __syncwarp();
-        cw_sync(0, CW_THREADS);
+        if (cw_vote(0, CW_THREADS, (bad & 4) != 0)) break;
       }
       // every copy has landed before the shared memory goes away
       if (lane == 0)
         for (int pipe = 0; pipe < 2; ++pipe)
           if (issued[pipe] > 0)
-            mbar_wait_bounded(bar(pipe, kKFull), static_cast<uint32_t>((issued[pipe] - 1) & 1), nullptr, CW_TIMEOUT_NS);
+            mbar_wait_bounded(bar(pipe, kKFull), static_cast<uint32_t>((issued[pipe] - 1) & 1), nullptr, CA_WAIT_NS);
     } else {
       // -------------------------------------------------------------- products
       const uint32_t qa = smem_addr(smem + L::kOffQ);
@@ -732,13 +767,12 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         }
         used[0] += (r.t1 - r.t0 + 1) / 2;
         used[1] += (r.t1 - r.t0) / 2;
-        __syncwarp();
-        cw_sync(0, CW_THREADS);
+        if (cw_vote(0, CW_THREADS, (bad & 4) != 0)) break;
       }
       if (lane == 0) {
         // every product issued has finished before TMEM is released
         mma_commit(drain);
-        mbar_wait_bounded(drain, 0u, nullptr, CW_TIMEOUT_NS);
+        mbar_wait_bounded(drain, 0u, nullptr, CA_WAIT_NS);
       }
       __syncwarp();
     }
