@@ -107,6 +107,10 @@ typedef enum {
 /* Version of this ABI; bumped when a signature or a layout changes. */
 CONVROT_API int convrot_abi_version(void);
 
+/* The hash of this header that the library was compiled with, or "" if its build gave none: what passes the
+ * structs below by their layout can compare it with its own. */
+CONVROT_API const char* convrot_header(void);
+
 /* Static English description of a status code. Never NULL. */
 CONVROT_API const char* convrot_status_string(int status);
 

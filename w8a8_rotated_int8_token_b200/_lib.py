@@ -27,6 +27,7 @@ CACHE_ATTENTION_ARGS = struct.Struct("@4P 4q 7P N 3q 2q 4q f i")
 # name -> (restype, argtypes), mirroring include/convrot.h
 SIGNATURES = {
     "convrot_abi_version": (_int, []),
+    "convrot_header": (ctypes.c_char_p, []),
     "convrot_status_string": (ctypes.c_char_p, [_int]),
     "convrot_prepare_weight_workspace_bytes": (_size, []),
     "convrot_prepare_weight": (_int, [_c_void_p, _i64, _i64, _int, _c_void_p, _c_void_p, _c_void_p, _size,
@@ -92,8 +93,8 @@ def load() -> ctypes.CDLL:
 
 def binding():
     """The native form of the binding's rope and cache calls (csrc/binding.cpp), bound to the loaded
-    library, or None if it was built for another torch or not at all: the Python form of the same
-    checks serves then."""
+    library, or None if it was built for another torch, with another convrot.h than the library, or not
+    at all: the Python form of the same checks serves then."""
     lib = load()
     try:
         import torch
@@ -101,7 +102,9 @@ def binding():
         from . import _binding
     except ImportError:
         return None
-    if _binding.torch_version != str(torch.__version__):
+    header = lib.convrot_header().decode()
+    if (getattr(_binding, "torch_version", None) != str(torch.__version__) or not header
+            or getattr(_binding, "header", None) != header):
         return None
     _binding.bind(*(ctypes.cast(fn, _c_void_p).value for fn in (
         lib.convrot_rope, lib.convrot_cache_append, lib.convrot_cache_read, lib.convrot_cache_attention_ex,

@@ -5,21 +5,25 @@
 needed to build. The CUDA runtime is linked statically and its symbols are
 kept private, so the library does not clash with the runtime PyTorch loads.
 Beside it, g++ compiles ``csrc/binding.cpp`` against the installed PyTorch into
-``_binding.so``, the Python binding's short way to the calls of a decoding step.
+the extension ``_binding``, the Python binding's short way to the calls of a
+decoding step. Both carry the hash of ``convrot.h``, whose structs they share.
 """
 
 from __future__ import annotations
 
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
 LIB_PATH = os.path.join(PKG_DIR, "libconvrot.so")
-BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
+# with the tag of this Python's binary interface, so that no other one loads it
+BINDING_PATH = os.path.join(PKG_DIR, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 BINDING_SOURCE = os.path.join(PKG_DIR, "csrc", "binding.cpp")
 
 NVCC_FLAGS = [
@@ -38,6 +42,11 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found (set NVCC or install the CUDA toolkit)")
+
+
+def _header_flag() -> str:
+    with open(os.path.join(ROOT, "include", "convrot.h"), "rb") as f:
+        return f'-DCONVROT_HEADER="{hashlib.sha256(f.read()).hexdigest()[:16]}"'
 
 
 def sources() -> list[str]:
@@ -68,8 +77,6 @@ def _binding_up_to_date() -> bool:
 
 
 def _binding_command(out: str) -> list[str]:
-    import sysconfig
-
     import torch
 
     base = os.path.dirname(torch.__file__)
@@ -77,7 +84,8 @@ def _binding_command(out: str) -> list[str]:
     include = [os.path.join(ROOT, "include"), os.path.join(base, "include"), os.path.join(cuda, "include"),
                sysconfig.get_paths()["include"]]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
-            f'-DBUILT_FOR_TORCH="{torch.__version__}"', f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{d}" for d in include),
+            f'-DBUILT_FOR_TORCH="{torch.__version__}"', _header_flag(),
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{d}" for d in include),
             BINDING_SOURCE, "-o", out, f"-L{os.path.join(base, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
             "-ltorch_python"]
 
@@ -87,7 +95,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     jobs = []
     if force or not up_to_date():
         tmp = LIB_PATH + ".tmp"
-        jobs.append((LIB_PATH, [_nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, *sources()]))
+        jobs.append((LIB_PATH, [_nvcc(), *NVCC_FLAGS, _header_flag(), "-I", os.path.join(ROOT, "include"), "-o", tmp,
+                                *sources()]))
     if force or not _binding_up_to_date():
         jobs.append((BINDING_PATH, _binding_command(BINDING_PATH + ".tmp")))
     running = []

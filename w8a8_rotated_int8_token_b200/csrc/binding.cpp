@@ -334,6 +334,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 PyMODINIT_FUNC PyInit__binding(void) {
   PyObject* m = PyModule_Create(&module);
-  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", BUILT_FOR_TORCH) != 0) Py_CLEAR(m);
+  // what the module may be used with: this torch, and a library compiled from the same convrot.h
+  if (m != nullptr && (PyModule_AddStringConstant(m, "torch_version", BUILT_FOR_TORCH) != 0 ||
+                       PyModule_AddStringConstant(m, "header", CONVROT_HEADER) != 0))
+    Py_CLEAR(m);
   return m;
 }

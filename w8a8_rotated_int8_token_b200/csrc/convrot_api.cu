@@ -157,6 +157,11 @@ extern "C" {
 
 int convrot_abi_version(void) { return kAbiVersion; }
 
+#ifndef CONVROT_HEADER
+#define CONVROT_HEADER ""
+#endif
+const char* convrot_header(void) { return CONVROT_HEADER; }
+
 const char* convrot_status_string(int status) {
   switch (status) {
     case CONVROT_OK: return "ok";
