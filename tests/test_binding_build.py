@@ -50,3 +50,64 @@ def test_the_file_names_its_python():
 
     assert "cpython" in sysconfig.get_config_var("EXT_SUFFIX")
     assert build.BINDING_PATH.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+@pytest.fixture
+def tools(tmp_path, monkeypatch):
+    """build() into a folder of its own, with compilers that write what they are asked for, or fail."""
+    from w8a8_rotated_int8_token_b200 import build
+
+    monkeypatch.setattr(build, "LIB_PATH", str(tmp_path / "libconvrot.so"))
+    monkeypatch.setattr(build, "BINDING_PATH", str(tmp_path / "_binding.so"))
+
+    def compiler(name, variable, works):
+        path = tmp_path / name
+        path.write_text("#!/bin/sh\n" + ('while [ "$1" != -o ]; do shift; done; echo made > "$2"\n' if works else
+                                         "echo no such header >&2; exit 1\n"))
+        path.chmod(0o755)
+        monkeypatch.setenv(variable, str(path))
+
+    compiler("nvcc", "NVCC", True)
+    compiler("g++", "CXX", True)
+    return build, compiler
+
+
+def test_build_makes_both(tools, recwarn):
+    build, _ = tools
+    assert build.build() == build.LIB_PATH
+    assert os.path.exists(build.LIB_PATH) and os.path.exists(build.BINDING_PATH) and not recwarn.list
+
+
+def test_build_without_torch_makes_the_library(tools, monkeypatch):
+    import sys
+
+    build, _ = tools
+    monkeypatch.setitem(sys.modules, "torch", None)
+    assert build.build() == build.LIB_PATH
+    assert os.path.exists(build.LIB_PATH) and not os.path.exists(build.BINDING_PATH)
+
+
+def test_a_binding_that_does_not_compile_is_a_warning(tools):
+    build, compiler = tools
+    with open(build.BINDING_PATH, "w") as f:
+        f.write("of older sources")
+    compiler("g++", "CXX", False)
+    with pytest.warns(UserWarning, match="Python form of the binding(.|\n)*no such header"):
+        assert build.build(force=True) == build.LIB_PATH
+    assert os.path.exists(build.LIB_PATH) and not os.path.exists(build.BINDING_PATH)
+
+
+def test_a_compiler_that_is_not_there_is_a_warning_for_the_binding(tools, monkeypatch):
+    build, _ = tools
+    monkeypatch.setenv("CXX", "/nowhere/g++")
+    with pytest.warns(UserWarning, match="Python form of the binding"):
+        assert build.build() == build.LIB_PATH
+    assert os.path.exists(build.LIB_PATH) and not os.path.exists(build.BINDING_PATH)
+
+
+def test_a_library_that_does_not_compile_is_an_error(tools):
+    build, compiler = tools
+    compiler("nvcc", "NVCC", False)
+    with pytest.raises(RuntimeError, match="no such header"):
+        build.build()
+    assert not os.path.exists(build.LIB_PATH)

@@ -7,6 +7,8 @@ kept private, so the library does not clash with the runtime PyTorch loads.
 Beside it, g++ compiles ``csrc/binding.cpp`` against the installed PyTorch into
 the extension ``_binding``, the Python binding's short way to the calls of a
 decoding step. Both carry the hash of ``convrot.h``, whose structs they share.
+The library needs no PyTorch to build; without one, or where g++ fails, it is
+built alone, and the Python form of the binding serves.
 """
 
 from __future__ import annotations
@@ -18,6 +20,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -69,6 +72,14 @@ def up_to_date() -> bool:
     return _newer(LIB_PATH, _deps())
 
 
+def _torch_works() -> bool:
+    try:
+        import torch  # noqa: F401
+    except (ImportError, OSError):  # none, or one whose libraries do not load
+        return False
+    return True
+
+
 def _binding_up_to_date() -> bool:
     import torch
 
@@ -91,23 +102,35 @@ def _binding_command(out: str) -> list[str]:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the library and the binding if a source is newer than them; return the library's path."""
+    """Compile the library and the binding if a source is newer than them; return the library's path.
+    Raises if the library cannot be built, warns if the binding cannot."""
     jobs = []
     if force or not up_to_date():
         tmp = LIB_PATH + ".tmp"
         jobs.append((LIB_PATH, [_nvcc(), *NVCC_FLAGS, _header_flag(), "-I", os.path.join(ROOT, "include"), "-o", tmp,
                                 *sources()]))
-    if force or not _binding_up_to_date():
+    if _torch_works() and (force or not _binding_up_to_date()):
         jobs.append((BINDING_PATH, _binding_command(BINDING_PATH + ".tmp")))
     running = []
     for path, cmd in jobs:
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        running.append((path, cmd[0], subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)))
-    ended = [(path, tool, *p.communicate(), p.returncode) for path, tool, p in running]
+        try:
+            p = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+        except OSError as e:  # no such compiler
+            p = subprocess.CompletedProcess(cmd, 127, "", str(e))
+        running.append((path, cmd[0], p))
+    ended = [(path, tool, *(p.communicate() if isinstance(p, subprocess.Popen) else (p.stdout, p.stderr)), p.returncode)
+             for path, tool, p in running]
     for path, tool, out, err, code in ended:
         if code != 0:
-            raise RuntimeError(f"{os.path.basename(tool)} failed ({code}):\n{out}\n{err}")
+            failed = f"{os.path.basename(tool)} failed ({code}):\n{out}\n{err}"
+            if path == LIB_PATH:
+                raise RuntimeError(failed)
+            warnings.warn(f"calls go through the Python form of the binding; {failed}")
+            if os.path.exists(path):
+                os.remove(path)  # of older sources
+            continue
         if verbose and (out or err):
             print(out + err, file=sys.stderr)
         os.replace(path + ".tmp", path)
