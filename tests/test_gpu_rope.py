@@ -212,3 +212,30 @@ def test_captured_and_on_another_stream(cr):
     torch.cuda.synchronize()
     assert torch.equal(out, Y.flip(2))
     del graph
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_pairs_of_no_axis_are_copied_whatever_they_hold(cr, kind, interleaved, shift):
+    """To the bit: an infinity beside a number, NaN, and zeros of either sign; the other pairs are turned as ever.
+    Off 16 bytes (shift) the scalar kernel does the same."""
+    import torch
+
+    X, pos = _inputs(1, 20, 9, 136, kind, 10)
+    X = X[..., 4 * shift:][..., :128]
+    freq, axis = cr.convrot_rope_tables([16, 24, 24])
+    want = cr.convrot_rope(X, pos, freq, axis, interleaved)
+    off = torch.tensor([0, 3, 17, 40, 41, 63], device="cuda")
+    axis[off] = torch.tensor([-1, 3, -2**31, 2**31 - 1, 4, -1], dtype=torch.int32, device="cuda")
+    first = 2 * off if interleaved else off
+    second = 2 * off + 1 if interleaved else off + 64
+    odd = torch.tensor([float("inf"), -0.0, float("nan"), 0.0, -float("inf"), 1.0], dtype=X.dtype, device="cuda")
+    X[..., first] = odd
+    X[..., second] = odd.flip(0) * -1.0
+    Y = cr.convrot_rope(X, pos, freq, axis, interleaved)
+    both = torch.cat([first, second])
+    assert torch.equal(Y[..., both].view(torch.int16), X[..., both].view(torch.int16))
+    rest = torch.ones(128, dtype=torch.bool, device="cuda")
+    rest[both] = False
+    assert torch.equal(Y[..., rest], want[..., rest])
