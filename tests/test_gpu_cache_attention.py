@@ -815,3 +815,25 @@ def test_a_wait_that_runs_out_makes_rows_nan_and_is_reported(cr):
     told.zero_()
     assert cr.lib().convrot_cache_attention_ex(args, told.data_ptr(), 0, stream) == 0
     assert cr.convrot_read_device_status(ws) == 0 and told.item() == 0 and torch.equal(O, want)
+
+
+@pytest.mark.parametrize("hq", [4, 80])
+def test_logits_of_any_size(cr, hq):
+    """Equal keys, so that every key weighs the same however far below (or above) zero its logit lies."""
+    keys = [1, 70, 300]
+    s = Setup(cr, [(n, 1) for n in keys], hq, 1, 16, seed=23)
+    for b, n in enumerate(keys):
+        s.codes[0][s.pages[b, :-(-n // 16)]] = s.codes[0][s.pages[b, 0], :, :1]
+        s.scales[0][s.pages[b, :-(-n // 16)]] = np.float32(1e30)
+    o = s.run().double().cpu().numpy()
+    for b, n in enumerate(keys):
+        (kc, ks), (vc, vs) = s.dense(b, 0), s.dense(b, 1)
+        qc, _ = oracle.quantize_heads(s.q[b], 128)
+        sums = qc.astype(np.int64) @ kc[0, 0].astype(np.int64)
+        assert (sums < 0).any() and (sums > 0).any() and not (sums == 0).any()
+        held = oracle.cache_value(vc[0], vs[0])
+        # a weight is 1 / n to fp16's half step, times the value's size; the rest as in the header
+        size = (vs[0][:, None].astype(np.float64) * np.abs(vc[0].astype(np.float64))).sum(0) / n
+        slack = (2.0**-11 + (n / 16 + 64) * 2.0**-22) * np.linalg.norm(size) * (1 + OUT_REL["bf16"])
+        want = held.mean(0)
+        assert np.all(np.abs(o[b] - want) <= OUT_REL["bf16"] * np.abs(want) + slack + OUT_ABS["bf16"])

@@ -16,9 +16,9 @@ constexpr int CA_BAD = CONVROT_ERR_INVALID_ARG;
 constexpr int CA_LATE = CONVROT_ERR_DEVICE_TIMEOUT;
 constexpr uint64_t CA_WAIT_NS = 2000000000ull;  // limit of a wait, unless the caller sets one
 constexpr int CA_MAX_WORKERS = 640;  // pieces the workspace has room for
-// The maximum of a row that has seen no key: below every logit, and finite, so that exponents of
+// The maximum of a row that has seen no key: below every other logit, and finite, so that exponents of
 // differences need no special case.
-constexpr float CA_NONE = -1e30f;
+constexpr float CA_NONE = -3.402823466e38f;
 
 // What a piece leaves for the join: its last item, if that goes on in the next pieces.
 struct CaCut {

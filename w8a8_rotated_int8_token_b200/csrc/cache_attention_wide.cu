@@ -70,6 +70,7 @@ constexpr uint32_t CW_IDESC_O = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | (
 constexpr float CW_MOST = 32768.0f;  // weights stay below 2^15
 constexpr float CW_GROWN = 16.0f;    // past it a row's reference goes up at the next tile
 constexpr float CW_SPAN = 100.0f;    // exponentials below 2^100
+constexpr float CW_FAR = 0x1p24f;    // logits from here on differ by whole numbers
 
 struct CwSmem {
   static constexpr int kOffQ = 0;
@@ -175,8 +176,9 @@ __device__ __forceinline__ float cw_exact(uint32_t tS, float c, const uint32_t (
 }
 
 // One pass over a tile's logits: the weights of the row in fp16 into its line of the operand, the sum of the
-// exponentials, and the largest weight.
-template <bool MASKED>
+// exponentials, and the largest weight. A logit's product is not rounded before the reference is taken off, which was;
+// past CW_FAR that difference could leave float32's exponents, and FAR rounds both alike (everywhere it took 3 % longer).
+template <bool MASKED, bool FAR>
 __device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, const uint32_t (&vis)[4], const float* sk,
                                         uint8_t* line, int sw, float* sum, float* most) {
   const float* sv = sk + 128;
@@ -207,7 +209,8 @@ __device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, const u
         for (int e = 0; e < 2; ++e) {
           const int k = i * 8 + 4 * q + 2 * e;
           const float2 u = cw_logits(a[k], a[k + 1], e == 0 ? make_float2(fk.x, fk.y) : make_float2(fk.z, fk.w));
-          const float2 t = __ffma2_rn(c2, u, nref);
+          const float2 t = FAR ? make_float2(__fadd_rn(__fmul_rn(c, u.x), -ref), __fadd_rn(__fmul_rn(c, u.y), -ref))
+                               : __ffma2_rn(c2, u, nref);
           float2 pr = make_float2(ex2_approx(t.x), ex2_approx(t.y));
           float2 x = __fmul2_rn(pr, e == 0 ? make_float2(fv.x, fv.y) : make_float2(fv.z, fv.w));
           if (MASKED) {
@@ -376,6 +379,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       const int clear = p.tree != nullptr ? context : context + 1;  // keys below it are seen by every row
       float ref = CA_NONE, l = 0.0f, largest = 0.0f;
       bool weighed = false;  // the row has had a weight
+      bool far = false;      // a row of the warp has a reference past CW_FAR
       bool ok = true;
       int use = used[pipe];
       for (int t = r.t0 + pipe; t < r.t1; t += 2, ++use) {
@@ -410,16 +414,19 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           // at this every weight of the tile is below 2^8, the largest usually little below
           const float tm = c * cw_top(tS, vis, sk);
           if (first) now = fmaxf(high > 0.0f ? tm + exponent_of(high) - 7.0f : tm, fmaxf(tm - CW_SPAN, least));
+          far = __any_sync(0xFFFFFFFFu, fabsf(now) > CW_FAR && now != CA_NONE);
         }
 #pragma unroll 1
         for (int attempt = 0;; ++attempt) {
           __syncwarp();  // a pass is the whole warp's; what led here differs by row
-          if (masked) cw_pass<true>(tS, c, now, vis, sk, line, sw, &sum, &big);
-          else cw_pass<false>(tS, c, now, vis, sk, line, sw, &sum, &big);
+          if (far) cw_pass<true, true>(tS, c, now, vis, sk, line, sw, &sum, &big);
+          else if (masked) cw_pass<true, false>(tS, c, now, vis, sk, line, sw, &sum, &big);
+          else cw_pass<false, false>(tS, c, now, vis, sk, line, sw, &sum, &big);
           const bool lost = !(big <= CW_MOST) || !(sum <= 0x1p110f) || (first && high > 0.0f && big < 1.0f);
           if (attempt == 1 || !__any_sync(0xFFFFFFFFu, lost)) break;
           const float at = cw_exact(tS, c, vis, sk);
           if (lost) now = fmaxf(at, least);
+          far = __any_sync(0xFFFFFFFFu, fabsf(now) > CW_FAR && now != CA_NONE);
         }
         weighed |= big > 0.0f;
         const float scale = now == ref ? 1.0f : ex2_approx(ref - now);
