@@ -837,3 +837,21 @@ def test_logits_of_any_size(cr, hq):
         slack = (2.0**-11 + (n / 16 + 64) * 2.0**-22) * np.linalg.norm(size) * (1 + OUT_REL["bf16"])
         want = held.mean(0)
         assert np.all(np.abs(o[b] - want) <= OUT_REL["bf16"] * np.abs(want) + slack + OUT_ABS["bf16"])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("hq", [4, 80])
+@pytest.mark.parametrize("odd", [float("nan"), float("inf"), -float("inf")])
+def test_a_query_that_is_no_number_gives_none(cr, kind, hq, odd):
+    """Its own row alone: no code stands for such a vector, so its weights are not those of any other query."""
+    import torch
+
+    s = Setup(cr, [(200, 1), (130, 1), (0, 1)] + [(1, 1)] * 9, hq, 1, 16, kind, seed=22)
+    want = s.run()
+    s.Q[2, 0, 0] = odd  # sees no key: zeros
+    lost = torch.zeros(12, hq, dtype=torch.bool, device="cuda")
+    for t, h, c in ((0, 1, 77), (1, hq - 1, 5), *((3 + i, i % 4, 14 * i) for i in range(9))):
+        s.Q[t, h, c] = odd
+        lost[t, h] = True
+    O = s.run()
+    assert bool(O[lost].isnan().all()) and torch.equal(O[~lost], want[~lost])

@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
       for (int e = 0; e < 4; ++e) c[e] = fmaf(v[e] * f.pre, f.ci, fwht::kRoundMagic);
       *reinterpret_cast<uint32_t*>(qs + row * CA_QPITCH + 4 * lane) = fwht::pack4(c[0], c[1], c[2], c[3]);
       if (lane == 0) {
-        row_c[row] = fwht::scale_of<128>(amax) * p.c_scale;
+        row_c[row] = ca_query_factor(p, amax);
         // keys below the limit are seen, and with a tree the drafted keys whose bit is set
         const bool tree = p.tree != nullptr;
         row_lim[row] = tree ? context : context + i + 1;

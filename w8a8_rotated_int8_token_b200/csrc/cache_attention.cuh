@@ -5,9 +5,11 @@
 
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 
 #include "convrot.h"
+#include "fwht_dev.cuh"
 
 namespace convrot {
 
@@ -55,6 +57,13 @@ struct CaParams {
   uint32_t wait_step;         // nanoseconds between two looks at it
   int workers;
 };
+
+// What turns a row's integer products into logits in base 2, from the largest magnitude of the rotated query. A channel
+// that is NaN or infinite leaves no other in its vector finite, and no code stands for such a vector: NaN, and so
+// are the logits of the keys that the row sees.
+__device__ __forceinline__ float ca_query_factor(const CaParams& p, float amax) {
+  return amax < INFINITY ? fwht::scale_of<128>(amax) * p.c_scale : __uint_as_float(0x7FFFFFFFu);
+}
 
 // How a kernel cuts the work: rows and keys of a tile, and in units of one tile what a run costs beside its
 // tiles (queries, first loads, the join) and the least that a piece takes.

@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
               fwht::fwht_first_pair<F16>(a[e], fwht::widen_pair<F16>(b[e]), v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
           }
           fwht::fwht128_quad(v, l4);
-          float amax = 0.0f;
+          float amax = fabsf(v[0].x);  // NaN where all are
 #pragma unroll
           for (int i = 0; i < 16; ++i) amax = fwht::fmax3f(amax, fabsf(v[i].x), fabsf(v[i].y));
           amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
@@ -362,13 +362,13 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             *reinterpret_cast<uint2*>(line_q + (((4 + 2 * j + (l4 >> 1)) ^ (at & 7)) << 4)) =
                 make_uint2(fwht::pack4(x[0].y, x[1].y, x[2].y, x[3].y), fwht::pack4(x[4].y, x[5].y, x[6].y, x[7].y));
           }
-          if (l4 == 0) row_c[at] = fwht::scale_of<128>(amax) * p.c_scale;
+          if (l4 == 0) row_c[at] = ca_query_factor(p, amax);
         }
       }
       fence_proxy_async_smem();
       cw_sync(0, CW_THREADS);
 
-      const float c = row_c[row];  // >= 0
+      const float c = row_c[row];  // >= 0 or NaN
       int lim = 0;                 // keys below it are seen, and with a tree the drafted keys whose bit is set
       unsigned long long bits = 0;
       {
