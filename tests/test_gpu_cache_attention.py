@@ -855,3 +855,19 @@ def test_a_query_that_is_no_number_gives_none(cr, kind, hq, odd):
         lost[t, h] = True
     O = s.run()
     assert bool(O[lost].isnan().all()) and torch.equal(O[~lost], want[~lost])
+
+
+@pytest.mark.parametrize("hq", [4, 10, 80])
+@pytest.mark.parametrize("value", [1e30, 1e33, 1e35])
+def test_seen_values_of_any_size_under_rising_logits(cr, hq, value):
+    """Value scales near the end of float32 while a row's maximum rises from key to key, by little and by much."""
+    for rise in (1.01, 1.3):
+        s = Setup(cr, [(500, 1), (33, 1)], hq, 1, 16, seed=24)
+        for b, (n, _) in enumerate(s.seqs):
+            for j in range(n):
+                s.scales[0][s.pages[b, j // 16], :, j % 16] = min(0.001 * rise ** j, 0.03)
+                s.scales[1][s.pages[b, j // 16], :, j % 16] *= value / 0.03
+        s.check(s.run())
+    s = Setup(cr, [(20000, 1)], hq, 1, 64, seed=25)  # cut among all CTAs, equal values
+    s.scales[1][np.isfinite(s.scales[1])] = value
+    s.check(s.run())

@@ -167,8 +167,13 @@ __device__ __forceinline__ float2 row_max(float2 v) {
 
 // 2^-e for the exponent e of a row's largest weight, within float32's normal range: it brings that weight to [1, 2).
 __device__ __forceinline__ float weight_factor(float weight) {
-  const uint32_t e = min(max(__float_as_uint(weight) >> 23, 27u), 227u);
+  const uint32_t e = min(max(__float_as_uint(weight) >> 23, 27u), 253u);
   return __uint_as_float((254u - e) << 23);
+}
+
+// The exponent of a sum of exponentials; 0 below 2, and at most 100, which no number of keys reaches.
+__device__ __forceinline__ float sum_exponent(float sum) {
+  return static_cast<float>(min(max(__float_as_uint(sum) >> 23, 127u), 227u) - 127u);
 }
 
 template <class Shape, bool F16>
@@ -371,11 +376,12 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
         uint32_t pw[NT][2], rest[NT][2];  // weights in fp16, and for fp16 outputs what that rounding left
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float2 top = make_float2(fmaxf(s[n][0].x, s[n][1].x), fmaxf(s[n][0].y, s[n][1].y));
-          if (__any_sync(0xFFFFFFFFu, top.x > mx[n].x + CA_RISE || top.y > mx[n].y + CA_RISE)) {
-            top = row_max(top);
+          const float2 top = make_float2(fmaxf(s[n][0].x, s[n][1].x), fmaxf(s[n][0].y, s[n][1].y));
+          // takes the references up to the largest logits
+          auto rise = [&]() {
+            const float2 most = row_max(top);
             // the sums stay as they are: their unit shrinks with the weights'
-            const float2 now = make_float2(fmaxf(mx[n].x, top.x), fmaxf(mx[n].y, top.y));
+            const float2 now = make_float2(fmaxf(mx[n].x, most.x), fmaxf(mx[n].y, most.y));
             const float2 by = make_float2(ex2_approx(mx[n].x - now.x), ex2_approx(mx[n].y - now.y));
             l[n] = __fmul2_rn(l[n], by);
             inv[n].x *= ex2_approx(now.x - mx[n].x);
@@ -390,19 +396,26 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
               if (fresh_x) acc[n][i][0] = acc[n][i][2] = 0.0f;
               if (fresh_y) acc[n][i][1] = acc[n][i][3] = 0.0f;
             }
-          }
-          // weights p s_v
-          const float2 away = make_float2(-mx[n].x, -mx[n].y);
-          float2 x[2];
+          };
+          if (__any_sync(0xFFFFFFFFu, top.x > mx[n].x + CA_RISE || top.y > mx[n].y + CA_RISE)) rise();
+          float2 pr[2], x[2], big;  // exponentials, weights p s_v and the largest of them
+          auto weigh = [&]() {
+            const float2 away = make_float2(-mx[n].x, -mx[n].y);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float2 y = __fadd2_rn(s[n][e], away);
-            const float2 pr = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-            l[n] = __fadd2_rn(l[n], pr);
-            x[e] = __fmul2_rn(pr, both(fv[e]));
-          }
-          float2 big = make_float2(fmaxf(x[0].x, x[1].x), fmaxf(x[0].y, x[1].y));
+            for (int e = 0; e < 2; ++e) {
+              const float2 y = __fadd2_rn(s[n][e], away);
+              pr[e] = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+              x[e] = __fmul2_rn(pr[e], both(fv[e]));
+            }
+            big = make_float2(fmaxf(x[0].x, x[1].x), fmaxf(x[0].y, x[1].y));
+          };
+          weigh();
           if (__any_sync(0xFFFFFFFFu, big.x * inv[n].x > CA_MOST || big.y * inv[n].y > CA_MOST)) {
+            // an exponential above 1 may take a weight out of float32, which is left by none up to 1
+            if (__any_sync(0xFFFFFFFFu, big.x == INFINITY || big.y == INFINITY)) {
+              rise();
+              weigh();
+            }
             big = row_max(big);
             const float2 to = make_float2(fminf(inv[n].x, weight_factor(big.x)), fminf(inv[n].y, weight_factor(big.y)));
             const float2 by = make_float2(to.x / inv[n].x, to.y / inv[n].y);
@@ -417,6 +430,7 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            l[n] = __fadd2_rn(l[n], pr[e]);
             const float2 w = __fmul2_rn(x[e], inv[n]);
             const __half2 h = __floats2half2_rn(w.x, w.y);
             pw[n][e] = transpose8(*reinterpret_cast<const uint32_t*>(&h));
@@ -476,7 +490,12 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
         l[n].x += __shfl_xor_sync(0xFFFFFFFFu, l[n].x, m);
         l[n].y += __shfl_xor_sync(0xFFFFFFFFu, l[n].y, m);
       }
-      const float2 by = make_float2(1.0f / inv[n].x, 1.0f / inv[n].y);
+      // the references taken up by the sums' exponents: the sums of values stay within twice the largest value
+      const float2 now = make_float2(mx[n].x + sum_exponent(l[n].x), mx[n].y + sum_exponent(l[n].y));
+      const float2 down = make_float2(ex2_approx(mx[n].x - now.x), ex2_approx(mx[n].y - now.y));
+      mx[n] = now;
+      l[n] = __fmul2_rn(l[n], down);
+      const float2 by = make_float2(down.x / inv[n].x, down.y / inv[n].y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         acc[n][i][0] *= by.x;
@@ -588,6 +607,8 @@ __global__ void __launch_bounds__(CA_THREADS, Shape::kOcc)
 constexpr int kJoinWarps = 8;
 constexpr int kJoinAhead = 8;  // parts whose loads a lane has in flight
 constexpr int kWideAhead = 4;
+// The weight of a part at the row's maximum: the sum of all pieces' parts stays within one part's range.
+constexpr float kJoinUnit = 0x1p-12f;
 
 // The call's status from the pieces' (by the first CTA).
 __device__ __forceinline__ void join_status(const CaParams& p) {
@@ -644,7 +665,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_attention_join_kernel(c
     for (int k0 = 0; k0 < cut.pieces; k0 += 32) {
       const int here = cut.pieces - k0 < 32 ? cut.pieces - k0 : 32;
       const float2 ml = k0 == 0 ? first : statistic(k0 + lane);
-      const float weight = ex2_approx(ml.x - top);
+      const float weight = ex2_approx(ml.x - top) * kJoinUnit;
       sum += weight * ml.y;  // a statistic of no part: 0
       for (int j0 = 0; j0 < here; j0 += kJoinAhead) {
 #pragma unroll
