@@ -508,6 +508,7 @@ CONVROT_API convrot_status convrot_cache_read(const convrot_cache_args* args, co
  *   starts    [B+1] int32, device, rising from >= 0 to <= T; or NULL with T = B:
  *             one token per sequence.
  *   tree      [T] 64-bit masks, device, or NULL.
+ *   softmax_scale  positive, and finite also times log2(e).
  *   ws        >= convrot_cache_attention_workspace_bytes(T, B, Hq, Hkv, D) bytes,
  *             256-byte aligned, no initialisation; its first word is the status
  *             word (convrot_read_device_status), written by every call with T > 0:

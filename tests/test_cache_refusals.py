@@ -211,3 +211,15 @@ def test_binding_without_its_status_argument_is_left_to_python(L):
 
     b = _lib.binding()
     assert b.attention(*[None] * 12) is None and b.attention(*[None] * 13) is None
+
+
+def test_a_softmax_scale_that_overflows_in_base_2(L):
+    """Times log2(e) it is infinite, and an all-zero query's equal logits 0 * inf."""
+    from w8a8_rotated_int8_token_b200 import _lib
+
+    def status(scale):  # no tokens: what is fine returns 0
+        args = _lib.CACHE_ATTENTION_ARGS.pack(*CELLS_OK, FAKE, FAKE, FAKE, FAKE, 0, 0, FAKE, 1 << 30, 0, 8, 0, 3, 3, 1024,
+                                              128, 1024, 128, scale, 0)
+        return L.convrot_cache_attention(args, None)
+
+    assert status(2.3e38) == 0 and status(2.4e38) == 1 and status(2.9e38) == 1

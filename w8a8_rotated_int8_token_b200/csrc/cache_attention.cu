@@ -866,7 +866,8 @@ convrot_status convrot_cache_attention_ex(const convrot_cache_attention_args* ar
       a.table_pages > 0x7FFFF000 / c.page_size)
     return CONVROT_ERR_UNSUPPORTED;
   if (a.starts == nullptr && a.T != a.B) return CONVROT_ERR_INVALID_ARG;
-  if (!(a.softmax_scale > 0.0f) || !(a.softmax_scale < 3.0e38f)) return CONVROT_ERR_INVALID_ARG;
+  const float c_scale = a.softmax_scale * 1.4426950408889634f;
+  if (!(a.softmax_scale > 0.0f) || !(c_scale < INFINITY)) return CONVROT_ERR_INVALID_ARG;
   auto stride = [](int64_t n, int64_t st) { return n > 1 ? st : 0; };
   CaParams p{};
   p.qt = stride(a.T, a.q_token), p.qh = stride(a.Hq, a.q_head);
@@ -902,7 +903,7 @@ convrot_status convrot_cache_attention_ex(const convrot_cache_attention_args* ar
   p.table_pages = static_cast<int>(a.table_pages);
   p.num_pages = static_cast<int>(c.num_pages);
   while ((int64_t{1} << p.page_shift) < c.page_size) ++p.page_shift;
-  p.c_scale = a.softmax_scale * 1.4426950408889634f;
+  p.c_scale = c_scale;
   p.told = status;
   p.wait_ns = wait_ns > 0 ? static_cast<uint64_t>(wait_ns) : CA_WAIT_NS;
   p.wait_step = p.wait_ns < 2000 ? static_cast<uint32_t>(p.wait_ns) : 2000;
