@@ -519,7 +519,7 @@ CONVROT_API convrot_status convrot_cache_read(const convrot_cache_args* args, co
  * Keys are read once per tile of 8, 16 or 128 query rows (n * Hq / Hkv rows per
  * key head; the tile follows from T, B and the heads), so this is the form for
  * single tokens, drafts and chunks; long prompts belong to
- * convrot_attention_int8. Two kernels; how the work is cut follows from the
+ * convrot_attention_int8. Two kernels (B = 0: a 4-byte memset of the status word); how the work is cut follows from the
  * lengths, and the result does not depend on timing. A timed-out wait (the tile
  * of 128 rows waits on its own copies and products) sets the status word to
  * CONVROT_ERR_DEVICE_TIMEOUT, and every row it cost is NaN.

@@ -223,3 +223,13 @@ def test_a_softmax_scale_that_overflows_in_base_2(L):
         return L.convrot_cache_attention(args, None)
 
     assert status(2.3e38) == 0 and status(2.4e38) == 1 and status(2.9e38) == 1
+
+
+def test_queries_of_no_sequence_need_a_workspace(L):
+    """Their call clears its status word, as every call with tokens writes it."""
+    from w8a8_rotated_int8_token_b200 import _lib
+
+    for ws, size in ((0, 1 << 20), (FAKE + 16, 1 << 20), (FAKE, 255)):
+        args = _lib.CACHE_ATTENTION_ARGS.pack(*CELLS_OK, FAKE, FAKE, FAKE, FAKE, FAKE, 0, ws, size, 4, 8, 0, 3, 3, 1024, 128,
+                                              1024, 128, 0.1, 0)
+        assert L.convrot_cache_attention(args, None) == 3

@@ -871,3 +871,15 @@ def test_seen_values_of_any_size_under_rising_logits(cr, hq, value):
     s = Setup(cr, [(20000, 1)], hq, 1, 64, seed=25)  # cut among all CTAs, equal values
     s.scales[1][np.isfinite(s.scales[1])] = value
     s.check(s.run())
+
+
+def test_queries_of_no_sequence(cr):
+    import torch
+
+    s = Setup(cr, [(40, 1)], 4, 2, 16, seed=26)
+    pages, lengths, starts = s.args()
+    ws = torch.full((256,), 255, dtype=torch.uint8, device="cuda")
+    O = torch.full_like(s.Q, 3.0)
+    cr.convrot_cache_attention(s.Q, *s.cells(), pages[:0], lengths[:0], starts[:1], O=O, ws=ws)
+    assert cr.convrot_read_device_status(ws) == 0 and bool((O == 3.0).all())
+    assert bool((ws[4:] == 255).all())

@@ -874,8 +874,15 @@ convrot_status convrot_cache_attention_ex(const convrot_cache_attention_args* ar
   p.ot = stride(a.T, a.o_token), p.oh = stride(a.Hq, a.o_head);
   p.table_stride = stride(a.B, a.table_stride);
   if ((p.qt | p.qh | p.ot | p.oh) % 8 != 0 || p.table_stride < 0) return CONVROT_ERR_INVALID_ARG;
-  if (a.T == 0 || a.B == 0) return CONVROT_OK;  // no queries
+  if (a.T == 0) return CONVROT_OK;  // no queries
   auto aligned = [](const void* ptr, uintptr_t to) { return (reinterpret_cast<uintptr_t>(ptr) % to) == 0; };
+  const bool room = a.ws != nullptr && aligned(a.ws, 256) &&
+                    a.ws_bytes >= convrot_cache_attention_workspace_bytes(a.T, a.B, a.Hq, c.H, c.D);
+  if (a.B == 0) {  // queries of no sequence: a clean status word is all there is to do
+    if (!room) return CONVROT_ERR_WORKSPACE;
+    return cudaMemsetAsync(a.ws, 0, sizeof(int), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? CONVROT_OK
+                                                                                                         : CONVROT_ERR_CUDA;
+  }
   for (const void* ptr : {a.Q, static_cast<const void*>(a.O), static_cast<const void*>(c.k_codes),
                           static_cast<const void*>(c.v_codes), static_cast<const void*>(c.k_scale),
                           static_cast<const void*>(c.v_scale)})
@@ -883,9 +890,7 @@ convrot_status convrot_cache_attention_ex(const convrot_cache_attention_args* ar
   if (a.lengths == nullptr || (a.pages == nullptr && a.table_pages > 0) || !aligned(a.pages, 4) ||
       !aligned(a.lengths, 4) || !aligned(a.starts, 4) || !aligned(a.tree, 8))
     return CONVROT_ERR_INVALID_ARG;
-  if (a.ws == nullptr || !aligned(a.ws, 256) ||
-      a.ws_bytes < convrot_cache_attention_workspace_bytes(a.T, a.B, a.Hq, c.H, c.D))
-    return CONVROT_ERR_WORKSPACE;
+  if (!room) return CONVROT_ERR_WORKSPACE;
   p.q = static_cast<const uint16_t*>(a.Q);
   p.o = static_cast<uint16_t*>(a.O);
   p.k_codes = c.k_codes;
