@@ -111,3 +111,50 @@ def test_a_library_that_does_not_compile_is_an_error(tools):
     with pytest.raises(RuntimeError, match="no such header"):
         build.build()
     assert not os.path.exists(build.LIB_PATH)
+
+
+@pytest.mark.gpu
+def test_an_error_behind_a_launch_is_not_answered_by_a_second_one():
+    """A library that launches and then reports a CUDA error (one left by an earlier call will do): the call is not
+    repeated in Python, which would turn heads in place twice."""
+    import ctypes
+
+    import torch
+
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import w8a8_rotated_int8_token_b200 as cr
+
+    heads = torch.randn(5, 2, 128, device="cuda").bfloat16()
+    pos = torch.arange(5, dtype=torch.int32, device="cuda").view(1, 5)
+    freq, axis = cr.convrot_rope_tables([64])
+    slots = torch.arange(5, dtype=torch.int32, device="cuda")
+    cache = cr.ConvRotCache(1, 2, 16)
+    pages, lengths = torch.zeros(5, 1, dtype=torch.int32, device="cuda"), torch.ones(5, dtype=torch.int32, device="cuda")
+    native = cr._lib.binding()
+    assert native is not None
+    real = [ctypes.cast(f, ctypes.c_void_p).value for f in (
+        cr.lib().convrot_rope, cr.lib().convrot_cache_append, cr.lib().convrot_cache_read,
+        cr.lib().convrot_cache_attention_ex, cr.lib().convrot_cache_attention_workspace_bytes)]
+    calls = [(lambda: cr.convrot_rope(heads, pos, freq, axis, Y=heads), "convrot_rope"),
+             (lambda: cache.append(heads, heads, slots), "convrot_cache_append"),
+             (lambda: cache.read(slots), "convrot_cache_read"),
+             (lambda: cache.attention(heads, pages, lengths), "convrot_cache_attention")]
+    for call, _ in calls:
+        call()  # the native form is bound
+    was = [t.clone() for t in (heads, *cache.cells)]
+    seen = []
+    three = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p)
+    four = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p)
+    fails = three(lambda *a: seen.append(0) or 4), four(lambda *a: seen.append(0) or 4)
+    at = [ctypes.cast(f, ctypes.c_void_p).value for f in fails]
+    try:
+        native.bind(at[0], at[0], at[0], at[1], real[4])
+        for call, name in calls:
+            with pytest.raises(cr.ConvRotError, match=name) as e:
+                call()
+            assert e.value.status == 4 and len(seen) == 1
+            seen.clear()
+    finally:
+        native.bind(*real)
+    assert all(torch.equal(a, b) for a, b in zip(was, (heads, *cache.cells)))

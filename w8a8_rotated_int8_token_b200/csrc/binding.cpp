@@ -18,6 +18,8 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
+#include <string>
 
 #include "convrot.h"
 
@@ -95,16 +97,34 @@ bool status_word(PyObject* o, int device, int** to) {
 }
 
 template <class Args, class... More, class... Same>
-bool call(Status (*fn)(const Args*, More...), const Args& args, int device, Same... more) {
-  if (fn == nullptr) return false;
+Status call(Status (*fn)(const Args*, More...), const Args& args, int device, Same... more) {
+  if (fn == nullptr) return CONVROT_ERR_INVALID_ARG;
   const convrot_stream_t s = stream_of(device);
   Status st;
   Py_BEGIN_ALLOW_THREADS st = fn(&args, more..., s);
-  Py_END_ALLOW_THREADS return st == CONVROT_OK;
+  Py_END_ALLOW_THREADS return st;
+}
+
+// A call that did not succeed: None for the Python form, which says what is wrong with it. An error of CUDA's is raised
+// here: it may have come behind a launch, and heads must not be turned in place a second time.
+PyObject* failed(PyObject* self, Status st, const char* name) {
+  if (st != CONVROT_ERR_CUDA) Py_RETURN_NONE;
+  const char* module_name = PyModule_GetName(self);
+  if (module_name == nullptr) return nullptr;
+  const char* dot = std::strrchr(module_name, '.');
+  const std::string package(module_name, dot != nullptr ? dot - module_name : std::strlen(module_name));
+  PyObject* home = PyImport_ImportModule(package.c_str());
+  PyObject* type = home != nullptr ? PyObject_GetAttrString(home, "ConvRotError") : nullptr;
+  PyObject* error = type != nullptr ? PyObject_CallFunction(type, "is", static_cast<int>(st), name) : nullptr;
+  if (error != nullptr) PyErr_SetObject(type, error);
+  Py_XDECREF(error);
+  Py_XDECREF(type);
+  Py_XDECREF(home);
+  return nullptr;
 }
 
 // rope(X, positions, freq, axis, interleaved, inverse, Y or None)
-PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 7) Py_RETURN_NONE;
   const at::Tensor *x = tensor(a[0]), *pos = tensor(a[1]), *freq = tensor(a[2]), *axis = tensor(a[3]);
@@ -146,7 +166,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r.dtype = code;
   r.pos_dtype = pos->scalar_type() == at::kInt ? CONVROT_POS_I32 : CONVROT_POS_F32;
   r.interleaved = inter, r.inverse = inverse;
-  if (!call(rope_fn, r, device)) Py_RETURN_NONE;
+  if (const Status st = call(rope_fn, r, device); st != CONVROT_OK) return failed(self, st, "convrot_rope");
   if (a[6] == Py_None) return THPVariable_Wrap(std::move(made));
   Py_INCREF(a[6]);
   return a[6];
@@ -154,7 +174,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status or None) -> True or None
-PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 8) Py_RETURN_NONE;
   const at::Tensor *k = tensor(a[0]), *v = tensor(a[1]), *slots = tensor(a[2]);
@@ -172,13 +192,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r.T = k->size(0);
   r.k_token = k->stride(0), r.k_head = k->stride(1), r.v_token = v->stride(0), r.v_head = v->stride(1);
   r.dtype = code;
-  if (!call(append_fn, r, device)) Py_RETURN_NONE;
+  if (const Status st = call(append_fn, r, device); st != CONVROT_OK) return failed(self, st, "convrot_cache_append");
   Py_RETURN_TRUE;
   END_HANDLE_TH_ERRORS
 }
 
 // read(slots, k_codes, v_codes, k_scale, v_scale, dtype code, K or None, V or None, status or None) -> (K, V) or None
-PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* read(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 9) Py_RETURN_NONE;
   const at::Tensor* slots = tensor(a[0]);
@@ -211,7 +231,7 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r.k_token = out[0]->stride(0), r.k_head = out[0]->stride(1);
   r.v_token = out[1]->stride(0), r.v_head = out[1]->stride(1);
   r.dtype = static_cast<int>(code);
-  if (!call(read_fn, r, device)) Py_RETURN_NONE;
+  if (const Status st = call(read_fn, r, device); st != CONVROT_OK) return failed(self, st, "convrot_cache_read");
   PyObject* pair = PyTuple_New(2);
   if (pair == nullptr) return nullptr;
   for (int i = 0; i < 2; ++i) {
@@ -230,7 +250,7 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree, softmax_scale, O, ws, status); the
 // last six may be None
-PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 13) Py_RETURN_NONE;
   const at::Tensor *q = tensor(a[0]), *pages = tensor(a[5]), *lengths = tensor(a[6]);
@@ -292,7 +312,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   r.table_pages = pages->size(1), r.table_stride = pages->stride(0);
   r.q_token = q->stride(0), r.q_head = q->stride(1), r.o_token = o->stride(0), r.o_head = o->stride(1);
   r.dtype = code;
-  if (!call(attention_fn, r, device, status, int64_t{0})) Py_RETURN_NONE;
+  if (const Status st = call(attention_fn, r, device, status, int64_t{0}); st != CONVROT_OK) return failed(self, st, "convrot_cache_attention");
   if (a[10] == Py_None) return THPVariable_Wrap(std::move(made));
   Py_INCREF(a[10]);
   return a[10];
