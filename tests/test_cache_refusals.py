@@ -233,3 +233,17 @@ def test_queries_of_no_sequence_need_a_workspace(L):
         args = _lib.CACHE_ATTENTION_ARGS.pack(*CELLS_OK, FAKE, FAKE, FAKE, FAKE, FAKE, 0, ws, size, 4, 8, 0, 3, 3, 1024, 128,
                                               1024, 128, 0.1, 0)
         assert L.convrot_cache_attention(args, None) == 3
+
+
+def test_cache_slots_of_pages_past_the_cache():
+    """They stay past it, where the append reports them, also where 32 bits would bring them back to its first slots."""
+    import torch
+
+    import w8a8_rotated_int8_token_b200 as cr
+
+    cache = cr.ConvRotCache(4, 1, 64, device="cpu")
+    pages = torch.tensor([[4, 1 << 26, (1 << 26) + 1, 2**31 - 1, -2**31, 3]], dtype=torch.int32)
+    at = torch.arange(6) * 64 + 5
+    got = cache.slots(pages, torch.zeros(6, dtype=torch.int64), at)
+    assert got.dtype == torch.int32
+    assert got.tolist() == [4 * 64 + 5, 2**31 - 1, 2**31 - 1, 2**31 - 1, -1, 3 * 64 + 5]

@@ -749,17 +749,19 @@ class ConvRotCache:
 
     def slots(self, pages, sequence, position):
         """Slots (int32) of the tokens at `position` of the sequences whose rows of `pages` are
-        `sequence`; -1 where `pages` has no such place or no page for it."""
+        `sequence`; -1 where `pages` has no such place or no page for it. A page past the cache gives a
+        slot past it, which the append reports."""
         import torch
 
         sequence, position = sequence.long(), position.long()
         if pages.numel() == 0:
             return torch.full(position.shape, -1, dtype=torch.int32, device=position.device)
         column = position // self.page_size
-        page = pages[sequence.clamp(0, pages.shape[0] - 1), column.clamp(0, pages.shape[1] - 1)]
+        page = pages[sequence.clamp(0, pages.shape[0] - 1), column.clamp(0, pages.shape[1] - 1)].long()
         there = ((sequence >= 0) & (sequence < pages.shape[0]) & (position >= 0) & (column < pages.shape[1])
                  & (page >= 0))
-        return torch.where(there, page * self.page_size + position % self.page_size, -1).to(torch.int32)
+        slot = (page * self.page_size + position % self.page_size).clamp(max=2**31 - 1)
+        return torch.where(there, slot, -1).to(torch.int32)
 
     def append(self, K, V, slots, stream=None):
         convrot_cache_append(K, V, slots, *self.cells, status=self.status, stream=stream)
