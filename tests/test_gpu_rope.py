@@ -239,3 +239,127 @@ def test_pairs_of_no_axis_are_copied_whatever_they_hold(cr, kind, interleaved, s
     rest = torch.ones(128, dtype=torch.bool, device="cuda")
     rest[both] = False
     assert torch.equal(Y[..., rest], want[..., rest])
+
+
+@pytest.mark.parametrize("kind,interleaved,D,R", [("bf16", False, 128, 128), ("f16", True, 128, 64), ("f16", False, 36, 30)])
+def test_autograd_records_it(cr, kind, interleaved, D, R):
+    """The gradient is the inverse's, of any gradient of the output: also a strided or broadcast one, of heads turned in
+    place, of heads written into a buffer of another order, and of the gradient itself."""
+    import torch
+
+    X, pos = _inputs(2, 9, 3, D, kind, 11, pad=1)
+    sizes = [R // 2 - 2 * (R // 6), R // 6, R // 6]
+    freq, axis = cr.convrot_rope_tables(sizes)
+    G = torch.randn_like(X, memory_format=torch.contiguous_format)
+    x = X.detach().clone().requires_grad_()
+    y = cr.convrot_rope(x, pos, freq, axis, interleaved)
+    assert torch.equal(y.detach(), cr.convrot_rope(X, pos, freq, axis, interleaved))
+    y.backward(G)
+    _check(cr, G, pos, freq, axis, kind, interleaved, True, x.grad)
+    want = x.grad.clone()
+
+    def gradient(make, g=G):
+        x = X.detach().clone().requires_grad_()
+        return torch.autograd.grad(make(x), x, g)[0]
+
+    def in_place(x):
+        z = x * 1
+        assert cr.convrot_rope(z, pos, freq, axis, interleaved, Y=z) is z
+        return z
+
+    def head_major(x):
+        room = torch.empty(2, 3, 9, D, dtype=X.dtype, device="cuda")
+        cr.convrot_rope(x, pos, freq, axis, interleaved, Y=room.transpose(1, 2))
+        return room.transpose(1, 2)
+
+    def three(x):
+        return torch.stack([cr.convrot_rope(x[b], pos[:, b], freq, axis, interleaved) for b in range(2)])
+
+    side = torch.cuda.Stream()
+
+    def elsewhere(x):
+        side.wait_stream(torch.cuda.current_stream())
+        out = cr.convrot_rope(x, pos, freq, axis, interleaved, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        return out
+
+    def part_of_a_row(x):  # in place in a view, beside what stays
+        rows = torch.cat([x, x * 0], 2)
+        part = rows[:, :, :3]
+        cr.convrot_rope(part, pos, freq, axis, interleaved, Y=part)
+        return rows[:, :, :3]
+
+    for make in (in_place, head_major, three, elsewhere, part_of_a_row):
+        assert torch.equal(gradient(make), want), make
+    turned = lambda x: cr.convrot_rope(x, pos, freq, axis, interleaved)  # noqa: E731
+    strided = G.transpose(1, 3).contiguous().transpose(1, 3)
+    assert strided.stride(-1) != 1 and torch.equal(gradient(turned, strided), want)
+    ones = gradient(lambda x: turned(x).sum(), None)
+    assert torch.equal(ones, cr.convrot_rope(torch.ones_like(X), pos, freq, axis, interleaved, inverse=True))
+    # what is overwritten has no gradient, what stands beside it keeps its own
+    x, w = X.detach().clone().requires_grad_(), torch.randn(2, 9, 4, D, device="cuda").to(X.dtype).requires_grad_()
+    rows = w * 1
+    cr.convrot_rope(x, pos, freq, axis, interleaved, Y=rows[:, :, 1:])
+    dx, dw = torch.autograd.grad(rows[:, :, 1:], (x, w), G, retain_graph=True)
+    assert torch.equal(dx, want) and not bool(dw.any())
+    dw = torch.autograd.grad(rows.sum(), w)[0]
+    assert bool((dw[:, :, 0] == 1).all()) and not bool(dw[:, :, 1:].any())
+    # through the inverse, and the gradient's own gradient
+    back = lambda x: cr.convrot_rope(x, pos, freq, axis, interleaved, inverse=True)  # noqa: E731
+    assert torch.equal(gradient(back), cr.convrot_rope(G, pos, freq, axis, interleaved))
+    x, g = X.detach().clone().requires_grad_(), G.clone().requires_grad_()
+    dx = torch.autograd.grad(turned(x), x, g, create_graph=True)[0]
+    assert torch.equal(torch.autograd.grad(dx, g, G)[0], cr.convrot_rope(G, pos, freq, axis, interleaved))
+
+
+def test_autograd_against_elementary_operations(cr):
+    """In float64, of the same pairs: the kernel's gradient is within its rounding."""
+    import torch
+
+    X, pos = _inputs(1, 7, 2, 64, "f16", 12)
+    freq, axis = cr.convrot_rope_tables([8, 12, 12])
+    G = torch.randn_like(X, memory_format=torch.contiguous_format)
+    x = X.detach().clone().requires_grad_()
+    cr.convrot_rope(x, pos, freq, axis).backward(G)
+    z = X.detach().double().requires_grad_()
+    angle = (pos.double()[axis.long()].permute(1, 2, 0) * freq)[:, :, None, :]
+    a, b = z[..., :32], z[..., 32:]
+    torch.cat([a * angle.cos() - b * angle.sin(), b * angle.cos() + a * angle.sin()], -1).backward(G.double())
+    pair = G.double().abs().view(1, 7, 2, 2, 32).sum(-2, keepdim=True).expand(1, 7, 2, 2, 32).reshape(1, 7, 2, 64)
+    bound = OUT_REL["f16"] * z.grad.abs() + 5e-7 * pair + OUT_ABS["f16"]
+    assert bool(((x.grad.double() - z.grad).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_autograd_learns_of_writes_and_is_told_what_cannot_be(cr, monkeypatch, native):
+    import torch
+
+    if not native:
+        monkeypatch.setattr(cr._T, "rope", lambda *a: None)
+    X, pos = _inputs(1, 5, 2, 64, "bf16", 13)
+    X = X.contiguous()
+    freq, axis = cr.convrot_rope_tables([32])
+    x = X.clone().requires_grad_()
+    with pytest.raises(RuntimeError, match="leaf"):
+        cr.convrot_rope(x, pos, freq, axis, Y=x)
+    assert torch.equal(x.detach(), X)
+    for given in (dict(positions=pos.float().requires_grad_()), dict(freq=freq.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="detach"):
+            cr.convrot_rope(**(dict(X=X, positions=pos, freq=freq, axis=axis) | given))
+        with torch.no_grad():
+            assert not cr.convrot_rope(**(dict(X=X, positions=pos, freq=freq, axis=axis) | given)).requires_grad
+    with torch.no_grad():
+        assert not cr.convrot_rope(x, pos, freq, axis).requires_grad
+        cr.convrot_rope(x, pos, freq, axis, Y=x)
+    with torch.inference_mode():
+        z = X.clone()
+        cr.convrot_rope(z, pos, freq, axis, Y=z)
+    cr.convrot_rope(X, pos, freq, axis, Y=z)  # a tensor without versions
+    # an operation that keeps its input learns that it has been overwritten
+    x = X.clone().requires_grad_()
+    z = x * 2
+    out = (z * z).sum()
+    with torch.no_grad():
+        cr.convrot_rope(z, pos, freq, axis, Y=z)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.backward()

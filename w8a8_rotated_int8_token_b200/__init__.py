@@ -423,6 +423,7 @@ class _Torch:
         self.float32, self.float64 = torch.float32, torch.float64
         self.dense = torch.contiguous_format
         self.empty_like, self.empty = torch.empty_like, torch.empty
+        self.grad = torch.is_grad_enabled
         self.device = torch._C._cuda_getDevice
         self.stream = torch._C._cuda_getCurrentRawStream  # a Stream object costs ten times as much
         # the native forms of the calls; they return None where the Python form has to see to a call
@@ -493,6 +494,12 @@ def _output(t, name, code, index, shape):
     return strides
 
 
+def _written(t):
+    """Tells autograd that a tensor of the caller's has been written, as torch's own operations do."""
+    if not t.is_inference():
+        _T.module.autograd.graph.increment_version(t)
+
+
 def convrot_rope_tables(sections, theta: float = 10000.0, shared: bool = False, device="cuda"):
     """The tables of convrot_rope for axes with sections[a] pairs of channels each, in order:
     (freq float64, axis int32), both [sum(sections)]. Each axis has its own ladder
@@ -515,7 +522,8 @@ def convrot_rope(X, positions, freq, axis, interleaved: bool = False, inverse: b
     positions[axis[i]] * freq[i]. positions [axes, S] or [axes, B, S], int32 or float32;
     freq float64 (radians), axis int32. `inverse` turns back, which is also the gradient.
     Y: an output of X's shape and any strides (X itself works in place); with
-    Y = buf.transpose(-3, -2) the heads come out as convrot_attention_int8 takes them."""
+    Y = buf.transpose(-3, -2) the heads come out as convrot_attention_int8 takes them.
+    Recorded by autograd for X, in place and into Y too; positions and freq take no gradient."""
     if stream is None:
         done = _T.rope(X, positions, freq, axis, interleaved, inverse, Y)
         if done is not None:
@@ -526,6 +534,9 @@ def convrot_rope(X, positions, freq, axis, interleaved: bool = False, inverse: b
         if where is not None:
             with where:
                 return convrot_rope(X, positions, freq, axis, interleaved, inverse, Y)
+    if _T.grad() and (X.requires_grad or positions.requires_grad or freq.requires_grad
+                      or (Y is not None and Y.requires_grad)):
+        return _recorded_rope(X, positions, freq, axis, interleaved, inverse, Y)
     if len(shape) == 4:
         B, S, H, D = shape
     else:
@@ -552,7 +563,8 @@ def convrot_rope(X, positions, freq, axis, interleaved: bool = False, inverse: b
         pb = None
     if pb is None or pshape[0] < 1 or pshape[-1] != S:
         raise ValueError(f"positions: expected [axes, {S}] or [axes, {B}, {S}], got {tuple(pshape)}")
-    if Y is None:
+    given = Y is not None
+    if not given:
         Y = _T.empty_like(X, memory_format=_T.dense)
         yb, ys, yh = S * H * D, H * D, D
     else:
@@ -564,7 +576,50 @@ def convrot_rope(X, positions, freq, axis, interleaved: bool = False, inverse: b
     status = (_lib._lib or lib()).convrot_rope(args, _T.stream(index))
     if status != 0:
         raise ConvRotError(status, "convrot_rope")
+    if given:
+        _written(Y)
     return Y
+
+
+@functools.lru_cache(maxsize=1)
+def _rope_function():
+    import torch
+
+    class Rope(torch.autograd.Function):
+        # Y, the tensor written in place, comes first, as autograd has it of views; X is None where Y is turned itself
+        @staticmethod
+        def forward(ctx, Y, X, positions, freq, axis, interleaved, inverse):
+            ctx.save_for_backward(positions, freq, axis)
+            ctx.turn = interleaved, inverse
+            ctx.in_place = X is None
+            out = convrot_rope(Y if X is None else X, positions, freq, axis, interleaved, inverse, Y)
+            if Y is not None:
+                ctx.mark_dirty(out)
+            return out
+
+        @staticmethod
+        def backward(ctx, dY):
+            interleaved, inverse = ctx.turn
+            dX = old = None
+            if ctx.needs_input_grad[0 if ctx.in_place else 1]:
+                rows = dY if dY.stride(-1) == 1 else dY.contiguous()
+                dX = convrot_rope(rows, *ctx.saved_tensors, interleaved, not inverse)
+            if ctx.in_place:
+                old, dX = dX, None
+            elif ctx.needs_input_grad[0]:
+                old = torch.zeros_like(dY)  # what Y held before is gone
+            return (old, dX) + (None,) * 5
+
+    return Rope
+
+
+def _recorded_rope(X, positions, freq, axis, interleaved, inverse, Y):
+    """convrot_rope where autograd follows X, or a Y that it has followed so far."""
+    if positions.requires_grad or freq.requires_grad:
+        raise ValueError("positions and freq take no gradient: detach them")
+    if Y is not None and Y.requires_grad and Y.is_leaf:
+        raise RuntimeError("Y is a leaf that requires grad: it cannot be written to in place")
+    return _rope_function().apply(Y, None if Y is X else X, positions, freq, axis, interleaved, inverse)
 
 
 def _cells(index, k_codes, v_codes, k_scale, v_scale):

@@ -9,6 +9,7 @@
 // nothing of it. Time of a call that the host bounds, checked in Python and here: rope
 // 8.0 and 4.5 us, a read 12.0 and 6.4, an append with a read of what it wrote 19.9 and 10.0.
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -60,6 +61,11 @@ bool output(const at::Tensor* t, int device, at::ScalarType type, at::IntArrayRe
   for (int64_t i = 0; i < t->dim(); ++i)
     if (t->size(i) > 1 && t->stride(i) == 0) return false;
   return true;
+}
+
+// Tells autograd that a tensor of the caller's has been written, as torch's own operations do.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 bool here(int device) { return device >= 0 && c10::cuda::current_device() == device; }
@@ -137,6 +143,10 @@ PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   r.B = dims == 4 ? x->size(0) : 1;
   r.S = x->size(dims - 3), r.H = x->size(dims - 2), r.D = x->size(dims - 1);
   const int64_t pairs = freq->numel();
+  // autograd's business is seen to in Python
+  if (at::GradMode::is_enabled() && (x->requires_grad() || pos->requires_grad() || freq->requires_grad() ||
+                                     (a[6] != Py_None && tensor(a[6]) != nullptr && tensor(a[6])->requires_grad())))
+    Py_RETURN_NONE;
   if (2 * pairs > r.D || !plain(freq, device, at::kDouble, {pairs}) || !plain(axis, device, at::kInt, {pairs}))
     Py_RETURN_NONE;
   const int64_t pdims = pos->dim();
@@ -168,6 +178,7 @@ PyObject* rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   r.interleaved = inter, r.inverse = inverse;
   if (const Status st = call(rope_fn, r, device); st != CONVROT_OK) return failed(self, st, "convrot_rope");
   if (a[6] == Py_None) return THPVariable_Wrap(std::move(made));
+  written(*y);
   Py_INCREF(a[6]);
   return a[6];
   END_HANDLE_TH_ERRORS
