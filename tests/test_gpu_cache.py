@@ -250,3 +250,33 @@ def test_read_with_a_last_warp_partly_without_tokens(cr, kind):
             want = want[:T].clone()
             want[T // 2] = 0.0
             assert torch.equal(x, want) and bool((rest[T:] == 3.0).all())
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_autograd_learns_of_outputs_written(cr, monkeypatch, native):
+    """An operation that keeps a tensor for its gradient learns that a read or an attention has overwritten it."""
+    import torch
+
+    if not native:
+        for name in ("read", "attention"):
+            monkeypatch.setattr(cr._T, name, lambda *a: None)
+    K, V = _heads(4, 2, "bf16", 6)
+    cache = cr.ConvRotCache(1, 2, 16)
+    slots = torch.arange(4, dtype=torch.int32, device="cuda")
+    cache.append(K, V, slots)
+    pages = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    lengths = torch.tensor([4], dtype=torch.int32, device="cuda")
+
+    def write(at):
+        room = [torch.ones(4, 2, 128, dtype=K.dtype, device="cuda") for _ in range(3)]
+        w = torch.ones(4, 2, 128, dtype=K.dtype, device="cuda", requires_grad=True)
+        out = (w * room[at]).sum()
+        if at < 2:
+            cache.read(slots, K=room[0], V=room[1])
+        else:
+            cache.attention(K[:1], pages, lengths, O=room[2][:1])
+        return out
+
+    for at in range(3):
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            write(at).backward()

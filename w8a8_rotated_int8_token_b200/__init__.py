@@ -692,6 +692,7 @@ def convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype=None, K=
         raise TypeError(f"dtype: expected bfloat16 or float16, got {dtype}")
     shape = (T, H, 128)
     ks = vs = (H * 128, 128)
+    given = [t for t in (K, V) if t is not None]
     if K is not None:
         ks = _output(K, "K", code, index, shape)
     else:
@@ -706,6 +707,8 @@ def convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype=None, K=
     status = (_lib._lib or lib()).convrot_cache_read(args, _T.stream(index))
     if status != 0:
         raise ConvRotError(status, "convrot_cache_read")
+    for t in given:
+        _written(t)
     return K, V
 
 
@@ -722,7 +725,8 @@ def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, length
     (None: token b belongs to sequence b). Among its new tokens a query sees the earlier ones and
     itself, or, with tree [T] int64, those whose bit is set in its mask (at most 64 a sequence).
     status: an int32 [1] tensor into which the call's status is ORed (1: a length, page or start was
-    out of range; 5: a wait ran out and the rows it cost are NaN), or None. See include/convrot.h."""
+    out of range; 5: a wait ran out and the rows it cost are NaN), or None. Nothing here is recorded
+    by autograd. See include/convrot.h."""
     if stream is None:
         done = _T.attention(Q, k_codes, v_codes, k_scale, v_scale, pages, lengths, starts, tree, softmax_scale, O, ws,
                             status)
@@ -757,7 +761,8 @@ def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, length
     if softmax_scale is None:
         softmax_scale = 0.08838834764831845  # 1 / sqrt(128)
     ot, oh = Hq * D, D
-    if O is not None:
+    given = O is not None
+    if given:
         ot, oh, _ = _output(O, "O", code, index, shape)
     else:
         O = _T.empty_like(Q, memory_format=_T.dense)
@@ -775,6 +780,8 @@ def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, length
     status = (_lib._lib or lib()).convrot_cache_attention_ex(args, status_ptr, 0, _T.stream(index))
     if status != 0:
         raise ConvRotError(status, "convrot_cache_attention")
+    if given:
+        _written(O)
     return O
 
 

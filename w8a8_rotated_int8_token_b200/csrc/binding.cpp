@@ -247,8 +247,12 @@ PyObject* read(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   if (pair == nullptr) return nullptr;
   for (int i = 0; i < 2; ++i) {
     PyObject* o = a[6 + i];
-    if (o == Py_None) o = THPVariable_Wrap(std::move(made[i]));
-    else Py_INCREF(o);
+    if (o == Py_None) {
+      o = THPVariable_Wrap(std::move(made[i]));
+    } else {
+      written(*out[i]);
+      Py_INCREF(o);
+    }
     if (o == nullptr) {
       Py_DECREF(pair);
       return nullptr;
@@ -325,6 +329,7 @@ PyObject* attention(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   r.dtype = code;
   if (const Status st = call(attention_fn, r, device, status, int64_t{0}); st != CONVROT_OK) return failed(self, st, "convrot_cache_attention");
   if (a[10] == Py_None) return THPVariable_Wrap(std::move(made));
+  written(*o);
   Py_INCREF(a[10]);
   return a[10];
   END_HANDLE_TH_ERRORS
