@@ -280,3 +280,26 @@ def test_autograd_learns_of_outputs_written(cr, monkeypatch, native):
     for at in range(3):
         with pytest.raises(RuntimeError, match="modified by an inplace operation"):
             write(at).backward()
+
+
+def test_vectors_that_the_kernels_cannot_take_are_named(cr):
+    import torch
+
+    K, V = _heads(4, 2, "bf16", 6)
+    cache = cr.ConvRotCache(1, 2, 16)
+    slots = torch.arange(4, dtype=torch.int32, device="cuda")
+    pages = torch.zeros(4, 1, dtype=torch.int32, device="cuda")
+    lengths = torch.ones(4, dtype=torch.int32, device="cuda")
+    wide = torch.zeros(4, 2, 136, dtype=K.dtype, device="cuda")
+    odd = torch.zeros(4, 2, 132, dtype=K.dtype, device="cuda")[..., :128]  # strides of 132
+    for bad in (wide[..., 4:132], odd):
+        for call, name in ((lambda: cache.append(bad, V, slots), "K"), (lambda: cache.append(K, bad, slots), "V"),
+                           (lambda: cache.read(slots, K=bad), "K"), (lambda: cache.read(slots, V=bad), "V"),
+                           (lambda: cache.attention(bad, pages, lengths), "Q"),
+                           (lambda: cache.attention(K, pages, lengths, O=bad), "O")):
+            with pytest.raises(cr.ConvRotError, match=f": {name} must start on 16 bytes") as e:
+                call()
+            assert e.value.status == 1
+    with pytest.raises(cr.ConvRotError) as e:
+        cache.attention(K, pages, lengths, softmax_scale=-1.0)
+    assert "16 bytes" not in str(e.value)

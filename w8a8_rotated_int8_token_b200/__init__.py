@@ -500,6 +500,14 @@ def _written(t):
         _T.module.autograd.graph.increment_version(t)
 
 
+def _refused(status, where, **vectors):
+    """The error of a call on head vectors, with the one that the kernels cannot take, if it is that."""
+    for name, t in vectors.items():
+        if status == 1 and (t.data_ptr() % 16 or any(st % 8 for n, st in zip(t.shape[:-1], t.stride()) if n > 1)):
+            where = f"{where}: {name} must start on 16 bytes, with strides that are multiples of 8 elements"
+    return ConvRotError(status, where)
+
+
 def convrot_rope_tables(sections, theta: float = 10000.0, shared: bool = False, device="cuda"):
     """The tables of convrot_rope for axes with sections[a] pairs of channels each, in order:
     (freq float64, axis int32), both [sum(sections)]. Each axis has its own ladder
@@ -637,7 +645,7 @@ def _cells(index, k_codes, v_codes, k_scale, v_scale):
 def convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status=None, stream=None):
     """Write keys and values K, V [T, H, 128] (bf16 or fp16, strided tokens and heads) into the
     rotated int8 cache: token t to slot slots[t] (int32; page * page size + place; negative: skipped;
-    the others must differ). Cache: codes int8 [pages, H, page size, 128], scales float32 [pages, H,
+    the others must differ). Head vectors here and below start on 16 bytes, their strides are multiples of 8. Cache: codes int8 [pages, H, page size, 128], scales float32 [pages, H,
     page size]. status: an int32 [1] tensor that a slot past the cache sets to 1, or None."""
     if stream is None and _T.append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status):
         return
@@ -660,7 +668,7 @@ def convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status
                                 vs[1], code)
     status = (_lib._lib or lib()).convrot_cache_append(args, _T.stream(index))
     if status != 0:
-        raise ConvRotError(status, "convrot_cache_append")
+        raise _refused(status, "convrot_cache_append", K=K, V=V)
 
 
 def convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype=None, K=None, V=None, status=None,
@@ -706,7 +714,7 @@ def convrot_cache_read(slots, k_codes, v_codes, k_scale, v_scale, dtype=None, K=
                                 vs[1], code)
     status = (_lib._lib or lib()).convrot_cache_read(args, _T.stream(index))
     if status != 0:
-        raise ConvRotError(status, "convrot_cache_read")
+        raise _refused(status, "convrot_cache_read", K=K, V=V)
     for t in given:
         _written(t)
     return K, V
@@ -779,7 +787,7 @@ def convrot_cache_attention(Q, k_codes, v_codes, k_scale, v_scale, pages, length
         T, Hq, B, pshape[1], ps[0], qs[0], qs[1], ot, oh, softmax_scale, code)
     status = (_lib._lib or lib()).convrot_cache_attention_ex(args, status_ptr, 0, _T.stream(index))
     if status != 0:
-        raise ConvRotError(status, "convrot_cache_attention")
+        raise _refused(status, "convrot_cache_attention", Q=Q, O=O)
     if given:
         _written(O)
     return O
