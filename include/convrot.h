@@ -485,7 +485,8 @@ CONVROT_API convrot_status convrot_cache_read(const convrot_cache_args* args, co
  *   O = (softmax(S) V) R with S, V from the cells as convrot_attention_int8 takes
  *   them from dense heads: the query head vector rotated and quantised to int8
  *   per head, exact integer products, float32 softmax; the weights p s_v are
- *   rounded to fp16 and P V accumulates in float32.
+ *   rounded to fp16 (for fp16 outputs held in two fp16 numbers) and P V accumulates
+ *   in float32.
  * Sequence b has lengths[b] keys in the cells that row b of the page table
  * names (key j in page pages[b, j / page_size], place j % page_size), and the
  * query tokens starts[b] .. starts[b+1]-1 of Q, n of them, which are its last n

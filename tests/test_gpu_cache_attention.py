@@ -883,3 +883,34 @@ def test_queries_of_no_sequence(cr):
     cr.convrot_cache_attention(s.Q, *s.cells(), pages[:0], lengths[:0], starts[:1], O=O, ws=ws)
     assert cr.convrot_read_device_status(ws) == 0 and bool((O == 3.0).all())
     assert bool((ws[4:] == 255).all())
+
+
+@pytest.mark.parametrize("hq,hkv,keys,page", [(8, 2, 700, 64), (12, 1, 333, 16), (80, 1, 1000, 16), (130, 1, 129, 32),
+                                              (96, 2, 64, 16), (70, 1, 65, 16)])
+def test_fp16_outputs_keep_the_weights_bits(cr, hq, hkv, keys, page):
+    """On every tile height a weight is held in two fp16 numbers, to 2^-22 of it or 2^-25 of the row's largest: what is
+    left is the output's half step and the float32 terms of the header."""
+    s = Setup(cr, [(keys, 1), (keys // 2 + 1, 1)], hq, hkv, page, "f16", seed=keys)
+    o = s.run().double().cpu().numpy()
+    u = OUT_REL["f16"]
+    for b, (n, _) in enumerate(s.seqs):
+        (kc, ks), (vc, vs) = s.dense(b, 0), s.dense(b, 1)
+        q = s.q[b:b + 1]
+        ref, w, qc, sq = oracle.cache_attention(q, kc, ks, vc, vs, np.ones((1, n), bool), SCALE)
+        quot = oracle.rotate(q, 128) / sq[..., None].astype(np.float64)
+        tie = (np.abs(np.abs(quot - np.floor(quot)) - 0.5) < 1e-3)[0]
+        some = 0
+        for h in range(hq):
+            g = h // (hq // hkv)
+            if tie[h].any():  # a code may round the other way: the looser bound of check() covers those rows
+                continue
+            some += 1
+            c, f = np.abs(vc[g].astype(np.float64)), vs[g].astype(np.float64)
+            top = np.abs((qc[0, h].astype(np.float64) @ kc[g].T) * ks[g]).max() * float(sq[0, h]) * SCALE
+            e = math.log(2) * 6 * 2.0**-24 * top * math.log2(math.e) + 2.0**-22
+            ws = w[0, h] * f
+            off = (2.0**-22 + 2 * e + (n / 16 + 64) * 2.0**-22) * (ws @ c) + 2.0**-25 * ws.max() * c.sum(0)
+            slack = np.linalg.norm(off) * (1 + u) + 8 * 2.0**-24 * np.linalg.norm(ws @ c)
+            want, got = ref[0, h], o[b, h]
+            assert np.all(np.abs(got - want) <= u * np.abs(want) + slack + OUT_ABS["f16"]), (b, h)
+        assert some >= hq // 4

@@ -28,6 +28,11 @@
 // 67 to 60 us for a tree of 64 drafts behind 32768 keys); only where a weight passes
 // 2^15 within one tile, or a row's first ones are far below their bound, is the tile taken
 // again, at a reference from the logit and scale of each key.
+// Rounding a weight to fp16 is far below bf16's own rounding of the output. For an fp16 output it
+// is as large (2.9e-4 of a row against 2.1e-4 without it), so there a second product adds what the first rounding
+// left, as in the kernel for few rows. Both operands of a whole tile do not fit beside the rest of the shared
+// memory: the tile is taken in two steps of 64 keys, which costs the tree of 64 drafts behind 32768 keys 62 us
+// a call for 51.
 // A run costs about as much as three tiles beside its tiles. Its first two tiles' keys
 // are fetched before its queries are in place, their pages looked up by eight lanes at
 // once, and the parts it leaves for the join lie four channels of all rows after one
@@ -82,15 +87,17 @@ struct CwSmem {
   static constexpr int kOffRow = kOffTile + 2 * 2 * 8 * 4;   // query factors
   static constexpr int kOffStat = kOffRow + 128 * 4;         // [pipeline][row] maximum, sum
   static constexpr int kOffScan = kOffStat + 2 * 128 * 8;
-  // per pipeline: keys there, keys read, S there, S read, weights there, P V done, values there, scales there (of each
-  // buffer); then drain
+  // per pipeline: keys there, keys read, S there, S read, values there, scales there (of each buffer), weights there and
+  // P V done (of each step); then drain
   static constexpr int kOffBar = kOffScan + 18 * 8;
-  static constexpr int kOffMisc = kOffBar + 19 * 8 + 8;
+  static constexpr int kBarriers = 23;
+  static constexpr int kOffMisc = kOffBar + kBarriers * 8 + 8;
   static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;
 };
 
-enum CwBar { kKFull, kKEmpty, kSFull, kSEmpty, kPFull, kODone, kVFull, kSc0, kSc1, kBars };
+enum CwBar { kKFull, kKEmpty, kSFull, kSEmpty, kVFull, kSc0, kSc1, kPFull, kPFull1, kODone, kODone1, kBars };
+static_assert(2 * kBars + 1 == CwSmem::kBarriers, "room for the barriers");
 
 // A barrier of whole warps: what stands before it may have been single lanes' work.
 __device__ __forceinline__ void cw_sync(int id, int threads) {
@@ -133,11 +140,14 @@ __device__ __forceinline__ float2 cw_logits(uint32_t a, uint32_t b, float2 scale
   return __fmul2_rn(__fadd2_rn(x, make_float2(-12582912.0f, -12582912.0f)), scale);
 }
 
+// The row's functions below work on one step of a tile: CHUNKS times 16 keys, from 16 w0 on.
+
 // The largest logit of a row among the keys it sees, without the row's factor.
-__device__ __forceinline__ float cw_top(uint32_t tS, const uint32_t (&vis)[4], const float* sk) {
+template <int CHUNKS>
+__device__ __forceinline__ float cw_top(uint32_t tS, const uint32_t (&vis)[4], const float* sk, int w0) {
   float top = -INFINITY;
 #pragma unroll 1
-  for (int w = 0; w < 4; ++w) {
+  for (int w = w0 >> 1; w < (w0 + CHUNKS) >> 1; ++w) {
     uint32_t a[32];
     tmem_ld_32x32b_x32(tS + w * 32, a);
     const uint32_t on = w == 0 ? vis[0] : w == 1 ? vis[1] : w == 2 ? vis[2] : vis[3];
@@ -153,10 +163,11 @@ __device__ __forceinline__ float cw_top(uint32_t tS, const uint32_t (&vis)[4], c
 
 // The reference at which a row's largest weight among the keys it sees lies near 2, unless exponentials would pass
 // 2^CW_SPAN: from the logit and the scale of each key.
-__device__ __forceinline__ float cw_exact(uint32_t tS, float c, const uint32_t (&vis)[4], const float* sk) {
+template <int CHUNKS>
+__device__ __forceinline__ float cw_exact(uint32_t tS, float c, const uint32_t (&vis)[4], const float* sk, int w0) {
   float top = -INFINITY, heavy = -INFINITY;
 #pragma unroll 1
-  for (int w = 0; w < 8; ++w) {
+  for (int w = w0; w < w0 + CHUNKS; ++w) {
     uint32_t a[16];
     tmem_ld_32x32b_x16(tS + w * 16, a);
     const uint32_t on = (w < 4 ? (w < 2 ? vis[0] : vis[1]) : (w < 6 ? vis[2] : vis[3])) >> (16 * (w & 1));
@@ -178,15 +189,16 @@ __device__ __forceinline__ float cw_exact(uint32_t tS, float c, const uint32_t (
 // One pass over a tile's logits: the weights of the row in fp16 into its line of the operand, the sum of the
 // exponentials, and the largest weight. A logit's product is not rounded before the reference is taken off, which was;
 // past CW_FAR that difference could leave float32's exponents, and FAR rounds both alike (everywhere it took 3 % longer).
-template <bool MASKED, bool FAR>
+// With REST the operand's second half holds what rounding the weights of the first left.
+template <bool MASKED, bool FAR, bool REST>
 __device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, const uint32_t (&vis)[4], const float* sk,
-                                        uint8_t* line, int sw, float* sum, float* most) {
+                                        uint8_t* line, int sw, int w0, float* sum, float* most) {
   const float* sv = sk + 128;
   const float2 c2 = make_float2(c, c), nref = make_float2(-ref, -ref);
   float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
   float big[2] = {0.0f, 0.0f};
 #pragma unroll 1
-  for (int w = 0; w < 8; ++w) {
+  for (int w = w0; w < w0 + (REST ? 4 : 8); ++w) {
     uint32_t a[16];
     tmem_ld_32x32b_x16(tS + w * 16, a);
     float4 fks[4], fvs[4];
@@ -197,11 +209,11 @@ __device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, const u
     }
     tmem_ld_wait_regs16(a);
     const uint32_t on = (w < 4 ? (w < 2 ? vis[0] : vis[1]) : (w < 6 ? vis[2] : vis[3])) >> (16 * (w & 1));
-    uint8_t* to = line + (w >= 4 ? CW_HALF : 0);
+    uint8_t* to = line + (!REST && w >= 4 ? CW_HALF : 0);
     const int c0 = 2 * (w & 3);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      uint32_t out[4];
+      uint32_t out[4], rest[4];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const float4 fk = fks[2 * i + q], fv = fvs[2 * i + q];
@@ -222,9 +234,16 @@ __device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, const u
           big[e] = fwht::fmax3f(big[e], x.x, x.y);
           const __half2 hx = __floats2half2_rn(x.x, x.y);
           out[2 * q + e] = *reinterpret_cast<const uint32_t*>(&hx);
+          if (REST) {
+            const float2 f = __half22float2(hx);
+            const __half2 hr = __floats2half2_rn(x.x - f.x, x.y - f.y);
+            rest[2 * q + e] = *reinterpret_cast<const uint32_t*>(&hr);
+          }
         }
       }
       *reinterpret_cast<uint4*>(to + (((c0 + i) ^ sw) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+      if (REST)
+        *reinterpret_cast<uint4*>(to + CW_HALF + (((c0 + i) ^ sw) << 4)) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
     }
   }
   const float2 all = __fadd2_rn(part[0], part[1]);
@@ -251,6 +270,11 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bar = [&](int pipe, int which) { return bars + pipe * kBars + which; };
 
+  // For an fp16 output, which keeps as many bits as a weight, a tile is taken in two steps of 64 keys, whose operand
+  // holds beside the weights what rounding them left.
+  constexpr int STEPS = F16 ? 2 : 1, CHUNKS = 8 / STEPS;
+  constexpr int kOLast = kODone + STEPS - 1;
+
   griddep_launch_dependents();
   if (tid == 0) {
     prefetch_tensormap(&tmK);
@@ -259,8 +283,10 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       mbar_init(bar(pipe, kKEmpty), 1);
       mbar_init(bar(pipe, kSFull), 1);
       mbar_init(bar(pipe, kSEmpty), 4);
-      mbar_init(bar(pipe, kPFull), 4);
-      mbar_init(bar(pipe, kODone), 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(bar(pipe, kPFull + h), 4);
+        mbar_init(bar(pipe, kODone + h), 1);
+      }
       mbar_init(bar(pipe, kVFull), 4);
       mbar_init(bar(pipe, kSc0), 4);
       mbar_init(bar(pipe, kSc1), 4);
@@ -390,73 +416,80 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
         const float* most = reinterpret_cast<const float*>(there + 4);
         ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kSc0 + (use & 1)), use >> 1) && wait(bar(pipe, kSFull), use));
         if (!ok) break;
-        // the pipeline's last P V has finished: O is stable and the operand's memory free
-        if (use > 0) {
-          ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kODone), use - 1));
-          if (!ok) break;
-        }
-        tc_fence_after();
         uint32_t vis[4] = {there[0], there[1], there[2], there[3]};
         const bool masked = key0 + CW_KT > clear || (vis[0] & vis[1] & vis[2] & vis[3]) != 0xFFFFFFFFu;
         if (masked) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) vis[w] &= below(lim - key0, w) | placed(bits, context - key0, w);
         }
-        const float high = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-        const bool first = !weighed && (vis[0] | vis[1] | vis[2] | vis[3]) != 0;
-        // the sum so far may be of keys without a value, and must stay in range where the reference comes down
-        const float least = l > 0.0f ? ref + exponent_of(l) - CW_SPAN : CA_NONE;
-        float now = ref, sum, big;
-        // A row whose weights have grown takes its reference up before they can pass fp16's range: one
-        // rescaling of O instead of a second pass.
-        if (largest > CW_GROWN) now += exponent_of(largest);
-        if (__any_sync(0xFFFFFFFFu, first)) {
-          // at this every weight of the tile is below 2^8, the largest usually little below
-          const float tm = c * cw_top(tS, vis, sk);
-          if (first) now = fmaxf(high > 0.0f ? tm + exponent_of(high) - 7.0f : tm, fmaxf(tm - CW_SPAN, least));
-          far = __any_sync(0xFFFFFFFFu, fabsf(now) > CW_FAR && now != CA_NONE);
-        }
 #pragma unroll 1
-        for (int attempt = 0;; ++attempt) {
-          __syncwarp();  // a pass is the whole warp's; what led here differs by row
-          if (far) cw_pass<true, true>(tS, c, now, vis, sk, line, sw, &sum, &big);
-          else if (masked) cw_pass<true, false>(tS, c, now, vis, sk, line, sw, &sum, &big);
-          else cw_pass<false, false>(tS, c, now, vis, sk, line, sw, &sum, &big);
-          const bool lost = !(big <= CW_MOST) || !(sum <= 0x1p110f) || (first && high > 0.0f && big < 1.0f);
-          if (attempt == 1 || !__any_sync(0xFFFFFFFFu, lost)) break;
-          const float at = cw_exact(tS, c, vis, sk);
-          if (lost) now = fmaxf(at, least);
-          far = __any_sync(0xFFFFFFFFu, fabsf(now) > CW_FAR && now != CA_NONE);
-        }
-        weighed |= big > 0.0f;
-        const float scale = now == ref ? 1.0f : ex2_approx(ref - now);
-        largest = fmaxf(largest * scale, big);
-        const float alpha = ref == CA_NONE ? (now == ref ? 1.0f : 0.0f) : scale;
-        ref = now;
-        l = l * alpha + sum;
-        // the logits have been read, the operand is in place, and O has the new reference
-        if (t >= r.t0 + 2 && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
-#pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(tO + ch * 32, o);
-            tmem_ld_wait_regs(o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st_32x32b_x32(tO + ch * 32, o);
+        for (int step = 0; step < STEPS; ++step) {
+          const int w0 = step * CHUNKS;
+          // the pipeline's last P V has finished: O is stable and the operand's memory free
+          if (step > 0 || use > 0) {
+            ok = __all_sync(0xFFFFFFFFu, step > 0 ? wait(bar(pipe, kODone), use) : wait(bar(pipe, kOLast), use - 1));
+            if (!ok) break;
           }
-          tmem_st_wait();
+          tc_fence_after();
+          const float high = STEPS == 1 ? fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]))
+                                        : fmaxf(most[2 * step], most[2 * step + 1]);
+          const uint32_t any = STEPS == 1 ? vis[0] | vis[1] | vis[2] | vis[3] : step == 0 ? vis[0] | vis[1] : vis[2] | vis[3];
+          const bool first = !weighed && any != 0;
+          // the sum so far may be of keys without a value, and must stay in range where the reference comes down
+          const float least = l > 0.0f ? ref + exponent_of(l) - CW_SPAN : CA_NONE;
+          float now = ref, sum, big;
+          // A row whose weights have grown takes its reference up before they can pass fp16's range: one
+          // rescaling of O instead of a second pass.
+          if (largest > CW_GROWN) now += exponent_of(largest);
+          if (__any_sync(0xFFFFFFFFu, first)) {
+            // at this every weight of the tile is below 2^8, the largest usually little below
+            const float tm = c * cw_top<CHUNKS>(tS, vis, sk, w0);
+            if (first) now = fmaxf(high > 0.0f ? tm + exponent_of(high) - 7.0f : tm, fmaxf(tm - CW_SPAN, least));
+            far = __any_sync(0xFFFFFFFFu, fabsf(now) > CW_FAR && now != CA_NONE);
+          }
+#pragma unroll 1
+          for (int attempt = 0;; ++attempt) {
+            __syncwarp();  // a pass is the whole warp's; what led here differs by row
+            if (far) cw_pass<true, true, F16>(tS, c, now, vis, sk, line, sw, w0, &sum, &big);
+            else if (masked) cw_pass<true, false, F16>(tS, c, now, vis, sk, line, sw, w0, &sum, &big);
+            else cw_pass<false, false, F16>(tS, c, now, vis, sk, line, sw, w0, &sum, &big);
+            const bool lost = !(big <= CW_MOST) || !(sum <= 0x1p110f) || (first && high > 0.0f && big < 1.0f);
+            if (attempt == 1 || !__any_sync(0xFFFFFFFFu, lost)) break;
+            const float at = cw_exact<CHUNKS>(tS, c, vis, sk, w0);
+            if (lost) now = fmaxf(at, least);
+            far = __any_sync(0xFFFFFFFFu, fabsf(now) > CW_FAR && now != CA_NONE);
+          }
+          weighed |= big > 0.0f;
+          const float scale = now == ref ? 1.0f : ex2_approx(ref - now);
+          largest = fmaxf(largest * scale, big);
+          const float alpha = ref == CA_NONE ? (now == ref ? 1.0f : 0.0f) : scale;
+          ref = now;
+          l = l * alpha + sum;
+          // the logits have been read, the operand is in place, and O has the new reference
+          if ((step > 0 || t >= r.t0 + 2) && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
+#pragma unroll 1
+            for (int ch = 0; ch < 4; ++ch) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(tO + ch * 32, o);
+              tmem_ld_wait_regs(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st_32x32b_x32(tO + ch * 32, o);
+            }
+            tmem_st_wait();
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (step == STEPS - 1) mbar_arrive(bar(pipe, kSEmpty));
+            mbar_arrive(bar(pipe, kPFull + step));
+          }
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(pipe, kSEmpty));
-          mbar_arrive(bar(pipe, kPFull));
-        }
+        if (!ok) break;
       }
       const int mine = r.t1 - r.t0 > pipe ? (r.t1 - r.t0 - pipe + 1) / 2 : 0;
-      if (ok && mine > 0) ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kODone), used[pipe] + mine - 1));
+      if (ok && mine > 0) ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kOLast), used[pipe] + mine - 1));
       stat[pipe * 128 + row] = make_float2(ref, l);
       tc_fence_before();
       const bool lost = cw_vote(1, 256, !ok);
@@ -637,7 +670,7 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           give_scales(n + 1, cell1, mk, mv);
           cell2 = n + 2 < tiles ? cell_of((r.t0 + n + 2) * CW_KT + me) : -1;
         }
-        if (use > 0 && !__all_sync(0xFFFFFFFFu, wait(bar(pipe, kODone), use - 1))) return false;
+        if (use > 0 && !__all_sync(0xFFFFFFFFu, wait(bar(pipe, kOLast), use - 1))) return false;
         uint8_t* to = smem + L::kOffV + pipe * 2 * CW_HALF + ((lane >> 2) & 1) * CW_HALF;  // channels from 64 on: second half
         const __half2 offset = __floats2half2_rn(1152.0f, 1152.0f);
 #pragma unroll
@@ -752,25 +785,33 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           };
           bool ok = logits(0);
           if (ok && tiles > 1) ok = logits(1);
-          for (int n = 0; n < tiles && ok; ++n) {
+          // a step of tile n: the pipeline's next S before the last P V of a tile: its softmax waits for it, and for this
+          // P V only after that
+          auto values = [&](int n, int step) {
             const int pipe = n & 1, use = used[pipe] + (n >> 1);
-            // the pipeline's next S first: its softmax waits for it, and for this P V only after that
-            if (n + 2 < tiles && !(wait(bar(pipe, kSEmpty), use) && logits(n + 2))) break;
-            if (!wait(bar(pipe, kPFull), use) || !wait(bar(pipe, kVFull), use)) break;
+            if (step == STEPS - 1 && n + 2 < tiles && !(wait(bar(pipe, kSEmpty), use) && logits(n + 2))) return false;
+            if (!wait(bar(pipe, kPFull + step), use) || (step == 0 && !wait(bar(pipe, kVFull), use))) return false;
             tc_fence_after();
             const uint32_t pa = smem_addr(smem + L::kOffP + pipe * 2 * CW_HALF);
             const uint32_t va = smem_addr(smem + L::kOffV + pipe * 2 * CW_HALF);
             // 16 keys an instruction: P's K-major rows advance 32 bytes inside a 64-key half; the values' atoms are
             // 8 keys x 64 channels (1 KB apart along the keys, the second 64 channels 16 KB on)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)  // halves of the keys, or a step's weights and their rest
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_bf16(tmem + 256 + pipe * 128, smem_desc_k_sw128(pa + h * CW_HALF + k * 32),
-                         smem_desc_mn_sw128(va + (4 * h + k) * 2048, CW_HALF, 1024), CW_IDESC_O,
-                         (n >= 2 || h > 0 || k > 0) ? 1u : 0u);
-            mma_commit(bar(pipe, kODone));
-          }
+                         smem_desc_mn_sw128(va + (4 * (STEPS == 1 ? h : step) + k) * 2048, CW_HALF, 1024), CW_IDESC_O,
+                         (n >= 2 || step > 0 || h > 0 || k > 0) ? 1u : 0u);
+            mma_commit(bar(pipe, kODone + step));
+            return true;
+          };
+          // both pipelines' first steps, then both their second ones, as their softmax takes turns
+          for (int n = 0; n < tiles && ok; n += 2)
+            for (int step = 0; step < STEPS && ok; ++step) {
+              ok = values(n, step);
+              if (ok && n + 1 < tiles) ok = values(n + 1, step);
+            }
         }
         used[0] += (r.t1 - r.t0 + 1) / 2;
         used[1] += (r.t1 - r.t0) / 2;
