@@ -247,3 +247,11 @@ def test_cache_slots_of_pages_past_the_cache():
     got = cache.slots(pages, torch.zeros(6, dtype=torch.int64), at)
     assert got.dtype == torch.int32
     assert got.tolist() == [4 * 64 + 5, 2**31 - 1, 2**31 - 1, 2**31 - 1, -1, 3 * 64 + 5]
+
+
+def test_workspace_of_each_tile_height(L):
+    """Parts of 640 pieces of 8 or 16 rows, of 160 pieces of 128."""
+    size = L.convrot_cache_attention_workspace_bytes
+    part = lambda pieces, rows: 2 * pieces * rows * 128 * 4  # noqa: E731
+    few, some, many = size(4, 4, 8, 2, 128), size(32, 4, 8, 2, 128), size(33, 4, 8, 2, 128)
+    assert part(640, 8) <= few < part(640, 16) <= some < part(160, 128) <= many < 2 * part(160, 128)

@@ -408,7 +408,7 @@ def test_two_graphs_share_a_workspace_and_follow_the_lengths(cr):
     graphs.clear()
 
 
-# ---- more than 72 rows a sequence and key head on average: tiles of 128 rows
+# ---- more than 32 rows a sequence and key head on average: tiles of 128 rows
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
@@ -790,12 +790,13 @@ def test_a_cache_learns_what_its_attention_met(cr, monkeypatch, native, hq):
         cr.convrot_cache_attention(s.Q, *cache.cells, pages, lengths, starts, status=own.float())
 
 
-def test_a_wait_that_runs_out_makes_rows_nan_and_is_reported(cr):
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+def test_a_wait_that_runs_out_makes_rows_nan_and_is_reported(cr, kind):
     """A limit of a nanosecond on the waits of the 128-row kernel, some of which take longer: each row is what it is
     with time, or NaN, and the status says so; the next call is as if nothing had been."""
     import torch
 
-    s = Setup(cr, [(20000, 1), (0, 1)] + [(300, 1)] * 198, 40, 1, 64, "bf16", seed=21)
+    s = Setup(cr, [(20000, 1), (0, 1)] + [(300, 1)] * 198, 40, 1, 64, kind, seed=21)
     cells, (pages, lengths, starts) = s.cells(), s.args()
     need = cr.convrot_cache_attention_workspace_bytes(200, 200, 40, 1)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
@@ -805,7 +806,7 @@ def test_a_wait_that_runs_out_makes_rows_nan_and_is_reported(cr):
     args = cr._lib.CACHE_ATTENTION_ARGS.pack(
         *(t.data_ptr() for t in cells), *cells[0].shape, s.Q.data_ptr(), O.data_ptr(), pages.data_ptr(),
         lengths.data_ptr(), starts.data_ptr(), 0, ws.data_ptr(), need, 200, 40, 200, pages.shape[1], pages.stride(0),
-        *s.Q.stride()[:2], *O.stride()[:2], SCALE, 0)
+        *s.Q.stride()[:2], *O.stride()[:2], SCALE, cr.DTYPE_F16 if kind == "f16" else cr.DTYPE_BF16)
     stream = torch.cuda.current_stream().cuda_stream
     assert cr.lib().convrot_cache_attention_ex(args, told.data_ptr(), 1, stream) == 0
     assert cr.convrot_read_device_status(ws) == 5 and told.item() == 5
@@ -914,3 +915,29 @@ def test_fp16_outputs_keep_the_weights_bits(cr, hq, hkv, keys, page):
             want, got = ref[0, h], o[b, h]
             assert np.all(np.abs(got - want) <= u * np.abs(want) + slack + OUT_ABS["f16"]), (b, h)
         assert some >= hq // 4
+
+
+@pytest.mark.parametrize("hq", [4, 12, 80])
+def test_strained_references_with_fp16_outputs(cr, hq):
+    """What strains the references above, where the weights' second product and, on tiles of 128 rows, the steps of 64
+    keys take part: value scales over many powers of ten in either order, keys without a value before others (also
+    whole steps of them), logits that rise by steps, a draft that no mask names and drafts that few see."""
+    for order in (1, -1):
+        s = Setup(cr, [(600, 1), (50, 1), (700, 1)], hq, 1, 16, "f16", seed=7)
+        for j in range(600):
+            s.scales[1][s.pages[0, j // 16], :, j % 16] = 10.0 ** (order * (j - 300) / 30.0 - 9.0)
+        for j in range(50):
+            s.scales[1][s.pages[1, j // 16], :, j % 16] = 0.0
+        for j in range(700):
+            if j < 520 and j // 64 % 3 != 1:
+                s.scales[1][s.pages[2, j // 16], :, j % 16] = 0.0
+            s.scales[0][s.pages[2, j // 16], :, j % 16] *= 1.0 + 0.5 * (j // 64)
+        o = s.check(s.run())
+        assert not o[1].any()
+    tree = np.array([1, 3, 1, 9, 17, 33], np.uint64)  # nothing sees draft 2
+    for keys in (64, 68, 130):  # the drafts before, across and behind the border of two steps
+        s = Setup(cr, [(keys, 6)], hq, 1, 16, "f16", seed=8, tree=tree)
+        j = keys - 6 + 2
+        s.scales[0][s.pages[0, j // 16], :, j % 16] = np.nan
+        s.scales[1][s.pages[0, j // 16], :, j % 16] = np.inf
+        s.check(s.run())
