@@ -941,3 +941,18 @@ def test_strained_references_with_fp16_outputs(cr, hq):
         s.scales[0][s.pages[0, j // 16], :, j % 16] = np.nan
         s.scales[1][s.pages[0, j // 16], :, j % 16] = np.inf
         s.check(s.run())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("hq", [4, 12, 80])
+def test_a_heavy_value_beside_sums_without_values(cr, kind, hq):
+    """Most of a row's sum lies in keys with next to no value, its mean in one key with a large one: the unit of a
+    row's weights differs by 2^120 and more between tiles, pipelines and pieces, and no sum is lost on the way."""
+    heavy, next_to_none = (1e15, 1e-28) if kind == "bf16" else (40.0, 1e-35)
+    for keys in (136, 300, 5000):
+        for at in (5, 100, 131, keys - 2):
+            s = Setup(cr, [(keys, 1)], hq, 1, 16, kind, seed=27)
+            s.scales[0][np.isfinite(s.scales[0])] = 0.002  # logits near one another
+            s.scales[1][np.isfinite(s.scales[1])] = next_to_none
+            s.scales[1][s.pages[0, at // 16], :, at % 16] = heavy
+            s.check(s.run())

@@ -731,13 +731,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_attention_join_wide_ker
       float most = top;
 #pragma unroll
       for (int i = 0; i < kWideAhead; ++i) most = fmaxf(most, st[i].x);
-      const float f = ex2_approx(top - most);
+      // a part's sum of exponentials reaches 2^110: its factor in two halves, where one is lost below 2^-126
+      const float h = ex2_approx(0.5f * (top - most)), f = h * h;
       top = most;
-      sum *= f, v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+      sum = sum * h * h;
+      v.x *= f, v.y *= f, v.z *= f, v.w *= f;
 #pragma unroll
       for (int i = 0; i < kWideAhead; ++i) {
-        const float w = ex2_approx(st[i].x - top);  // of no part: no sum, no values
-        sum = fmaf(w, st[i].y, sum);
+        const float half = ex2_approx(0.5f * (st[i].x - top)), w = half * half;  // of no part: no sum, no values
+        sum = fmaf(half * st[i].y, half, sum);
         v.x = fmaf(w, x[i].x, v.x), v.y = fmaf(w, x[i].y, v.y), v.z = fmaf(w, x[i].z, v.z), v.w = fmaf(w, x[i].w, v.w);
       }
     }

@@ -460,11 +460,12 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
             far = __any_sync(0xFFFFFFFFu, fabsf(now) > CW_FAR && now != CA_NONE);
           }
           weighed |= big > 0.0f;
-          const float scale = now == ref ? 1.0f : ex2_approx(ref - now);
+          // in two factors for the sum: one of up to 2^110 may count where a single factor is lost below 2^-126
+          const float half = now == ref ? 1.0f : ex2_approx(0.5f * (ref - now)), scale = half * half;
           largest = fmaxf(largest * scale, big);
           const float alpha = ref == CA_NONE ? (now == ref ? 1.0f : 0.0f) : scale;
           ref = now;
-          l = l * alpha + sum;
+          l = l * half * half + sum;
           // the logits have been read, the operand is in place, and O has the new reference
           if ((step > 0 || t >= r.t0 + 2) && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
 #pragma unroll 1
@@ -511,8 +512,9 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       const bool second = r.t1 - r.t0 > 1;
       const float2 s0 = stat[row], s1 = second ? stat[128 + row] : make_float2(CA_NONE, 0.0f);
       const float top = fmaxf(s0.x, s1.x);
-      const float f0 = ex2_approx(s0.x - top), f1 = ex2_approx(s1.x - top);
-      const float total = s0.y * f0 + s1.y * f1;
+      const float h0 = ex2_approx(0.5f * (s0.x - top)), h1 = ex2_approx(0.5f * (s1.x - top));  // halves, as above
+      const float f0 = h0 * h0, f1 = h1 * h1;
+      const float total = s0.y * h0 * h0 + s1.y * h1 * h1;
       const bool whole = r.t0 == 0 && r.t1 == walk.s.tiles;
       const uint32_t tO0 = tmem + lanes + 256, tO1 = tO0 + 128;
       if (!there) {
