@@ -956,3 +956,63 @@ def test_a_heavy_value_beside_sums_without_values(cr, kind, hq):
             s.scales[1][np.isfinite(s.scales[1])] = next_to_none
             s.scales[1][s.pages[0, at // 16], :, at % 16] = heavy
             s.check(s.run())
+
+
+@pytest.mark.parametrize("hq", [4, 12, 80])
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e9, 1e12, 1e30])
+def test_far_logits_pick_their_largest(cr, hq, size):
+    """Key scales so large, and so far apart, that one key holds a row's whole weight: its value is the row."""
+    s = Setup(cr, [(300, 1), (20, 2), (131, 1)], hq, 1, 16, "bf16", seed=28)
+    rng = np.random.default_rng(4)
+    held = np.isfinite(s.scales[0])
+    s.scales[0][held] = (size * 10.0 ** rng.uniform(-3, 1, held.sum())).astype(np.float32)
+    o = s.run().double().cpu().numpy()
+    assert np.all(np.isfinite(o))
+    u, sure = OUT_REL["bf16"], 0
+    for b, (n, news) in enumerate(s.seqs):
+        (kc, ks), (vc, vs) = s.dense(b, 0), s.dense(b, 1)
+        for i in range(news):
+            row = s.starts[b] + i
+            qc, sq = oracle.quantize_heads(s.q[row], 128)
+            seen = n - news + i + 1
+            logits = (qc.astype(np.float64) @ kc[0, :seen].T.astype(np.float64)) * ks[0, :seen] * sq[:, None] * SCALE
+            for h in range(hq):
+                order = np.argsort(logits[h])
+                first, second = logits[h, order[-1]], logits[h, order[-2]]
+                # what codes that round the other way move, and the float32 roundings of both logits
+                sway = 3 * float(sq[h]) * SCALE * 127 * float(ks[0, order[-2:]].max())
+                if first - second <= 2 * sway + 12 * 2.0**-24 * abs(first) + 60:
+                    continue
+                sure += 1
+                at = order[-1]
+                want = oracle.cache_value(vc[0, at], vs[0, at])
+                off = np.linalg.norm(vc[0, at] * float(vs[0, at])) * (2.0**-11 + 2.0**-18)
+                assert np.all(np.abs(o[row, h] - want) <= u * np.abs(want) + off), (b, i, h)
+    assert sure >= 2
+
+
+@pytest.mark.parametrize("hq", [4, 12, 80])
+def test_far_logits_with_values_of_any_size(cr, hq):
+    """Equal keys with logits of any magnitude, values over 40 powers of ten, in any order: every weight is 1 / n."""
+    rng = np.random.default_rng(6)
+    for size in (1e6, 1e8, 1e9, 1e12, 1e25):
+        for order in ("rising", "falling", "any", "zeros first"):
+            keys = [300, 140, 40]
+            s = Setup(cr, [(n, 1) for n in keys], hq, 1, 16, seed=29)
+            for b, n in enumerate(keys):
+                at = s.pages[b, :-(-n // 16)]
+                s.codes[0][at] = s.codes[0][s.pages[b, 0], :, :1]
+                s.scales[0][at] = np.float32(size)
+                power = rng.uniform(-20, 20, n)
+                power = {"rising": np.sort(power), "falling": -np.sort(-power)}.get(order, power)
+                for j in range(n):
+                    s.scales[1][s.pages[b, j // 16], :, j % 16] = 0.0 if order == "zeros first" and j < n - 9 \
+                        else 10.0 ** power[j]
+            o = s.run().double().cpu().numpy()
+            assert np.all(np.isfinite(o))
+            for b, n in enumerate(keys):
+                _, (vc, vs) = s.dense(b, 0), s.dense(b, 1)
+                want = oracle.cache_value(vc[0], vs[0]).mean(0)
+                size_ = (vs[0][:, None].astype(np.float64) * np.abs(vc[0].astype(np.float64))).sum(0) / n
+                slack = (2.0**-11 + (n / 16 + 64) * 2.0**-22) * np.linalg.norm(size_) * (1 + OUT_REL["bf16"])
+                assert np.all(np.abs(o[b] - want) <= OUT_REL["bf16"] * np.abs(want) + slack + OUT_ABS["bf16"]), (size, order, b)

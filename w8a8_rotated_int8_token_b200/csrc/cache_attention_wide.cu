@@ -140,6 +140,11 @@ __device__ __forceinline__ float2 cw_logits(uint32_t a, uint32_t b, float2 scale
   return __fmul2_rn(__fadd2_rn(x, make_float2(-12582912.0f, -12582912.0f)), scale);
 }
 
+// Exponent of a positive float: 2^e <= x < 2^(e + 1).
+__device__ __forceinline__ float exponent_of(float x) {
+  return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127);
+}
+
 // The row's functions below work on one step of a tile: CHUNKS times 16 keys, from 16 w0 on.
 
 // The largest logit of a row among the keys it sees, without the row's factor.
@@ -162,9 +167,11 @@ __device__ __forceinline__ float cw_top(uint32_t tS, const uint32_t (&vis)[4], c
 }
 
 // The reference at which a row's largest weight among the keys it sees lies near 2, unless exponentials would pass
-// 2^CW_SPAN: from the logit and the scale of each key.
+// 2^CW_SPAN: from the logit and the scale of each key. Past CW_FAR, where a logit has no bits left for the scale's
+// exponent beside it, the largest logit, and apart from it in `lift` what the reference should lie above it.
 template <int CHUNKS>
-__device__ __forceinline__ float cw_exact(uint32_t tS, float c, const uint32_t (&vis)[4], const float* sk, int w0) {
+__device__ __forceinline__ float cw_exact(uint32_t tS, float c, const uint32_t (&vis)[4], const float* sk, int w0,
+                                          float* lift) {
   float top = -INFINITY, heavy = -INFINITY;
 #pragma unroll 1
   for (int w = w0; w < w0 + CHUNKS; ++w) {
@@ -183,16 +190,39 @@ __device__ __forceinline__ float cw_exact(uint32_t tS, float c, const uint32_t (
                            y + __uint_as_float(0x4B000000u | (__float_as_uint(v.y) >> 23 & 255u)));
     }
   }
-  return fmaxf(heavy - (8388608.0f + 127.0f + 1.0f), top - CW_SPAN);
+  const float at = fmaxf(heavy - (8388608.0f + 127.0f + 1.0f), top - CW_SPAN);
+  const bool far = fabsf(top) > CW_FAR && top > -INFINITY;
+  *lift = 0.0f;
+  if (__any_sync(0xFFFFFFFFu, far)) {
+    heavy = -INFINITY;
+#pragma unroll 1
+    for (int w = w0; w < w0 + CHUNKS; ++w) {
+      uint32_t a[16];
+      tmem_ld_32x32b_x16(tS + w * 16, a);
+      const uint32_t on = (w < 4 ? (w < 2 ? vis[0] : vis[1]) : (w < 6 ? vis[2] : vis[3])) >> (16 * (w & 1));
+      tmem_ld_wait_regs16(a);
+#pragma unroll
+      for (int k = 0; k < 16; k += 2) {
+        const float2 u = cw_logits(a[k], a[k + 1], *reinterpret_cast<const float2*>(sk + w * 16 + k));
+        const float2 v = *reinterpret_cast<const float2*>(sk + 128 + w * 16 + k);
+        const float x = __fadd_rn(__fmul_rn(c, u.x), -top) + exponent_of(v.x);
+        const float y = __fadd_rn(__fmul_rn(c, u.y), -top) + exponent_of(v.y);
+        heavy = fwht::fmax3f(heavy, on >> k & 1u ? x : -INFINITY, on >> (k + 1) & 1u ? y : -INFINITY);
+      }
+    }
+    if (far) *lift = fmaxf(heavy - 1.0f, -CW_SPAN);
+  }
+  return far ? top : at;
 }
 
 // One pass over a tile's logits: the weights of the row in fp16 into its line of the operand, the sum of the
 // exponentials, and the largest weight. A logit's product is not rounded before the reference is taken off, which was;
-// past CW_FAR that difference could leave float32's exponents, and FAR rounds both alike (everywhere it took 3 % longer).
+// past CW_FAR that difference could leave float32's exponents, and FAR rounds both alike (everywhere it took 3 % longer),
+// and takes off the lift, which is 0 for other rows.
 // With REST the operand's second half holds what rounding the weights of the first left.
 template <bool MASKED, bool FAR, bool REST>
-__device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, const uint32_t (&vis)[4], const float* sk,
-                                        uint8_t* line, int sw, int w0, float* sum, float* most) {
+__device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, float lift, const uint32_t (&vis)[4],
+                                        const float* sk, uint8_t* line, int sw, int w0, float* sum, float* most) {
   const float* sv = sk + 128;
   const float2 c2 = make_float2(c, c), nref = make_float2(-ref, -ref);
   float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
@@ -221,7 +251,8 @@ __device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, const u
         for (int e = 0; e < 2; ++e) {
           const int k = i * 8 + 4 * q + 2 * e;
           const float2 u = cw_logits(a[k], a[k + 1], e == 0 ? make_float2(fk.x, fk.y) : make_float2(fk.z, fk.w));
-          const float2 t = FAR ? make_float2(__fadd_rn(__fmul_rn(c, u.x), -ref), __fadd_rn(__fmul_rn(c, u.y), -ref))
+          const float2 t = FAR ? make_float2(__fadd_rn(__fmul_rn(c, u.x), -ref) - lift,
+                                             __fadd_rn(__fmul_rn(c, u.y), -ref) - lift)
                                : __ffma2_rn(c2, u, nref);
           float2 pr = make_float2(ex2_approx(t.x), ex2_approx(t.y));
           float2 x = __fmul2_rn(pr, e == 0 ? make_float2(fv.x, fv.y) : make_float2(fv.z, fv.w));
@@ -251,9 +282,18 @@ __device__ __forceinline__ void cw_pass(uint32_t tS, float c, float ref, const u
   *most = fmaxf(big[0], big[1]);
 }
 
-// Exponent of a positive float: 2^e <= x < 2^(e + 1).
-__device__ __forceinline__ float exponent_of(float x) {
-  return static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127);
+// A row's sums of values in TMEM by a factor.
+__device__ __forceinline__ void cw_scale(uint32_t tO, float by) {
+#pragma unroll 1
+  for (int ch = 0; ch < 4; ++ch) {
+    uint32_t o[32];
+    tmem_ld_32x32b_x32(tO + ch * 32, o);
+    tmem_ld_wait_regs(o);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+    tmem_st_32x32b_x32(tO + ch * 32, o);
+  }
+  tmem_st_wait();
 }
 
 template <bool F16>
@@ -405,7 +445,10 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       const int clear = p.tree != nullptr ? context : context + 1;  // keys below it are seen by every row
       float ref = CA_NONE, l = 0.0f, largest = 0.0f;
       bool weighed = false;  // the row has had a weight
-      bool far = false;      // a row of the warp has a reference past CW_FAR
+      // A row of the warp has a reference past CW_FAR, which is then the sum of ref and lift (0 in other rows). That
+      // costs bf16 trees of 8 sequences 45.4 us of device time for 43.7, by registers.
+      bool far = false;
+      float lift = 0.0f;
       bool ok = true;
       int use = used[pipe];
       for (int t = r.t0 + pipe; t < r.t1; t += 2, ++use) {
@@ -436,48 +479,50 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
           const uint32_t any = STEPS == 1 ? vis[0] | vis[1] | vis[2] | vis[3] : step == 0 ? vis[0] | vis[1] : vis[2] | vis[3];
           const bool first = !weighed && any != 0;
           // the sum so far may be of keys without a value, and must stay in range where the reference comes down
-          const float least = l > 0.0f ? ref + exponent_of(l) - CW_SPAN : CA_NONE;
-          float now = ref, sum, big;
+          const float least = !(l > 0.0f) ? CA_NONE : fabsf(ref) > CW_FAR ? ref : ref + exponent_of(l) - CW_SPAN;
+          float now = ref, now_lift = lift, sum, big;
           // A row whose weights have grown takes its reference up before they can pass fp16's range: one
           // rescaling of O instead of a second pass.
-          if (largest > CW_GROWN) now += exponent_of(largest);
+          if (largest > CW_GROWN) (far && fabsf(ref) > CW_FAR ? now_lift : now) += exponent_of(largest);
           if (__any_sync(0xFFFFFFFFu, first)) {
             // at this every weight of the tile is below 2^8, the largest usually little below
             const float tm = c * cw_top<CHUNKS>(tS, vis, sk, w0);
-            if (first) now = fmaxf(high > 0.0f ? tm + exponent_of(high) - 7.0f : tm, fmaxf(tm - CW_SPAN, least));
+            if (first) {
+              now = fabsf(tm) > CW_FAR ? fmaxf(tm, least)
+                                       : fmaxf(high > 0.0f ? tm + exponent_of(high) - 7.0f : tm, fmaxf(tm - CW_SPAN, least));
+              if (!(fabsf(now) > CW_FAR)) now_lift = 0.0f;
+            }
             far = __any_sync(0xFFFFFFFFu, fabsf(now) > CW_FAR && now != CA_NONE);
           }
 #pragma unroll 1
           for (int attempt = 0;; ++attempt) {
             __syncwarp();  // a pass is the whole warp's; what led here differs by row
-            if (far) cw_pass<true, true, F16>(tS, c, now, vis, sk, line, sw, w0, &sum, &big);
-            else if (masked) cw_pass<true, false, F16>(tS, c, now, vis, sk, line, sw, w0, &sum, &big);
-            else cw_pass<false, false, F16>(tS, c, now, vis, sk, line, sw, w0, &sum, &big);
+            if (far) cw_pass<true, true, F16>(tS, c, now, now_lift, vis, sk, line, sw, w0, &sum, &big);
+            else if (masked) cw_pass<true, false, F16>(tS, c, now, 0.0f, vis, sk, line, sw, w0, &sum, &big);
+            else cw_pass<false, false, F16>(tS, c, now, 0.0f, vis, sk, line, sw, w0, &sum, &big);
             const bool lost = !(big <= CW_MOST) || !(sum <= 0x1p110f) || (first && high > 0.0f && big < 1.0f);
             if (attempt == 1 || !__any_sync(0xFFFFFFFFu, lost)) break;
-            const float at = cw_exact<CHUNKS>(tS, c, vis, sk, w0);
-            if (lost) now = fmaxf(at, least);
+            float up;
+            const float at = cw_exact<CHUNKS>(tS, c, vis, sk, w0, &up);
+            if (lost) {
+              now = fmaxf(at, least);
+              now_lift = 0.0f;
+              if (fabsf(now) > CW_FAR && now != CA_NONE)  // the sum so far must stay in range here as well
+                now_lift = fmaxf(up + (at - now), l > 0.0f ? ref - now + lift + exponent_of(l) - CW_SPAN : -CW_SPAN);
+            }
             far = __any_sync(0xFFFFFFFFu, fabsf(now) > CW_FAR && now != CA_NONE);
           }
           weighed |= big > 0.0f;
           // in two factors for the sum: one of up to 2^110 may count where a single factor is lost below 2^-126
-          const float half = now == ref ? 1.0f : ex2_approx(0.5f * (ref - now)), scale = half * half;
+          const float half = ex2_approx(0.5f * (ref - now + (lift - now_lift))), scale = half * half;
           largest = fmaxf(largest * scale, big);
           const float alpha = ref == CA_NONE ? (now == ref ? 1.0f : 0.0f) : scale;
           ref = now;
+          lift = now_lift;
           l = l * half * half + sum;
           // the logits have been read, the operand is in place, and O has the new reference
           if ((step > 0 || t >= r.t0 + 2) && __any_sync(0xFFFFFFFFu, alpha != 1.0f)) {
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(tO + ch * 32, o);
-              tmem_ld_wait_regs(o);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st_32x32b_x32(tO + ch * 32, o);
-            }
-            tmem_st_wait();
+            cw_scale(tO, alpha);
           }
           fence_proxy_async_smem();
           tc_fence_before();
@@ -491,6 +536,13 @@ __global__ void __launch_bounds__(CW_THREADS, 1)
       }
       const int mine = r.t1 - r.t0 > pipe ? (r.t1 - r.t0 - pipe + 1) / 2 : 0;
       if (ok && mine > 0) ok = __all_sync(0xFFFFFFFFu, wait(bar(pipe, kOLast), used[pipe] + mine - 1));
+      if (ok && far) {
+        // the join knows one number for a reference: back to the logit's
+        tc_fence_after();
+        const float half = ex2_approx(0.5f * lift);
+        cw_scale(tO, half * half);
+        l = l * half * half;
+      }
       stat[pipe * 128 + row] = make_float2(ref, l);
       tc_fence_before();
       const bool lost = cw_vote(1, 256, !ok);
