@@ -39,6 +39,7 @@
 //         the first rounding left.
 // The reference maximum and that factor move only when a key passes them by far;
 // a vote of the warp is all it costs otherwise.
+// Times here and below are of the device, for captured calls with bf16 outputs.
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -777,7 +778,8 @@ CaLayout ca_layout(int rows) {
 // fewer tiles, a lower one wastes fewer of its rows. 16 rows against 128, 8 sequences and 8 key heads: behind 4096 keys
 // 32 rows each 38 against 46 us, 40 rows 50 against 46, 64 rows 63 against 47, 128 rows 112 against 50; behind 512 keys
 // 32 rows 19 against 23, 40 rows 22 against 23, 56 rows 25 against 23; behind 16384 32 rows 106 against 136, 40 rows
-// 149 against 136; 4 to 96 rows (mean 48) behind 4096 keys 57 against 47.
+// 149 against 136; 4 to 96 rows (mean 48) behind 4096 keys 57 against 47. (bf16 outputs; for fp16 ones the 128 rows take
+// about a fifth longer.)
 int ca_rows(int64_t T, int64_t B, int64_t G) { return T * G <= 8 * B ? 8 : T * G <= 32 * B ? 16 : CA_WIDE_ROWS; }
 
 bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {

@@ -4,6 +4,7 @@
 //
 // Here a key is read for 128 rows, so the softmax bounds it, as in the dense INT8
 // attention: one exponential per row and key and five or six instructions beside it.
+// (Times are of the device, for captured calls, unless they say otherwise.)
 // One CTA per SM, two pipelines in it that take turns over the key tiles, so that
 // one's softmax runs while the other's products do; each has its own sums (O in
 // TMEM, reference and row sum in registers), joined at the end of a run:
@@ -31,14 +32,16 @@
 // Rounding a weight to fp16 is far below bf16's own rounding of the output. For an fp16 output it
 // is as large (2.9e-4 of a row against 2.1e-4 without it), so there a second product adds what the first rounding
 // left, as in the kernel for few rows. Both operands of a whole tile do not fit beside the rest of the shared
-// memory: the tile is taken in two steps of 64 keys, which costs the tree of 64 drafts behind 32768 keys 62 us
-// a call for 51.
+// memory: the tile is taken in two steps of 64 keys, which costs the tree of 64 drafts behind 32768 keys 60 us
+// for 49.
 // A run costs about as much as three tiles beside its tiles. Its first two tiles' keys
 // are fetched before its queries are in place, their pages looked up by eight lanes at
 // once, and the parts it leaves for the join lie four channels of all rows after one
 // another, so that both sides move whole lines: 54.3 to 43.9 us for the trees of 8
 // sequences (42.5 since the warps keep the registers they are launched with: handing
-// some of the others' to the softmax warps gained nothing and cost spills).
+// some of the others' to the softmax warps gained nothing. 14 warps are allocated as 16, so
+// that a thread has 128 registers and spills 200 to 220 bytes, most of them once a run or tile).
+// What holds every wait, reference and sum right, wherever they lie, took it from there to 45.4.
 // What bounds a tile now (2 us per SM): the latencies of a pass, 1024 cycles of
 // which are the exponentials, and between passes the turn of the products, which need the
 // logits read before the next are made.

@@ -14,9 +14,9 @@
 // tokens; hp x (D/16) threads share a token, and a thread keeps the same eight
 // pairs for every head it visits, so their sines and cosines are read from
 // shared memory once. The first four heads' loads are issued before the angles
-// are computed. Six CTAs of 128 threads per SM (80 registers): 43.9 us for 16896
-// tokens of 32 heads, 98 % of the copy bandwidth; CTAs of 256 threads took 46.2 to
-// 53.8 us, two heads ahead 49.5.
+// are computed. Six CTAs of 128 threads per SM (80 registers): 43.9 us of device time
+// for 16896 tokens of 32 heads (a call alone 47), 98 % of the copy bandwidth; CTAs of 256
+// threads took 46.2 to 53.8 us, two heads ahead 49.5.
 
 #include <cuda_runtime.h>
 
@@ -33,6 +33,7 @@ namespace {
 constexpr int kRopeThreads = 128;
 constexpr int kRopeAhead = 4;        // heads whose loads a thread has in flight
 constexpr int kRopeMaxDim = 512;
+constexpr int kRopeSms = 148;         // of a B200
 constexpr int kRopeTableMax = 2048;   // sine/cosine pairs a CTA holds (16 KB)
 constexpr float kRopeLeft = 2.0f;     // for a cosine: the pair is not turned
 
@@ -157,7 +158,8 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(const RopeParams 
   uint32_t left = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) left |= cs[i].x == kRopeLeft ? 1u << i : 0u;
-  // in a loop of its own, so that the usual one has no register more: 50.1 against 48.0 us a call for 16896 tokens
+  // in a loop of its own, so that the usual one has no register more: together 50.1 against 47.1 us a call for 16896
+  // tokens
   auto visit = [&](auto keeps_pairs) {
     constexpr bool keeps = decltype(keeps_pairs)::value;
     for (int hb = h0; hb < p.H; hb += kRopeAhead * p.hp) {
@@ -281,7 +283,8 @@ convrot_status convrot_rope(const convrot_rope_args* args, convrot_stream_t stre
   if (p.hp > most) p.hp = most;
   p.tok = kRopeThreads / (p.hp * per_head);
   if (p.R > 0 && p.tok > kRopeTableMax / (p.R / 2)) p.tok = kRopeTableMax / (p.R / 2);
-  if (few && p.tok > (p.tokens + 147) / 148) p.tok = static_cast<int>((p.tokens + 147) / 148);
+  const int64_t spread = (p.tokens + kRopeSms - 1) / kRopeSms;  // a CTA on every SM
+  if (few && p.tok > spread) p.tok = static_cast<int>(spread);
   const unsigned grid = static_cast<unsigned>((p.tokens + p.tok - 1) / p.tok);
   if (p.interleaved)
     (f16 ? rope_kernel<true, true> : rope_kernel<false, true>)<<<grid, kRopeThreads, 0, s>>>(p);
