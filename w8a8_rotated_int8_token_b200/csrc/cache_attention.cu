@@ -775,11 +775,11 @@ CaLayout ca_layout(int rows) {
 }
 
 // The tile of rows by the mean number of rows a sequence has for a key head. A taller tile reads the keys for
-// fewer tiles, a lower one wastes fewer of its rows. 16 rows against 128, 8 sequences and 8 key heads: behind 4096 keys
-// 32 rows each 38 against 46 us, 40 rows 50 against 46, 64 rows 63 against 47, 128 rows 112 against 50; behind 512 keys
-// 32 rows 19 against 23, 40 rows 22 against 23, 56 rows 25 against 23; behind 16384 32 rows 106 against 136, 40 rows
-// 149 against 136; 4 to 96 rows (mean 48) behind 4096 keys 57 against 47. (bf16 outputs; for fp16 ones the 128 rows take
-// about a fifth longer.)
+// fewer tiles, a lower one wastes fewer of its rows. Tiles of 16 rows against 128, 8 sequences and 8 key heads, bf16
+// outputs: behind 4096 keys 36 rows each 50 against 49 us, 48 rows 50 against 51, 64 rows 63 against 51, 96 rows 86
+// against 56; behind 512 keys 36 rows 22 against 25, 64 rows 26 against 27, 96 rows 32 against 28; behind 16384 36 rows
+// 149 against 141, 64 rows 202 against 144. fp16 outputs: behind 4096 36 rows 55 against 60, 64 rows 69 against 62; behind
+// 16384 36 rows 176 against 169, 64 rows 240 against 173.
 int ca_rows(int64_t T, int64_t B, int64_t G) { return T * G <= 8 * B ? 8 : T * G <= 32 * B ? 16 : CA_WIDE_ROWS; }
 
 bool ca_sizes_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
