@@ -519,9 +519,10 @@ CONVROT_API convrot_status convrot_cache_read(const convrot_cache_args* args, co
  *             within [0, T] (they are clamped).
  * Keys are read once per tile of 8, 16 or 128 query rows (n * Hq / Hkv rows per
  * key head; the tile follows from T, B and the heads), so this is the form for
- * single tokens, drafts and chunks; long prompts belong to
- * convrot_attention_int8. Two kernels (B = 0: a 4-byte memset of the status word); how the work is cut follows from the
- * lengths, and the result does not depend on timing. A timed-out wait (the tile
+ * single tokens, drafts and chunks. convrot_attention_int8 is for long prompts
+ * without a causal mask, in bf16, with a key head for each query head. Two kernels (B = 0: a 4-byte memset of the status
+ * word); how the work is cut follows from the lengths, and the result does not
+ * depend on timing. A timed-out wait (the tile
  * of 128 rows waits on its own copies and products) sets the status word to
  * CONVROT_ERR_DEVICE_TIMEOUT, and every row it cost is NaN.
  */

@@ -342,6 +342,9 @@ def test_autograd_learns_of_writes_and_is_told_what_cannot_be(cr, monkeypatch, n
     x = X.clone().requires_grad_()
     with pytest.raises(RuntimeError, match="leaf"):
         cr.convrot_rope(x, pos, freq, axis, Y=x)
+    with pytest.raises(RuntimeError, match="leaf"):
+        part = x[:, 1:]
+        cr.convrot_rope(part, pos[..., 1:], freq, axis, Y=part)
     assert torch.equal(x.detach(), X)
     for given in (dict(positions=pos.float().requires_grad_()), dict(freq=freq.clone().requires_grad_())):
         with pytest.raises(ValueError, match="detach"):

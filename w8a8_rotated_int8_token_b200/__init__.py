@@ -625,8 +625,8 @@ def _recorded_rope(X, positions, freq, axis, interleaved, inverse, Y):
     """convrot_rope where autograd follows X, or a Y that it has followed so far."""
     if positions.requires_grad or freq.requires_grad:
         raise ValueError("positions and freq take no gradient: detach them")
-    if Y is not None and Y.requires_grad and Y.is_leaf:
-        raise RuntimeError("Y is a leaf that requires grad: it cannot be written to in place")
+    if Y is not None and Y.requires_grad and (Y.is_leaf or (Y._is_view() and Y._base.is_leaf)):
+        raise RuntimeError("Y is a leaf that requires grad, or a view of one: it cannot be written to in place")
     return _rope_function().apply(Y, None if Y is X else X, positions, freq, axis, interleaved, inverse)
 
 
@@ -645,8 +645,8 @@ def _cells(index, k_codes, v_codes, k_scale, v_scale):
 def convrot_cache_append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status=None, stream=None):
     """Write keys and values K, V [T, H, 128] (bf16 or fp16, strided tokens and heads) into the
     rotated int8 cache: token t to slot slots[t] (int32; page * page size + place; negative: skipped;
-    the others must differ). Head vectors here and below start on 16 bytes, their strides are multiples of 8. Cache: codes int8 [pages, H, page size, 128], scales float32 [pages, H,
-    page size]. status: an int32 [1] tensor that a slot past the cache sets to 1, or None."""
+    the others must differ). Cache: codes int8 [pages, H, page size, 128], scales float32 [pages, H,
+    page size]. Head vectors here and below start on 16 bytes, their strides are multiples of 8. status: an int32 [1] tensor that a slot past the cache sets to 1, or None."""
     if stream is None and _T.append(K, V, slots, k_codes, v_codes, k_scale, v_scale, status):
         return
     code, index, shape, ks = _head_vectors(K, "K")
